@@ -426,12 +426,201 @@ qspec_status qspec_select_tokens(const uint16_t* logits, int32_t R, int32_t V, c
 qspec_status qspec_copy(void* dst, const void* src, size_t bytes, qspec_stream_t stream);
 
 /*
+ * ---------------------------------------------------------------------------------------------------
+ * Around the linears: rotary positions, a paged 8-bit key/value cache, attention over it, and the
+ * adjustment of the logits that a verify call reads.  The pages have no counterpart of these; they are
+ * what a decoder layer and a serving loop put between the two linear modes and the verify step: in
+ * one iteration every sequence adds gamma + 1 positions (or the nodes of a tree) to its cache, attends
+ * over it at each of them, and shortens it again to what was accepted.
+ */
+
+/*
+ * qspec_rotary_turns -- the frequencies of a rotary embedding, for qspec_rotary and qspec_kv_append.
+ * A HOST function: writes rot/2 words and one float to host memory; the caller copies the words to the
+ * device.  Word i is the rotation of pair i per position as a 64-bit fraction of a full turn, so
+ * position * word modulo 2^64 is the angle with no error from range reduction, at any position.
+ *     w_i = base^(-2 i / rot) radians per position, scaled for long contexts:
+ *     QSPEC_ROTARY_PLAIN   w_i
+ *     QSPEC_ROTARY_LINEAR  w_i / factor
+ *     QSPEC_ROTARY_BASE    base replaced by base * factor^(rot / (rot - 2))
+ *     QSPEC_ROTARY_BANDS   t_i = original w_i / (2 pi) turns over the trained context:
+ *                          w_i / factor below `low` turns, w_i above `high`, linear in t_i between
+ *     QSPEC_ROTARY_YARN    pairs that turn more than `high` times over the trained context keep w_i, those
+ *                          that turn less than `low` times take w_i / factor, with a linear ramp over
+ *                          the pair index between (edges rounded outwards to whole indices);
+ *                          *mult = 0.1 ln(factor) + 1
+ *   rot even, 2 <= rot <= 1024 (rot >= 4 for QSPEC_ROTARY_BASE); base > 1; factor >= 1; original > 0;
+ *   0 < low < high (BANDS and YARN; ignored otherwise)
+ *   turns [rot/2] uint64 HOST (output);  mult HOST (output): factor on the rotated values, 1 unless YARN
+ */
+#define QSPEC_ROTARY_PLAIN 0
+#define QSPEC_ROTARY_LINEAR 1
+#define QSPEC_ROTARY_BASE 2
+#define QSPEC_ROTARY_BANDS 3
+#define QSPEC_ROTARY_YARN 4
+qspec_status qspec_rotary_turns(int32_t rot, double base, int32_t scaling, double factor, double original,
+                                double low, double high, uint64_t* turns, float* mult);
+
+/* A rotary embedding on the device. */
+typedef struct {
+  const uint64_t* turns;  /* [rot/2] DEVICE, from qspec_rotary_turns                              */
+  int32_t rot;            /* leading values of each head that rotate, even                        */
+  int32_t interleaved;    /* 0: pairs (i, i + rot/2); 1: pairs (2i, 2i + 1)                       */
+  float mult;             /* factor on the rotated values                                         */
+  int32_t reserved;       /* must be 0                                                            */
+} qspec_rotary_plan;
+
+/*
+ * qspec_rotary -- rotary positions: for every token, head and pair (a, b) with angle t = pos * w_i,
+ *     (a, b) -> mult * (a cos t - b sin t, a sin t + b cos t);   values from rot on are copied.
+ * With `inverse` the angle is negated (mult stays): the transpose of the forward rotation, which is its
+ * backward pass.  Computed in fp32, rounded to bf16 once.
+ *
+ *   x    bf16, value d of head h of token t at x[t * x_token + h * x_head + d]
+ *   pos  [T] int32 device, 4-byte aligned; any value, negative ones included
+ *   out  as x with its own strides; out may be x itself with the same strides, else no overlap
+ *   dim a multiple of 8, 8 <= dim <= 1024, rot <= dim; 1 <= heads <= 65535; strides non-negative multiples
+ *   of 8 (QSPEC_ERR_MISALIGNED otherwise); T <= 2^31 - 1, every offset below 2^40
+ */
+qspec_status qspec_rotary(const uint16_t* x, int64_t x_token, int64_t x_head, const int32_t* pos, int64_t T,
+                          int32_t heads, int32_t dim, const qspec_rotary_plan* plan, int32_t inverse,
+                          uint16_t* out, int64_t out_token, int64_t out_head, qspec_stream_t stream);
+
+/*
+ * A paged key/value cache of 8-bit codes.  A page holds `page` consecutive tokens of one sequence; keys
+ * and values of each (page, head) share one power-of-two scale each: value = e4m3(code) * 2^exp.
+ *     k, v          [n_pages, heads, page, dim] uint8, e4m3 codes (finite ones: 0x7F and 0xFF do not occur)
+ *     k_exp, v_exp  [n_pages, heads] int8, -40 .. 40 (QSPEC_KV_MIN_EXP .. QSPEC_KV_MAX_EXP)
+ * page is 16, 32, 64 or 128; dim is 64 or 128.  Contents need no initialisation.
+ */
+#define QSPEC_KV_MIN_EXP (-40)
+#define QSPEC_KV_MAX_EXP 40
+#define QSPEC_KV_MAX_B 1024
+typedef struct {
+  uint8_t* k;
+  uint8_t* v;
+  int8_t* k_exp;
+  int8_t* v_exp;
+  int64_t n_pages;
+  int32_t heads, page, dim;
+  int32_t reserved;  /* must be 0 */
+} qspec_kv_cache;
+
+/*
+ * The sequences of one step.  Sequence b owns the tokens cu_tok[b] .. cu_tok[b+1] - 1 of the step's T
+ * new ones; they are the last ones of its kv_len[b] cached positions, in order.  Its cache position p lies
+ * in page pages[b, p / page], slot p mod page.
+ *     cu_tok  [B+1] int32, from 0 non-decreasing to at most T;  kv_len [B] int32;  pages [B, max_pages] int32
+ * (all three DEVICE, 4-byte aligned; only the entries of pages that kv_len reaches are read).
+ * max_tok: at least the largest number of new tokens of one sequence.  1 <= B <= QSPEC_KV_MAX_B,
+ * 1 <= T < 2^31, 1 <= max_tok <= T, max_pages * page < 2^31.
+ * A sequence whose numbers are out of range, and a page id outside [0, n_pages), touch no memory outside
+ * the arrays: the call leaves the sequence out (a bad page: its tokens), and the next
+ * qspec_check_status returns QSPEC_ERR_INVALID_ARG.
+ */
+typedef struct {
+  const int32_t* cu_tok;
+  const int32_t* kv_len;
+  const int32_t* pages;
+  int32_t B, max_pages, max_tok;
+  int32_t reserved;  /* must be 0 */
+  int64_t T;
+} qspec_kv_batch;
+
+/*
+ * qspec_kv_append -- write the step's keys and values into the cache; rotate keys and queries on the way.
+ *     e(a)   the smallest exponent with a <= 448 * 2^e, limited to [-40, 40]
+ *     per (page, head) that receives tokens, amax over the tokens that this call writes there:
+ *       page begun by this call (its slot 0 is written):  exp = e(amax)
+ *       otherwise:  exp = max(exp, e(amax)); where that raises it, the codes of the page's other slots are
+ *                   quantised again: code = e4m3(code * 2^(old - new))
+ *     code = e4m3(x * 2^-exp), round to nearest even, saturating
+ * Dropping rejected tokens needs no call: use a smaller kv_len next time.  A page's scale does not shrink
+ * until the page is begun again.  A non-finite key or value is stored as 0 and makes the next
+ * qspec_check_status return QSPEC_ERR_INVALID_ARG.
+ *
+ *   k, v   bf16, value d of head h of token t at k[t * k_token + h * dim + d]
+ *   plan   rotary embedding of the keys and queries (keys are rounded to bf16 before they are
+ *          quantised), or NULL: none
+ *   pos    [T] int32 device: each token's rotary position, or NULL: its cache position
+ *   q      bf16 [T] tokens of heads_q * dim values, stride q_token, rotated into q_out (stride
+ *          q_out_token; q_out may be q itself with the same stride), or NULL: no queries
+ *          (heads_q is then ignored)
+ * Token strides are multiples of 8 and at least heads * dim.  No other call may read or write the pages
+ * at the same time; the pages written must belong to one sequence only.  Given rotated keys, bit-exact.
+ */
+qspec_status qspec_kv_append(const qspec_kv_cache* cache, const qspec_kv_batch* batch, const uint16_t* k,
+                             int64_t k_token, const uint16_t* v, int64_t v_token, const qspec_rotary_plan* plan,
+                             const int32_t* pos, const uint16_t* q, int64_t q_token, int32_t heads_q,
+                             uint16_t* q_out, int64_t q_out_token, qspec_stream_t stream);
+
+/*
+ * qspec_kv_attention -- causal attention of the step's tokens over the cache (the step's own keys and
+ * values included: append first).  For token i of a sequence with n new tokens and query head h, which
+ * reads key head h / (heads_q / heads):
+ *     p = kv_len - n + i                                   (its cache position)
+ *     s_j = scale * q . k_j  for the visible j;   out = sum_j softmax(s)_j v_j;   lse = ln sum_j exp(s_j)
+ *     visible:  j <= p, and j > p - window when window > 0;
+ *     with a tree:  j < kv_len - n, or bit (j - (kv_len - n)) of the token's tree word is set (j < kv_len)
+ * A token that sees nothing gets out = 0 and lse = -inf; a query with a NaN or an infinity that sees
+ * anything gets out = lse = NaN.  Scores and softmax statistics are fp32; the
+ * probabilities are rounded to fp16 for the product with the (exactly converted) codes, out is rounded
+ * to bf16 once.
+ *
+ *   q      bf16, value d of head h of token t at q[t * q_token + h * dim + d]
+ *   window 0: none
+ *   tree   [T] uint64 device, or NULL; needs max_tok <= 64 and window == 0
+ *   out    bf16 as q with stride out_token; tokens beyond cu_tok[B] are not written
+ *   lse    [T, heads_q] fp32 or NULL
+ *   ws, ws_bytes  device workspace of >= qspec_kv_attention_workspace_size() bytes, zero-filled before
+ *          its first use; it serves every shape and is left ready for the next call
+ *   heads_q a multiple of the cache's heads, at most 128 times them; scale finite; token strides multiples of
+ *   8 and at least heads_q * dim
+ */
+size_t qspec_kv_attention_workspace_size(void);
+qspec_status qspec_kv_attention(const qspec_kv_cache* cache, const qspec_kv_batch* batch, const uint16_t* q,
+                                int64_t q_token, int32_t heads_q, float scale, int32_t window, const uint64_t* tree,
+                                uint16_t* out, int64_t out_token, float* lse, void* ws, size_t ws_bytes,
+                                qspec_stream_t stream);
+
+/*
+ * qspec_logits_adjust -- penalties for repeated tokens, biases and a grammar mask on the logits of a verify
+ * call (or of plain decoding: rows = 1).  Row i of sequence b scores the token after its history and its
+ * first i draft tokens, so those count as history there:
+ *     c[v]    occurrences of v in hist[b, prompt_len .. hist_len - 1] and draft_tok[b, 0 .. i-1]
+ *     seen[v] v occurs there or in the prompt, hist[b, 0 .. prompt_len - 1]
+ *     z = logit;  if seen: z = z > 0 ? z / repetition : z * repetition
+ *     z = z - frequency * c - (c > 0 ? presence : 0) + bias[v];   masked out: z = -inf
+ * computed in fp32 and rounded to bf16 once; a logit that nothing touches keeps its bits.
+ *
+ *   logits     [B, rows, V] bf16;  out [B, rows, V] bf16, may be logits itself
+ *   draft_tok  [B, rows-1] int32, or NULL: none
+ *   hist       [B, hist_stride] int32, hist_len [B] int32, or both NULL: no history
+ *   prompt_len [B] int32, or NULL: 0
+ *   penalties  [B, 3] fp32 (repetition > 0, frequency, presence), or NULL: 1, 0, 0
+ *   bias_ids   [B, n_bias] int32 (negative: unused entry; the last entry of an id that is repeated counts) and
+ *              bias [B, n_bias] fp32, or both NULL
+ *   mask       [B, rows, ceil(V/32)] uint32: bit v mod 32 of word v / 32 allows token v, or NULL
+ *   1 <= rows <= QSPEC_MAX_GAMMA + 1, 2 <= V <= 2^24, B*rows*V < 2^40, B <= 65535; logits and out 16-byte
+ *   aligned, the other arrays 4-byte aligned.
+ * Ids outside [0, V), lengths outside [0, hist_stride] (limited to it), prompt_len > hist_len and a repetition
+ * penalty that is not > 0 (taken as 1) make the next qspec_check_status return QSPEC_ERR_INVALID_ARG; such
+ * ids count for nothing.
+ */
+qspec_status qspec_logits_adjust(const uint16_t* logits, int32_t B, int32_t rows, int32_t V,
+                                 const int32_t* draft_tok, const int32_t* hist, int64_t hist_stride,
+                                 const int32_t* hist_len, const int32_t* prompt_len, const float* penalties,
+                                 const int32_t* bias_ids, const float* bias, int32_t n_bias, const uint32_t* mask,
+                                 uint16_t* out, qspec_stream_t stream);
+
+/*
  * qspec_check_status -- synchronises `stream`, then reports (and clears) the error words that the
  * kernels set on the device: the verify workspace's word when `ws` is not NULL, and the library's
  * own words for the linear and decode-loop kernels of the current device.  QSPEC_ERR_TIMEOUT if a
  * kernel gave up a bounded wait, QSPEC_ERR_WORKSPACE if a linear call found its workspace laid out
- * for another shape, QSPEC_ERR_INVALID_ARG if a draft token id or a gather id was out of range,
- * QSPEC_ERR_CUDA if the stream reported an error, QSPEC_OK otherwise.
+ * for another shape, QSPEC_ERR_INVALID_ARG if a draft token id or a gather id was out of range
+ * (or a kernel of the cache and logits calls met a bad value), QSPEC_ERR_CUDA if the stream reported an
+ * error, QSPEC_OK otherwise.
  */
 qspec_status qspec_check_status(void* ws, qspec_stream_t stream);
 

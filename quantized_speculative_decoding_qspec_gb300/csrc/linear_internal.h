@@ -21,7 +21,7 @@ struct WsGuard {
   unsigned long long tag;   // this call's layout tag (never 0)
   unsigned int* err;        // device address of the linear error word (current context)
 };
-enum : unsigned int { kErrTimeout = 1u, kErrWorkspace = 2u };
+enum : unsigned int { kErrTimeout = 1u, kErrWorkspace = 2u, kErrInvalid = 8u };
 // The tickets of the tensor-core kernels (split tiles) follow the header.  They must read zero when a
 // kernel starts (each kernel resets the ones it used), so both kernels keep them in one region of
 // this many words -- enough for 128-row tiles of 16 tokens, the finest split either kernel uses --

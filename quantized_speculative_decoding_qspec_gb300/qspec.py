@@ -31,6 +31,7 @@ STATUS = {
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
 _I32 = ctypes.c_int32
+_F64 = ctypes.c_double
 SIGNATURES = {
     "qspec_pack_weights": (ctypes.c_int, [_P, _I64, _I64, _P, _P, _P]),
     "qspec_linear_workspace_size": (ctypes.c_size_t, [_I64, _I64, _I64]),
@@ -52,6 +53,13 @@ SIGNATURES = {
     "qspec_linear_group": (ctypes.c_int, [_I32, _P, _I64, _I64, _P, _I32, _P, ctypes.c_size_t, _P]),
     "qspec_linear_pass_workspace_size": (ctypes.c_size_t, []),
     "qspec_linear_pass": (ctypes.c_int, [_I32, _I64, _P, _I32, _P, ctypes.c_size_t, _P]),
+    "qspec_rotary_turns": (ctypes.c_int, [_I32, _F64, _I32, _F64, _F64, _F64, _F64, _P, _P]),
+    "qspec_rotary": (ctypes.c_int, [_P, _I64, _I64, _P, _I64, _I32, _I32, _P, _I32, _P, _I64, _I64, _P]),
+    "qspec_kv_append": (ctypes.c_int, [_P, _P, _P, _I64, _P, _I64, _P, _P, _P, _I64, _I32, _P, _I64, _P]),
+    "qspec_kv_attention_workspace_size": (ctypes.c_size_t, []),
+    "qspec_kv_attention": (ctypes.c_int, [_P, _P, _P, _I64, _I32, ctypes.c_float, _I32, _P, _P, _I64, _P, _P,
+                                          ctypes.c_size_t, _P]),
+    "qspec_logits_adjust": (ctypes.c_int, [_P, _I32, _I32, _I32, _P, _P, _I64, _P, _P, _P, _P, _P, _I32, _P, _P, _P]),
     "qspec_check_status": (ctypes.c_int, [_P, _P]),
     "qspec_copy": (ctypes.c_int, [_P, _P, ctypes.c_size_t, _P]),
     "qspec_status_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -417,6 +425,213 @@ def qspec_verify_tree_greedy(tgt_logits, tree_tok, tree_parent, accept_len, out_
            load().qspec_verify_tree_greedy(_ptr(tgt_logits), _ptr(tree_tok), _ptr(tree_parent), B, R - 1, V,
                                            _ptr(accept_len), _ptr(out_tok), _ptr(accept_nodes), _ptr(ws),
                                            ws.numel(), _stream(stream)))
+
+
+def _rows(t, heads, dim, name):
+    """Pointer and token stride of a [T, heads, dim] GPU tensor whose tokens are contiguous rows."""
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim:
+        raise ValueError(f"{name} must be [T, {heads}, {dim}], got {list(t.shape)}")
+    if (dim > 1 and t.stride(2) != 1) or (heads > 1 and t.stride(1) != dim):
+        raise ValueError(f"the heads of a token of {name} must be contiguous")
+    if not t.is_cuda:
+        raise ValueError("tensor must live on the GPU")
+    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else heads * dim
+
+
+class RotaryPlan(ctypes.Structure):
+    """A rotary embedding on the device (the C struct qspec_rotary_plan)."""
+    _fields_ = [("turns", ctypes.c_void_p), ("rot", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("mult", ctypes.c_float), ("reserved", ctypes.c_int32)]
+
+
+ROTARY_SCALINGS = {"none": 0, "linear": 1, "base": 2, "bands": 3, "yarn": 4}
+
+
+def qspec_rotary_turns(rot, base=10000.0, scaling="none", factor=1.0, original=0.0, low=1.0, high=4.0):
+    """Frequencies of a rotary embedding: (int64 CPU tensor [rot/2] of 64-bit turn fractions, mult)."""
+    if scaling not in ROTARY_SCALINGS:
+        raise ValueError(f"scaling must be one of {sorted(ROTARY_SCALINGS)}")
+    turns = torch.empty(max(int(rot) // 2, 1), dtype=torch.int64)
+    mult = ctypes.c_float()
+    _check("qspec_rotary_turns", load().qspec_rotary_turns(rot, base, ROTARY_SCALINGS[scaling], factor, original, low,
+                                                           high, turns.data_ptr(), ctypes.addressof(mult)))
+    return turns, mult.value
+
+
+class Rotary:
+    """A rotary embedding, made once: frequencies on the device and the pair layout.
+
+    rot: rotated values per head; interleaved: pairs (2i, 2i+1) instead of (i, i + rot/2); scaling:
+    "none", "linear", "base", "bands" (original, low, high) or "yarn" (original, slow, fast).
+    """
+
+    def __init__(self, rot, base=10000.0, interleaved=False, scaling="none", factor=1.0, original=0.0, low=1.0,
+                 high=4.0, slow=1.0, fast=32.0, device="cuda"):
+        if scaling == "yarn":
+            low, high = slow, fast
+        turns, self.mult = qspec_rotary_turns(rot, base, scaling, factor, original, low, high)
+        self.turns = turns.to(device)
+        self.rot, self.interleaved = int(rot), bool(interleaved)
+        self.plan = RotaryPlan(_ptr(self.turns), self.rot, int(self.interleaved), self.mult, 0)
+
+    def _ref(self):
+        return ctypes.addressof(self.plan)
+
+
+def qspec_rotary(x, pos, rotary, out, inverse=False, stream=None):
+    """Rotate x bf16 [T, heads, dim] (any token and head strides) by pos int32 [T] into out (may be x)."""
+    _dt(x, torch.bfloat16, "x"); _dt(out, torch.bfloat16, "out"); _dt(pos, torch.int32, "pos")
+    if x.dim() != 3 or out.shape != x.shape:
+        raise ValueError("x and out must be [T, heads, dim]")
+    T, H, D = x.shape
+    for name, t in (("x", x), ("out", out)):
+        if not t.is_cuda:
+            raise ValueError("tensor must live on the GPU")
+        if D > 1 and t.stride(2) != 1:
+            raise ValueError(f"the values of a head of {name} must be contiguous")
+    _need(pos, T, "pos")
+    xs = [x.stride(0) if T > 1 else 0, x.stride(1) if H > 1 else 0]
+    os_ = [out.stride(0) if T > 1 else 0, out.stride(1) if H > 1 else 0]
+    _check("qspec_rotary", load().qspec_rotary(x.data_ptr(), *xs, _ptr(pos), T, H, D, rotary._ref(), int(inverse),
+                                               out.data_ptr(), *os_, _stream(stream)))
+
+
+class KVCacheDesc(ctypes.Structure):
+    """The C struct qspec_kv_cache."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_exp", ctypes.c_void_p), ("v_exp", ctypes.c_void_p),
+                ("n_pages", ctypes.c_int64), ("heads", ctypes.c_int32), ("page", ctypes.c_int32),
+                ("dim", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class KVBatchDesc(ctypes.Structure):
+    """The C struct qspec_kv_batch."""
+    _fields_ = [("cu_tok", ctypes.c_void_p), ("kv_len", ctypes.c_void_p), ("pages", ctypes.c_void_p),
+                ("B", ctypes.c_int32), ("max_pages", ctypes.c_int32), ("max_tok", ctypes.c_int32),
+                ("reserved", ctypes.c_int32), ("T", ctypes.c_int64)]
+
+
+class KVCache:
+    """A paged key/value cache: k, v uint8 [pages, heads, page, dim] of e4m3 codes, k_exp, v_exp int8 [pages, heads]."""
+
+    def __init__(self, k, v, k_exp, v_exp):
+        for name, t in (("k", k), ("v", v)):
+            _dt(t, torch.uint8, name)
+            if t.dim() != 4 or t.shape != k.shape:
+                raise ValueError("k and v must be [pages, heads, page, dim]")
+        _dt(k_exp, torch.int8, "k_exp"); _dt(v_exp, torch.int8, "v_exp")
+        n, self.heads, self.page, self.dim = k.shape
+        _need(k_exp, n * self.heads, "k_exp"); _need(v_exp, n * self.heads, "v_exp")
+        self.k, self.v, self.k_exp, self.v_exp = k, v, k_exp, v_exp
+        self.desc = KVCacheDesc(_ptr(k), _ptr(v), _ptr(k_exp), _ptr(v_exp), n, self.heads, self.page, self.dim, 0)
+
+    def values(self, which="k"):
+        """The cached values as fp32 [pages, heads, page, dim] (a torch expression, for inspection)."""
+        codes, exps = (self.k, self.k_exp) if which == "k" else (self.v, self.v_exp)
+        return codes.view(torch.float8_e4m3fn).float() * torch.exp2(exps.float())[..., None, None]
+
+
+def new_kv_cache(n_pages, heads, page, dim, device="cuda"):
+    """An empty cache of n_pages pages."""
+    def codes():
+        return torch.zeros(n_pages, heads, page, dim, dtype=torch.uint8, device=device)
+
+    def exps():
+        return torch.zeros(n_pages, heads, dtype=torch.int8, device=device)
+    return KVCache(codes(), codes(), exps(), exps())
+
+
+class KVBatch:
+    """The sequences of a step: cu_tok int32 [B+1], kv_len int32 [B], pages int32 [B, max_pages], max_tok.
+
+    The tensors are read by the kernels: update them in place between steps (graph replays included).
+    """
+
+    def __init__(self, cu_tok, kv_len, pages, max_tok):
+        _dt(cu_tok, torch.int32, "cu_tok"); _dt(kv_len, torch.int32, "kv_len"); _dt(pages, torch.int32, "pages")
+        if pages.dim() != 2:
+            raise ValueError("pages must be [B, max_pages]")
+        B, max_pages = pages.shape
+        _need(cu_tok, B + 1, "cu_tok"); _need(kv_len, B, "kv_len")
+        self.cu_tok, self.kv_len, self.pages = cu_tok, kv_len, pages
+        self.desc = KVBatchDesc(_ptr(cu_tok), _ptr(kv_len), _ptr(pages), B, max_pages, int(max_tok), 0, 0)
+
+    def _ref(self, T):
+        self.desc.T = T
+        return ctypes.addressof(self.desc)
+
+
+def qspec_kv_append(cache, batch, k, v, rotary=None, pos=None, q=None, q_out=None, stream=None):
+    """Write the step's k and v (bf16 [T, heads, dim]) into the cache; rotate k and q [T, heads_q, dim] (into
+    q_out, q itself when omitted) with a Rotary at pos int32 [T] (cache positions when omitted)."""
+    for name, t in (("k", k), ("v", v), ("q", q), ("q_out", q_out)):
+        _dt(t, torch.bfloat16, name)
+    _dt(pos, torch.int32, "pos")
+    T = k.shape[0]
+    if v.shape[0] != T or (q is not None and q.shape[0] != T):
+        raise ValueError("k, v and q must have the same number of tokens")
+    _need(pos, T, "pos")
+    kp, ks = _rows(k, cache.heads, cache.dim, "k")
+    vp, vs = _rows(v, cache.heads, cache.dim, "v")
+    qp = qs = qop = qos = hq = 0
+    if q is not None:
+        q_out = q if q_out is None else q_out
+        if q_out.shape != q.shape:
+            raise ValueError("q_out must have the shape of q")
+        hq = q.shape[1]
+        qp, qs = _rows(q, hq, cache.dim, "q")
+        qop, qos = _rows(q_out, hq, cache.dim, "q_out")
+    _check("qspec_kv_append",
+           load().qspec_kv_append(ctypes.addressof(cache.desc), batch._ref(T), kp, ks, vp, vs,
+                                  rotary._ref() if rotary is not None else None, _ptr(pos), qp or None, qs, hq,
+                                  qop or None, qos, _stream(stream)))
+
+
+def qspec_kv_attention_workspace_size():
+    return int(load().qspec_kv_attention_workspace_size())
+
+
+def new_kv_attention_workspace(device="cuda"):
+    """A zero-filled attention workspace (zero once; it serves every shape, calls keep it ready)."""
+    return torch.zeros(qspec_kv_attention_workspace_size(), dtype=torch.uint8, device=device)
+
+
+def qspec_kv_attention(cache, batch, q, out, ws, scale=None, window=0, tree=None, lse=None, stream=None):
+    """out = causal attention of q (bf16 [T, heads_q, dim]) over the cache; scale defaults to dim^-0.5, tree:
+    int64 [T] words of visible new tokens, lse: fp32 [T, heads_q]."""
+    _dt(q, torch.bfloat16, "q"); _dt(out, torch.bfloat16, "out"); _dt(tree, torch.int64, "tree")
+    _dt(lse, torch.float32, "lse"); _dt(ws, torch.uint8, "ws")
+    T, hq = q.shape[0], q.shape[1]
+    if out.shape != q.shape:
+        raise ValueError("out must have the shape of q")
+    _need(tree, T, "tree"); _need(lse, T * hq, "lse")
+    qp, qs = _rows(q, hq, cache.dim, "q")
+    op, os_ = _rows(out, hq, cache.dim, "out")
+    _check("qspec_kv_attention",
+           load().qspec_kv_attention(ctypes.addressof(cache.desc), batch._ref(T), qp, qs, hq,
+                                     cache.dim ** -0.5 if scale is None else float(scale), int(window), _ptr(tree), op,
+                                     os_, _ptr(lse), _ptr(ws), ws.numel(), _stream(stream)))
+
+
+def qspec_logits_adjust(logits, out, draft_tok=None, hist=None, hist_len=None, prompt_len=None, penalties=None,
+                        bias_ids=None, bias=None, mask=None, stream=None):
+    """Penalties, biases and a grammar mask on logits bf16 [B, rows, V] into out (may be logits)."""
+    _dt(logits, torch.bfloat16, "logits"); _dt(out, torch.bfloat16, "out")
+    for name, t in (("draft_tok", draft_tok), ("hist", hist), ("hist_len", hist_len), ("prompt_len", prompt_len),
+                    ("bias_ids", bias_ids), ("mask", mask)):
+        _dt(t, torch.int32, name)
+    _dt(penalties, torch.float32, "penalties"); _dt(bias, torch.float32, "bias")
+    B, rows, V = logits.shape
+    n_bias = bias_ids.shape[1] if bias_ids is not None else 0
+    _need(out, B * rows * V, "out"); _need(draft_tok, B * (rows - 1), "draft_tok"); _need(hist_len, B, "hist_len")
+    _need(prompt_len, B, "prompt_len"); _need(penalties, 3 * B, "penalties"); _need(bias_ids, B * n_bias, "bias_ids")
+    _need(bias, B * n_bias, "bias"); _need(mask, B * rows * ((V + 31) // 32), "mask")
+    if hist is not None and (hist.dim() != 2 or hist.shape[0] < B):
+        raise ValueError("hist must be [B, length]")
+    _check("qspec_logits_adjust",
+           load().qspec_logits_adjust(_ptr(logits), B, rows, V, _ptr(draft_tok), _ptr(hist),
+                                      hist.shape[1] if hist is not None else 0, _ptr(hist_len), _ptr(prompt_len),
+                                      _ptr(penalties), _ptr(bias_ids), _ptr(bias), n_bias, _ptr(mask), _ptr(out),
+                                      _stream(stream)))
 
 
 def _ptr_any(t, name):
