@@ -1,126 +1,42 @@
-// Attention of a step's tokens over the paged cache of e4m3 codes.
-//
-// out = sum_j softmax(scale q . k_j) v_j over the visible cache positions j, in one pass: a running
-// maximum m, the sum l of exp(s_j - m) and the weighted sum of the values are rescaled when m grows.
-// This is the plain kernel: a warp owns one (token, query head); in a step of 32 positions each lane
-// scores one key, and each lane then adds its D / 32 channels of the 32 values.
-#include "kv_internal.h"
+// Attention of a step's tokens over the paged cache of e4m3 codes: the entry point and its choice of kernel.
+#include "kv_decode.cuh"
 
 namespace qspec {
+namespace att {
 namespace {
 
-constexpr int kWarps = 4;
+// The workspace: tickets, then two partial items per CTA.  Its layout does not depend on the call's shape.
+constexpr size_t kTicketBytes = 8192;
+constexpr int kMaxGrid = 2048;
+constexpr int kSlotRows = 32, kSlotFloats = kSlotRows * (128 + 2);
 
-struct AttArgs {
-  qspec_kv_cache c;
-  qspec_kv_batch b;
-  const uint16_t* q;
-  uint16_t* out;
-  float* lse;
-  const unsigned long long* tree;
-  unsigned int* err;
-  int64_t q_token, out_token;
-  int heads_q, group, window;
-  float scale;
-};
+int max_grid() {
+  const int n = 2 * num_sms();
+  return n < kMaxGrid ? n : kMaxGrid;
+}
 
-template <int D>
-__global__ void __launch_bounds__(kWarps * 32) attention_kernel(const AttArgs a) {
-  __shared__ float qs[kWarps][D];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int b = blockIdx.z, i = blockIdx.x, h = blockIdx.y * kWarps + warp;
-  const int P = a.c.page;
-  const SeqSpan sp = seq_span(a.b, P, b);
-  if (!sp.ok && threadIdx.x == 0) atomicOr(a.err, kErrInvalid);
-  if (i >= sp.n || h >= a.heads_q) return;
-  const int64_t t = sp.tok0 + i;
-  const uint16_t* q = a.q + t * a.q_token + static_cast<int64_t>(h) * D;
-  bool odd = false;  // a NaN or an infinity in the query
-  for (int d = lane; d < D; d += 32) {
-    odd |= (q[d] & 0x7F80u) == 0x7F80u;
-    qs[warp][d] = odd ? 0.0f : bf16_lo(q[d]) * a.scale;
-  }
-  odd = __any_sync(0xFFFFFFFFu, odd);
-  const int base = sp.kv - sp.n;
-  const int hi = a.tree ? sp.kv : min(base + i + 1, sp.kv);
-  const int lo = a.window > 0 ? max(base + i + 1 - a.window, 0) : 0;
-  const unsigned long long bits = a.tree ? a.tree[t] : 0ull;
-  const int hk = h / a.group;
-  const int32_t* pages = a.b.pages + static_cast<int64_t>(b) * a.b.max_pages;
-
-  constexpr int kPer = D / 32;
-  float m = -INFINITY, l = 0.0f, acc[kPer] = {};
-  for (int j0 = lo; j0 < hi; j0 += 32) {
-    const int j = j0 + lane;
-    bool see = j < hi;
-    if (a.tree && see && j >= base) see = (bits >> (j - base)) & 1ull;
-    int page = 0;
-    if (see) {
-      page = pages[j / P];
-      if (page < 0 || page >= a.c.n_pages) {
-        atomicOr(a.err, kErrInvalid);
-        see = false;
-        page = 0;
-      }
-    }
-    const int64_t ph = static_cast<int64_t>(page) * a.c.heads + hk;
-    const int64_t at = (ph * P + (see ? j % P : 0)) * D;
-    float s = -INFINITY;
-    if (see) {
-      s = 0.0f;
-      const uint4* kp = reinterpret_cast<const uint4*>(a.c.k + at);
-      for (int d = 0; d < D / 16; ++d) {
-        const uint4 w = kp[d];
-        const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float2 x = e4m3x2_to_f32(ww[e] & 0xFFFFu), y = e4m3x2_to_f32(ww[e] >> 16);
-          const float* qd = qs[warp] + 16 * d + 4 * e;
-          s += qd[0] * x.x + qd[1] * x.y + qd[2] * y.x + qd[3] * y.y;
-        }
-      }
-      s *= exp2_int(a.c.k_exp[ph]);
-    }
-    float mx = s;
-#pragma unroll
-    for (int off = 16; off >= 1; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, off));
-    const float m1 = fmaxf(m, mx);
-    if (m1 == -INFINITY) continue;
-    const float keep = expf(m - m1), p = see ? expf(s - m1) : 0.0f;
-    m = m1;
-    l = l * keep + p;
-#pragma unroll
-    for (int e = 0; e < kPer; ++e) acc[e] *= keep;
-    const float pv = see ? p * exp2_int(a.c.v_exp[ph]) : 0.0f;
-    for (int n = 0; n < 32; ++n) {
-      const float w = __shfl_sync(0xFFFFFFFFu, pv, n);
-      const long long vat = __shfl_sync(0xFFFFFFFFu, static_cast<long long>(at), n);
-      if (!__shfl_sync(0xFFFFFFFFu, see ? 1 : 0, n)) continue;
-#pragma unroll
-      for (int e = 0; e < kPer; e += 2) {
-        const float2 x = e4m3x2_to_f32(*reinterpret_cast<const uint16_t*>(a.c.v + vat + lane * kPer + e));
-        acc[e] += w * x.x;
-        acc[e + 1] += w * x.y;
-      }
-    }
-  }
-#pragma unroll
-  for (int off = 16; off >= 1; off >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, off);
-  const float inv = l > 0.0f ? (odd ? NAN : 1.0f / l) : 0.0f;
-  uint16_t* o = a.out + t * a.out_token + static_cast<int64_t>(h) * D + lane * kPer;
-#pragma unroll
-  for (int e = 0; e < kPer; e += 2) *reinterpret_cast<uint32_t*>(o + e) = pack_bf16(acc[e] * inv, acc[e + 1] * inv);
-  if (a.lse && lane == 0) a.lse[t * a.heads_q + h] = l > 0.0f ? (odd ? NAN : m + logf(l)) : -INFINITY;
+template <int D, int RG>
+qspec_status launch_decode(const AttArgs& a, cudaStream_t s) {
+  using C = DecodeCfg<D, RG>;
+  const size_t smem = C::kSmem + sizeof(int2) * (a.b.B + 1);
+  static_assert(C::kRows <= kSlotRows && D <= 128, "partial slots");
+  if (cudaFuncSetAttribute(decode_kernel<D, RG>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           C::kSmem + static_cast<int>(sizeof(int2)) * (QSPEC_KV_MAX_B + 1)) != cudaSuccess)
+    return QSPEC_ERR_CUDA;
+  const int grid = C::kCtas * num_sms();
+  return launch_pdl(decode_kernel<D, RG>, dim3(grid < max_grid() ? grid : max_grid()), dim3(C::kThreads), smem, s, a);
 }
 
 }  // namespace
+}  // namespace att
 }  // namespace qspec
 
 using namespace qspec;
+using namespace qspec::att;
 
-extern "C" size_t qspec_kv_attention_workspace_size(void) { return 256; }
+extern "C" size_t qspec_kv_attention_workspace_size(void) {
+  return kTicketBytes + sizeof(float) * kSlotFloats * 2 * static_cast<size_t>(max_grid());
+}
 
 extern "C" qspec_status qspec_kv_attention(const qspec_kv_cache* cache, const qspec_kv_batch* batch, const uint16_t* q,
                                            int64_t q_token, int32_t heads_q, float scale, int32_t window,
@@ -136,11 +52,18 @@ extern "C" qspec_status qspec_kv_attention(const qspec_kv_cache* cache, const qs
   if ((st = check_rows(out, batch->T, row, out_token)) != QSPEC_OK) return st;
   if ((tree && (reinterpret_cast<uintptr_t>(tree) & 7u)) || !aligned4(lse) || !aligned16(ws)) return QSPEC_ERR_MISALIGNED;
   if (!ws || ws_bytes < qspec_kv_attention_workspace_size()) return QSPEC_ERR_WORKSPACE;
-  AttArgs a{*cache, *batch, q, out, lse, reinterpret_cast<const unsigned long long*>(tree), linear_error_word(),
-            q_token, out_token, heads_q, heads_q / cache->heads, window, scale};
+  AttArgs a{*cache, *batch, q, out, lse, reinterpret_cast<const unsigned long long*>(tree), linear_error_word()};
   if (!a.err) return QSPEC_ERR_CUDA;
-  const dim3 grid(batch->max_tok, (heads_q + kWarps - 1) / kWarps, batch->B);
+  a.tickets = static_cast<unsigned int*>(ws);
+  a.partial = reinterpret_cast<float*>(static_cast<char*>(ws) + kTicketBytes);
+  a.q_token = q_token;
+  a.out_token = out_token;
+  a.heads_q = heads_q;
+  a.group = heads_q / cache->heads;
+  a.window = window;
+  a.scale_log2 = scale * 1.44269504088896f;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (cache->dim == 128) return launch_pdl(attention_kernel<128>, grid, dim3(kWarps * 32), 0, s, a);
-  return launch_pdl(attention_kernel<64>, grid, dim3(kWarps * 32), 0, s, a);
+  const int64_t rows = static_cast<int64_t>(batch->max_tok) * a.group;
+  if (cache->dim == 128) return rows <= 16 ? launch_decode<128, 1>(a, s) : launch_decode<128, 2>(a, s);
+  return rows <= 16 ? launch_decode<64, 1>(a, s) : launch_decode<64, 2>(a, s);
 }

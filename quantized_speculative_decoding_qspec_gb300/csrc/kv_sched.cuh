@@ -1,0 +1,279 @@
+// How the attention kernels share out their work, and what they have in common.
+//
+// An item is one (sequence, tile of query rows, key head): the rows of a sequence and key head are its new tokens
+// times the G query heads that read that key head, packed as row = token * G + g.  An item's keys come
+// in tiles of kKeys positions; a unit is one such tile of one item.  All units of the call, in the order
+// (sequence, row tile, head, key tile), are cut into equal runs, one per CTA, whatever the lengths of the
+// sequences: every CTA reads the same number of cache bytes, and one launch serves ragged batches, single
+// long sequences and anything a graph replay finds in kv_len.  Items that lie in one run are finished
+// there; an item cut by run boundaries leaves its partial sums in the workspace, and the last of its CTAs to
+// arrive (atomic ticket) adds them in run order, so results do not depend on timing.
+#pragma once
+
+#include "kv_internal.h"
+#include "tc_ptx.cuh"
+
+namespace qspec {
+namespace att {
+
+constexpr int kKeys = 64;                        // key positions per tile
+constexpr long long kWaitLimit = 4000000000LL;   // clock cycles (about 2 s) before a wait gives up
+constexpr float kNoMax = -3.3e38f;               // running maximum of a row that has seen nothing
+
+struct AttArgs {
+  qspec_kv_cache c;
+  qspec_kv_batch b;
+  const uint16_t* q;
+  uint16_t* out;
+  float* lse;
+  const unsigned long long* tree;
+  unsigned int* err;
+  unsigned int* tickets;  // [grid]
+  float* partial;         // [grid][2][rows * (D + 2)]
+  int64_t q_token, out_token;
+  int heads_q, group, window;
+  float scale_log2;       // scale * log2(e)
+};
+
+// One item as the kernels walk it.
+struct Item {
+  int b, tile, head;
+  int tok0, n, kv;     // the sequence's first new token, their number, its cache length
+  int row0, rows;      // packed rows of the tile
+  int lo, hi;          // visible positions of any of its rows: [lo, hi)
+  int kt0, kt1;        // key tiles of this run's part
+  long long ub, ue;    // units of the whole item
+};
+
+__device__ __forceinline__ void key_range(int i0, int i1, int base, int kv, bool tree, int window, int& lo, int& hi) {
+  hi = tree ? kv : min(max(base + i1 + 1, 0), kv);
+  lo = window > 0 ? max(base + i0 + 1 - window, 0) : 0;
+  if (lo > hi) lo = hi;
+}
+__device__ __forceinline__ int key_tiles(int lo, int hi) { return max((hi + kKeys - 1) / kKeys - lo / kKeys, 1); }
+
+// Sequences in shared memory: seq[b] = {first new token, cache length, or -1 for one that is left out}, b <= B.
+template <int kRows>
+struct Walk {
+  const int2* seq;
+  int B, heads, group, window;
+  bool tree;
+  long long u, u1;
+  Item it;
+  long long first;  // units before the current (sequence, tile)
+  int nk;
+
+  __device__ int tiles(int b, int& n) const {
+    n = seq[b].y < 0 ? 0 : seq[b + 1].x - seq[b].x;
+    return (n * group + kRows - 1) / kRows;
+  }
+  __device__ void tile_range(int n, int kv, int t, int& lo, int& hi) const {
+    const int i0 = t * kRows / group, i1 = (min((t + 1) * kRows, n * group) - 1) / group;
+    key_range(i0, i1, kv - n, kv, tree, window, lo, hi);
+  }
+  // Units of sequence b.
+  __device__ long long units(int b) const {
+    int n;
+    const int nt = tiles(b, n);
+    long long s = 0;
+    for (int t = 0; t < nt; ++t) {
+      int lo, hi;
+      tile_range(n, seq[b].y, t, lo, hi);
+      s += static_cast<long long>(key_tiles(lo, hi)) * heads;
+    }
+    return s;
+  }
+  // Positions the walk at sequence b, which begins at unit `before` <= u.
+  __device__ void start(int b, long long before) {
+    it.b = b;
+    it.tile = -1;
+    first = before;
+    nk = 0;
+    int n;
+    left_ = tiles(b, n);
+    it.n = n;
+  }
+  // The next part of this run, or false.
+  __device__ bool next() {
+    if (u >= u1) return false;
+    while (it.tile < 0 || u >= first + static_cast<long long>(nk) * heads) {
+      if (it.tile >= 0) first += static_cast<long long>(nk) * heads;
+      ++it.tile;
+      while (it.tile >= left_) {
+        if (++it.b >= B) return false;
+        it.tile = 0;
+        left_ = tiles(it.b, it.n);
+      }
+      it.tok0 = seq[it.b].x;
+      it.kv = seq[it.b].y;
+      it.row0 = it.tile * kRows;
+      it.rows = min(it.n * group - it.row0, kRows);
+      tile_range(it.n, it.kv, it.tile, it.lo, it.hi);
+      nk = key_tiles(it.lo, it.hi);
+    }
+    const long long r = u - first;
+    it.head = static_cast<int>(r / nk);
+    it.ub = first + static_cast<long long>(it.head) * nk;
+    it.ue = it.ub + nk;
+    const int base = it.lo / kKeys;
+    it.kt0 = base + static_cast<int>(u - it.ub);
+    const long long end = it.ue < u1 ? it.ue : u1;
+    it.kt1 = base + static_cast<int>(end - it.ub);
+    u = end;
+    return true;
+  }
+  int left_;  // row tiles of the current sequence
+};
+
+struct ScanShared {
+  long long warp_sum[32];
+  long long total, before;
+  int b, runs;
+};
+
+// Fills seq (all threads), shares the units out and positions the walk for this CTA.  Ends with a barrier.
+template <int kRows, int kThreads>
+__device__ __forceinline__ void share_out(const AttArgs& a, int2* seq, ScanShared* sh, Walk<kRows>& w) {
+  const int B = a.b.B;
+  for (int b = threadIdx.x; b <= B; b += kThreads) {
+    if (b == B) {
+      seq[b] = make_int2(a.b.cu_tok[B], -1);
+    } else {
+      const SeqSpan s = seq_span(a.b, a.c.page, b);
+      if (!s.ok && blockIdx.x == 0) atomicOr(a.err, kErrInvalid);
+      seq[b] = make_int2(s.tok0, s.ok ? s.kv : -1);
+    }
+  }
+  __syncthreads();
+  w.seq = seq;
+  w.B = B;
+  w.heads = a.c.heads;
+  w.group = a.group;
+  w.window = a.window;
+  w.tree = a.tree != nullptr;
+  const int per = (B + kThreads - 1) / kThreads;
+  const int b0 = threadIdx.x * per;
+  long long mine = 0;
+  for (int b = b0; b < min(b0 + per, B); ++b) mine += w.units(b);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  long long incl = mine;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const long long o = __shfl_up_sync(0xFFFFFFFFu, incl, off);
+    if (lane >= off) incl += o;
+  }
+  if (lane == 31) sh->warp_sum[warp] = incl;
+  __syncthreads();
+  long long before = incl - mine, total = 0;
+  for (int i = 0; i < kThreads / 32; ++i) {
+    if (i < warp) before += sh->warp_sum[i];
+    total += sh->warp_sum[i];
+  }
+  // as many runs as CTAs, none of them empty; CTAs beyond the last run have no work
+  const long long runs = total < gridDim.x ? total : gridDim.x, c = blockIdx.x;
+  w.u = c < runs ? c * total / runs : 0;
+  w.u1 = c < runs ? (c + 1) * total / runs : 0;
+  if (w.u < w.u1 && w.u >= before && w.u < before + mine) {  // (one thread)
+    int b = b0;
+    for (long long n; w.u >= before + (n = w.units(b)); ++b) before += n;
+    sh->b = b;
+    sh->before = before;
+  }
+  if (threadIdx.x == 0) {
+    sh->total = total;
+    sh->runs = static_cast<int>(runs);
+  }
+  __syncthreads();
+  if (w.u < w.u1) w.start(sh->b, sh->before);
+}
+
+// The run that holds unit u.
+__device__ __forceinline__ int owner_of(long long u, const ScanShared* sh) {
+  return static_cast<int>(((u + 1) * sh->runs - 1) / sh->total);
+}
+
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatile int* abort_flag, unsigned int* err) {
+  if (ptx::mbar_try_wait(bar, parity)) return true;
+  const long long t0 = clock64();
+  while (true) {
+    if (*abort_flag) return false;
+    if (ptx::mbar_try_wait(bar, parity)) return true;
+    if (clock64() - t0 > kWaitLimit) {
+      *abort_flag = 1;
+      atomicOr(err, kErrTimeout);
+      return false;
+    }
+  }
+}
+// Ignores the abort flag (lets copies in flight land before the CTA exits); bounded.
+__device__ __forceinline__ void wait_bar_final(uint64_t* bar, uint32_t parity, unsigned int* err) {
+  const long long t0 = clock64();
+  while (!ptx::mbar_try_wait(bar, parity))
+    if (clock64() - t0 > kWaitLimit) {
+      atomicOr(err, kErrTimeout);
+      return;
+    }
+}
+
+// Untiled bulk copy to shared memory; 16-byte aligned addresses and size.
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(ptx::smem_u32(dst)),
+      "l"(src), "r"(bytes), "r"(ptx::smem_u32(bar))
+      : "memory");
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// What a query row needs: its factor 2^-e for fp16 (largest value at 2^14 or just above) and what turns a
+// product of such rows with codes into a score in powers of two.  amax: largest |value| as bf16 bits.
+__device__ __forceinline__ float row_shrink(uint32_t amax) {
+  // 2^(14 + 127 - exponent), limited to fp32's normal range (rows below 2^-112 are scaled less)
+  const int e = 14 + 127 - static_cast<int>(amax >> 7);
+  return exp2_int(min(max(e, -126), 126));
+}
+__device__ __forceinline__ float row_mult(uint32_t amax, float scale_log2) {
+  const int e = min(max(14 + 127 - static_cast<int>(amax >> 7), -126), 126);
+  return scale_log2 * exp2_int(-e);
+}
+// The factor of one group of keys with scale 2^ek: finite, so a zero product stays a zero score.
+__device__ __forceinline__ float score_mult(float mult, int ek) {
+  return fminf(fmaxf(mult * exp2_int(ek), -3e38f), 3e38f);
+}
+
+// Stage bookkeeping of the producer: the key segments (pages, or halves of 128-slot pages) of an item.
+// Lane l of the producer warp holds segment seg0 + l: its page and its exponents, or page -1.
+struct SegBatch {
+  int seg0 = -1, page = -1, ek = 0, ev = 0;
+};
+__device__ __forceinline__ SegBatch load_segs(const AttArgs& a, const Item& it, int seg0, int seg_keys) {
+  SegBatch s;
+  s.seg0 = seg0;
+  const long long key = static_cast<long long>(seg0 + (threadIdx.x & 31)) * seg_keys;
+  if (key < it.hi && key + seg_keys > it.lo) {
+    const int page = a.b.pages[static_cast<int64_t>(it.b) * a.b.max_pages + key / a.c.page];
+    if (page >= 0 && page < a.c.n_pages) {
+      s.page = page;
+      const int64_t ph = static_cast<int64_t>(page) * a.c.heads + it.head;
+      s.ek = a.c.k_exp[ph];
+      s.ev = a.c.v_exp[ph];
+      s.ek = min(max(s.ek, kKvMinExp), kKvMaxExp);
+      s.ev = min(max(s.ev, kKvMinExp), kKvMaxExp);
+    } else {
+      atomicOr(a.err, kErrInvalid);
+    }
+  }
+  return s;
+}
+
+}  // namespace att
+}  // namespace qspec
