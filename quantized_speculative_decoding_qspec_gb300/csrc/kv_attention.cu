@@ -1,5 +1,6 @@
 // Attention of a step's tokens over the paged cache of e4m3 codes: the entry point and its choice of kernel.
 #include "kv_decode.cuh"
+#include "kv_prefill.cuh"
 
 namespace qspec {
 namespace att {
@@ -8,10 +9,10 @@ namespace {
 // The workspace: tickets, then two partial items per CTA.  Its layout does not depend on the call's shape.
 constexpr size_t kTicketBytes = 8192;
 constexpr int kMaxGrid = 2048;
-constexpr int kSlotRows = 32, kSlotFloats = kSlotRows * (128 + 2);
+constexpr size_t slot_bytes(int rows) { return sizeof(float) * 2 * rows * (128 + 2); }  // of a CTA, heads of 128
 
-int max_grid() {
-  const int n = 2 * num_sms();
+int max_grid(int ctas_per_sm) {
+  const int n = ctas_per_sm * num_sms();
   return n < kMaxGrid ? n : kMaxGrid;
 }
 
@@ -19,12 +20,20 @@ template <int D, int RG>
 qspec_status launch_decode(const AttArgs& a, cudaStream_t s) {
   using C = DecodeCfg<D, RG>;
   const size_t smem = C::kSmem + sizeof(int2) * (a.b.B + 1);
-  static_assert(C::kRows <= kSlotRows && D <= 128, "partial slots");
   if (cudaFuncSetAttribute(decode_kernel<D, RG>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            C::kSmem + static_cast<int>(sizeof(int2)) * (QSPEC_KV_MAX_B + 1)) != cudaSuccess)
     return QSPEC_ERR_CUDA;
-  const int grid = C::kCtas * num_sms();
-  return launch_pdl(decode_kernel<D, RG>, dim3(grid < max_grid() ? grid : max_grid()), dim3(C::kThreads), smem, s, a);
+  return launch_pdl(decode_kernel<D, RG>, dim3(max_grid(C::kCtas)), dim3(C::kThreads), smem, s, a);
+}
+
+template <int D>
+qspec_status launch_prefill(const AttArgs& a, cudaStream_t s) {
+  using C = PrefillCfg<D>;
+  const size_t smem = C::kSmem + sizeof(int2) * (a.b.B + 1);
+  if (cudaFuncSetAttribute(prefill_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           C::kSmem + static_cast<int>(sizeof(int2)) * (QSPEC_KV_MAX_B + 1)) != cudaSuccess)
+    return QSPEC_ERR_CUDA;
+  return launch_pdl(prefill_kernel<D>, dim3(max_grid(1)), dim3(C::kThreads), smem, s, a);
 }
 
 }  // namespace
@@ -35,7 +44,8 @@ using namespace qspec;
 using namespace qspec::att;
 
 extern "C" size_t qspec_kv_attention_workspace_size(void) {
-  return kTicketBytes + sizeof(float) * kSlotFloats * 2 * static_cast<size_t>(max_grid());
+  const size_t few = max_grid(2) * slot_bytes(DecodeCfg<128, 2>::kRows), many = max_grid(1) * slot_bytes(PrefillCfg<128>::kRows);
+  return kTicketBytes + (few > many ? few : many);
 }
 
 extern "C" qspec_status qspec_kv_attention(const qspec_kv_cache* cache, const qspec_kv_batch* batch, const uint16_t* q,
@@ -64,6 +74,7 @@ extern "C" qspec_status qspec_kv_attention(const qspec_kv_cache* cache, const qs
   a.scale_log2 = scale * 1.44269504088896f;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const int64_t rows = static_cast<int64_t>(batch->max_tok) * a.group;
+  if (rows > 32) return cache->dim == 128 ? launch_prefill<128>(a, s) : launch_prefill<64>(a, s);
   if (cache->dim == 128) return rows <= 16 ? launch_decode<128, 1>(a, s) : launch_decode<128, 2>(a, s);
   return rows <= 16 ? launch_decode<64, 1>(a, s) : launch_decode<64, 2>(a, s);
 }

@@ -26,6 +26,7 @@ namespace att {
 template <int D, int RG>
 struct DecodeCfg {
   static constexpr int kRows = 16 * RG;
+  static constexpr int kKeys = 64;
   static constexpr int kConsumers = 128 * RG;
   static constexpr int kThreads = kConsumers + 32;
   static constexpr int kCtas = RG == 1 ? 2 : 1;              // resident per SM
@@ -39,7 +40,6 @@ struct DecodeCfg {
 struct StageMeta {
   int ek[4], ev[4];  // per 16 keys; ek = kBadGroup: nothing there
 };
-constexpr int kBadGroup = 1000;
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -52,7 +52,7 @@ template <int D, int RG>
 __global__ void __launch_bounds__(DecodeCfg<D, RG>::kThreads, DecodeCfg<D, RG>::kCtas) decode_kernel(const AttArgs a) {
   using C = DecodeCfg<D, RG>;
   using namespace ptx;
-  constexpr int kRows = C::kRows, kS = C::kStages, kSide = C::kSide, kPad = C::kRowPad;
+  constexpr int kRows = C::kRows, kKeys = C::kKeys, kS = C::kStages, kSide = C::kSide, kPad = C::kRowPad;
   constexpr int kSteps = D / 16;   // k16 steps of a score
   constexpr int kTiles = D / 8;    // n8 tiles of the output
   extern __shared__ uint8_t smem_raw[];
@@ -78,8 +78,8 @@ __global__ void __launch_bounds__(DecodeCfg<D, RG>::kThreads, DecodeCfg<D, RG>::
   }
   grid_launch_dependents();
   grid_dependency_wait();
-  Walk<kRows> walk;
-  share_out<kRows, C::kThreads>(a, seq, scan, walk);
+  Walk<kRows, kKeys> walk;
+  share_out<C::kThreads>(a, seq, scan, walk);
   const long long run0 = walk.u;
 
   if (warp == 4 * RG) {
@@ -94,7 +94,8 @@ __global__ void __launch_bounds__(DecodeCfg<D, RG>::kThreads, DecodeCfg<D, RG>::
         const int seg = kt * per_tile;
         if (sb.seg0 < 0 || seg >= sb.seg0 + 32) sb = load_segs(a, it, seg, seg_keys);
         const int st = s % kS;
-        if (s >= kS && !wait_bar(empty + st, ((s / kS) - 1) & 1, abort_flag, a.err)) break;
+        const bool ok = s < kS || wait_bar(empty + st, ((s / kS) - 1) & 1, abort_flag, a.err);
+        if (!__all_sync(0xFFFFFFFFu, ok)) break;
         const int l0 = seg - sb.seg0;
         const bool mine = lane >= l0 && lane < l0 + per_tile && sb.page >= 0;
         if (lane < 4) meta[st].ek[lane] = kBadGroup;
@@ -118,7 +119,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, RG>::kThreads, DecodeCfg<D, RG>::
           bulk_load(dst + kSide, a.c.v + at, seg_bytes, full + st);
         }
       }
-      if (*abort_flag) break;
+      if (__any_sync(0xFFFFFFFFu, *abort_flag)) break;
     }
     // nothing may still be copying into shared memory when the CTA exits
     __syncwarp();
@@ -197,7 +198,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, RG>::kThreads, DecodeCfg<D, RG>::
 
     for (int kt = it.kt0; kt < it.kt1; ++kt, ++s) {
       const int st = s % kS;
-      const bool ok = wait_bar(full + st, (s / kS) & 1, abort_flag, a.err);
+      const bool ok = __all_sync(0xFFFFFFFFu, wait_bar(full + st, (s / kS) & 1, abort_flag, a.err));
       const int ek = meta[st].ek[kw];
       const int key0 = kt * kKeys + 16 * kw;
       if (ok && ek != kBadGroup && key0 < it.hi && key0 + 16 > it.lo) {

@@ -2,7 +2,7 @@
 //
 // An item is one (sequence, tile of query rows, key head): the rows of a sequence and key head are its new tokens
 // times the G query heads that read that key head, packed as row = token * G + g.  An item's keys come
-// in tiles of kKeys positions; a unit is one such tile of one item.  All units of the call, in the order
+// in tiles of a kernel's kKeys positions; a unit is one such tile of one item.  All units of the call, in the order
 // (sequence, row tile, head, key tile), are cut into equal runs, one per CTA, whatever the lengths of the
 // sequences: every CTA reads the same number of cache bytes, and one launch serves ragged batches, single
 // long sequences and anything a graph replay finds in kv_len.  Items that lie in one run are finished
@@ -16,7 +16,6 @@
 namespace qspec {
 namespace att {
 
-constexpr int kKeys = 64;                        // key positions per tile
 constexpr long long kWaitLimit = 4000000000LL;   // clock cycles (about 2 s) before a wait gives up
 constexpr float kNoMax = -3.3e38f;               // running maximum of a row that has seen nothing
 
@@ -50,10 +49,13 @@ __device__ __forceinline__ void key_range(int i0, int i1, int base, int kv, bool
   lo = window > 0 ? max(base + i0 + 1 - window, 0) : 0;
   if (lo > hi) lo = hi;
 }
-__device__ __forceinline__ int key_tiles(int lo, int hi) { return max((hi + kKeys - 1) / kKeys - lo / kKeys, 1); }
+template <int kKeys>
+__device__ __forceinline__ int key_tiles(int lo, int hi) {
+  return max((hi + kKeys - 1) / kKeys - lo / kKeys, 1);
+}
 
 // Sequences in shared memory: seq[b] = {first new token, cache length, or -1 for one that is left out}, b <= B.
-template <int kRows>
+template <int kRows, int kKeys>
 struct Walk {
   const int2* seq;
   int B, heads, group, window;
@@ -79,7 +81,7 @@ struct Walk {
     for (int t = 0; t < nt; ++t) {
       int lo, hi;
       tile_range(n, seq[b].y, t, lo, hi);
-      s += static_cast<long long>(key_tiles(lo, hi)) * heads;
+      s += static_cast<long long>(key_tiles<kKeys>(lo, hi)) * heads;
     }
     return s;
   }
@@ -109,7 +111,7 @@ struct Walk {
       it.row0 = it.tile * kRows;
       it.rows = min(it.n * group - it.row0, kRows);
       tile_range(it.n, it.kv, it.tile, it.lo, it.hi);
-      nk = key_tiles(it.lo, it.hi);
+      nk = key_tiles<kKeys>(it.lo, it.hi);
     }
     const long long r = u - first;
     it.head = static_cast<int>(r / nk);
@@ -132,8 +134,8 @@ struct ScanShared {
 };
 
 // Fills seq (all threads), shares the units out and positions the walk for this CTA.  Ends with a barrier.
-template <int kRows, int kThreads>
-__device__ __forceinline__ void share_out(const AttArgs& a, int2* seq, ScanShared* sh, Walk<kRows>& w) {
+template <int kThreads, int kRows, int kKeys>
+__device__ __forceinline__ void share_out(const AttArgs& a, int2* seq, ScanShared* sh, Walk<kRows, kKeys>& w) {
   const int B = a.b.B;
   for (int b = threadIdx.x; b <= B; b += kThreads) {
     if (b == B) {
@@ -255,6 +257,7 @@ __device__ __forceinline__ float score_mult(float mult, int ek) {
 struct SegBatch {
   int seg0 = -1, page = -1, ek = 0, ev = 0;
 };
+constexpr int kBadGroup = 1000;  // in the place of an exponent: no keys there
 __device__ __forceinline__ SegBatch load_segs(const AttArgs& a, const Item& it, int seg0, int seg_keys) {
   SegBatch s;
   s.seg0 = seg0;
