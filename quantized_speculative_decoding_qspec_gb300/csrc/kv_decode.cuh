@@ -10,7 +10,7 @@
 //  * Keys' scales multiply the fp32 scores.  Values' scales 2^ev go into the exponent: with
 //    z = score + ev and m = max z, P = 2^(z - m) weights the bare codes and l = sum P 2^-ev is the softmax sum,
 //    so pages of different scales share one accumulator and fp16 rounds relative to the largest weight.
-//  * m only moves when a score exceeds it by more than 2^8 (fp16 has the room), which one vote per 16
+//  * m only moves when a score exceeds it by more than 2^15 (fp16 has the room), which one vote per 16
 //    keys decides; the common step has no shuffles.
 //  * A producer warp streams tiles of 64 keys through a ring with bulk copies (a page and head is one
 //    contiguous run of bytes), page ids and exponents fetched 32 segments at a time.
@@ -238,7 +238,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, RG>::kThreads, DecodeCfg<D, RG>::
         }
         const float top0 = fmaxf(fmaxf(z[0][0], z[0][1]), fmaxf(z[1][0], z[1][1]));
         const float top1 = fmaxf(fmaxf(z[0][2], z[0][3]), fmaxf(z[1][2], z[1][3]));
-        if (__any_sync(0xFFFFFFFFu, top0 > m[0] + 8.0f || top1 > m[1] + 8.0f)) {
+        if (__any_sync(0xFFFFFFFFu, top0 > m[0] + kSlack || top1 > m[1] + kSlack)) {
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
             float top = r == 0 ? top0 : top1;

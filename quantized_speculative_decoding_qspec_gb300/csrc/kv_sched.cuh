@@ -18,6 +18,8 @@ namespace att {
 
 constexpr long long kWaitLimit = 4000000000LL;   // clock cycles (about 2 s) before a wait gives up
 constexpr float kNoMax = -3.3e38f;               // running maximum of a row that has seen nothing
+// A row's maximum stays until a score exceeds it by this many powers of two: P = 2^(z - m) <= 2^15 fits fp16.
+constexpr float kSlack = 15.0f;
 
 struct AttArgs {
   qspec_kv_cache c;
@@ -127,6 +129,17 @@ struct Walk {
   int left_;  // row tiles of the current sequence
 };
 
+// A walk in shared memory, one per warp: a lane advances it, all read its item.
+template <int kRows, int kKeys>
+__device__ __forceinline__ bool walk_next(Walk<kRows, kKeys>* w) {
+  __syncwarp();
+  bool more = false;
+  if ((threadIdx.x & 31) == 0) more = w->next();
+  more = __any_sync(0xFFFFFFFFu, more);
+  __syncwarp();
+  return more;
+}
+
 struct ScanShared {
   long long warp_sum[32];
   long long total, before;
@@ -233,6 +246,29 @@ __device__ __forceinline__ float ex2(float x) {
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// (x, y) * m + b on both halves of a register pair.
+__device__ __forceinline__ void fma_pair(float& x, float& y, float m, float b) {
+  asm("{\n\t.reg .b64 v, f, c;\n\t"
+      "mov.b64 v, {%0, %1};\n\tmov.b64 f, {%2, %2};\n\tmov.b64 c, {%3, %3};\n\t"
+      "fma.rn.f32x2 v, v, f, c;\n\tmov.b64 {%0, %1}, v;\n\t}"
+      : "+f"(x), "+f"(y)
+      : "f"(m), "f"(b));
+}
+// (x, y) += (u, v).
+__device__ __forceinline__ void add_pair(float& x, float& y, float u, float v) {
+  asm("{\n\t.reg .b64 a, b;\n\t"
+      "mov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %3};\n\t"
+      "add.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
+      : "+f"(x), "+f"(y)
+      : "f"(u), "f"(v));
+}
+
+__device__ __forceinline__ float max3(float x, float y, float z) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
   return r;
 }
 
