@@ -17,8 +17,9 @@ int max_grid(int ctas_per_sm) {
 }
 
 template <int D, int RG>
-qspec_status launch_decode(const AttArgs& a, cudaStream_t s) {
+qspec_status launch_decode(AttArgs& a, int64_t rows, cudaStream_t s) {
   using C = DecodeCfg<D, RG>;
+  a.max_tiles = static_cast<int>((rows + C::kRows - 1) / C::kRows);
   const size_t smem = C::kSmem + sizeof(int2) * (a.b.B + 1);
   if (cudaFuncSetAttribute(decode_kernel<D, RG>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            C::kSmem + static_cast<int>(sizeof(int2)) * (QSPEC_KV_MAX_B + 1)) != cudaSuccess)
@@ -26,14 +27,15 @@ qspec_status launch_decode(const AttArgs& a, cudaStream_t s) {
   return launch_pdl(decode_kernel<D, RG>, dim3(max_grid(C::kCtas)), dim3(C::kThreads), smem, s, a);
 }
 
-template <int D>
-qspec_status launch_prefill(const AttArgs& a, cudaStream_t s) {
+template <int D, bool kBigPages>
+qspec_status launch_prefill(AttArgs& a, int64_t rows, cudaStream_t s) {
   using C = PrefillCfg<D>;
+  a.max_tiles = static_cast<int>((rows + C::kRows - 1) / C::kRows);
   const size_t smem = C::kSmem + sizeof(int2) * (a.b.B + 1);
-  if (cudaFuncSetAttribute(prefill_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  if (cudaFuncSetAttribute(prefill_kernel<D, kBigPages>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            C::kSmem + static_cast<int>(sizeof(int2)) * (QSPEC_KV_MAX_B + 1)) != cudaSuccess)
     return QSPEC_ERR_CUDA;
-  return launch_pdl(prefill_kernel<D>, dim3(max_grid(1)), dim3(C::kThreads), smem, s, a);
+  return launch_pdl(prefill_kernel<D, kBigPages>, dim3(max_grid(1)), dim3(C::kThreads), smem, s, a);
 }
 
 }  // namespace
@@ -62,6 +64,8 @@ extern "C" qspec_status qspec_kv_attention(const qspec_kv_cache* cache, const qs
   if ((st = check_rows(out, batch->T, row, out_token)) != QSPEC_OK) return st;
   if ((tree && (reinterpret_cast<uintptr_t>(tree) & 7u)) || !aligned4(lse) || !aligned16(ws)) return QSPEC_ERR_MISALIGNED;
   if (!ws || ws_bytes < qspec_kv_attention_workspace_size()) return QSPEC_ERR_WORKSPACE;
+  const int64_t rows = static_cast<int64_t>(batch->max_tok) * (heads_q / cache->heads);
+  if (rows > 0x7FFFFF00) return QSPEC_ERR_UNSUPPORTED_SHAPE;
   AttArgs a{*cache, *batch, q, out, lse, reinterpret_cast<const unsigned long long*>(tree), linear_error_word()};
   if (!a.err) return QSPEC_ERR_CUDA;
   a.tickets = static_cast<unsigned int*>(ws);
@@ -71,10 +75,16 @@ extern "C" qspec_status qspec_kv_attention(const qspec_kv_cache* cache, const qs
   a.heads_q = heads_q;
   a.group = heads_q / cache->heads;
   a.window = window;
+  int shift = 0;
+  while ((1 << shift) < a.group) ++shift;
+  a.group_shift = 31 + shift;
+  a.group_mul = static_cast<uint32_t>(((uint64_t(1) << a.group_shift) + a.group - 1) / a.group);
   a.scale_log2 = scale * 1.44269504088896f;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const int64_t rows = static_cast<int64_t>(batch->max_tok) * a.group;
-  if (rows > 32) return cache->dim == 128 ? launch_prefill<128>(a, s) : launch_prefill<64>(a, s);
-  if (cache->dim == 128) return rows <= 16 ? launch_decode<128, 1>(a, s) : launch_decode<128, 2>(a, s);
-  return rows <= 16 ? launch_decode<64, 1>(a, s) : launch_decode<64, 2>(a, s);
+  if (rows > 32) {
+    if (cache->page >= 64) return cache->dim == 128 ? launch_prefill<128, true>(a, rows, s) : launch_prefill<64, true>(a, rows, s);
+    return cache->dim == 128 ? launch_prefill<128, false>(a, rows, s) : launch_prefill<64, false>(a, rows, s);
+  }
+  if (cache->dim == 128) return rows <= 16 ? launch_decode<128, 1>(a, rows, s) : launch_decode<128, 2>(a, rows, s);
+  return rows <= 16 ? launch_decode<64, 1>(a, rows, s) : launch_decode<64, 2>(a, rows, s);
 }

@@ -4,15 +4,23 @@
 //   S_X = Q_X K^T (both from shared memory), P_X = 2^(S_X c + ev - m) by one thread per row, O_X += P_X V
 // with S, P and O in TMEM (S 2 x 128 columns, P over the S it came from, O 2 x D).  The two tiles alternate
 // on the tensor core, PV_0 S_0' PV_1 S_1', so that the softmax of one tile runs under the products of the other.
-//  * The cache's codes arrive by bulk copies in a ring of raw tiles; four warps turn them into fp16 (exact) in
+//  * The cache's codes arrive by bulk copies in a ring of raw tiles; six warps turn them into fp16 (exact) in
 //    the 128-byte swizzled layout.  Keys are read along channels (K-major); the same layout of the values is
 //    read along tokens (N-major B operand), so nothing is transposed.  Their lane mapping (two keys, opposite
 //    halves of the channels per quarter warp) keeps loads and stores free of bank conflicts.
 //  * Scales as in the decode kernel: 2^ek on the scores, 2^ev in the exponent, l = sum P 2^-ev.
 //  * m moves only when a score exceeds it by 2^15; then the row's O is rescaled in TMEM (S of a tile is
 //    complete only after the tile's last PV, so O is at rest).
-// Warps: 0-7 softmax (thread = row), 8-11 converters, 12 copies, 13 MMA issue.  Stages change hands by
-// mbarriers; every wait is bounded and ends the CTA in order (kErrTimeout) when it runs out.
+//  * What bounds a tile is the time from its scores to its P, about 1900 cycles, and back to the next scores
+//    (PV and S of the tile, about 1500): the other tile's products cover about 1000 of them.  A thread holds its
+//    row's 128 scores in registers, taken from the other roles' share, and issues the exponentials, which run on a
+//    pipe of their own, between the packing and summing of earlier ones.  (Two threads to a row, 64 scores
+//    each, had no registers for that: 372 to 441 us against 372 for 4096 new tokens over 8192 positions, 32 heads;
+//    reading the scores from TMEM twice, 387.)
+//  * One lane issues all MMAs.  An MMA runs 64 cycles; with descriptors built in a diverged lane it took 110 to
+//    150 to issue one and the whole kernel 556 us, so the issuing warp stays converged and only its MMAs are elected.
+// Warps: 0-7 softmax, 8 copies, 9 MMA issue, 10-15 converters.  Stages change hands by mbarriers; every wait is
+// bounded and ends the CTA in order (kErrTimeout) when it runs out.
 #pragma once
 
 #include "kv_sched.cuh"
@@ -23,9 +31,10 @@ namespace att {
 template <int D>
 struct PrefillCfg {
   static constexpr int kRows = 256, kKeys = 128;
-  static constexpr int kThreads = 16 * 32;       // (warps 14 and 15 only give their registers away)
-  // Registers of 512 threads x 128: the softmax holds 128 scores a thread and takes the others' share.
-  static constexpr int kRegsSoftmax = 200, kRegsOther = 56;
+  static constexpr int kSoftmax = 8, kCopy = 8, kMma = 9, kConv0 = 10, kConvs = 6;  // warps
+  static constexpr int kThreads = 16 * 32;
+  // Registers of 512 threads x 128: the softmax holds 128 scores a thread and takes part of the others' share.
+  static constexpr int kRegsSoftmax = 184, kRegsOther = 72;
   static constexpr int kRaw = kKeys * D;          // one side of a tile, codes
   static constexpr int kConv = kKeys * D * 2;     // the same in fp16
   static constexpr int kHalves = D / 64;          // 128-byte wide sub-tiles
@@ -40,7 +49,8 @@ struct TileMeta {
   int whole[4];  // [0]: all eight groups have keys
 };
 
-template <int D>
+// kBigPages: pages of 64 slots or more, so 64 keys lie in one page and share its scales.
+template <int D, bool kBigPages>
 __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1) prefill_kernel(const AttArgs a) {
   using C = PrefillCfg<D>;
   using namespace ptx;
@@ -73,10 +83,10 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1) prefill_kernel(con
   if (threadIdx.x == 0) {
     for (int i = 0; i < kNR; ++i) {
       mbar_init(rawfull + i, 1);
-      mbar_init(rawempty + i, 4);
+      mbar_init(rawempty + i, C::kConvs);
     }
     for (int i = 0; i < kNC; ++i) {
-      mbar_init(convfull + i, 4);
+      mbar_init(convfull + i, C::kConvs);
       mbar_init(convempty + i, 1);
     }
     for (int i = 0; i < kMeta; ++i) mbar_init(metafull + i, 1);
@@ -90,7 +100,7 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1) prefill_kernel(con
     flags[0] = 0;
     fence_mbar_init();
   }
-  if (warp == 13) {
+  if (warp == C::kMma) {
     tmem_alloc(tmem_base, kCols);
     tmem_relinquish();
   }
@@ -111,15 +121,15 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1) prefill_kernel(con
   const uint32_t tmem = *tmem_base;
 
   static_assert(2 * C::kRegsSoftmax + 2 * C::kRegsOther <= 4 * 128, "registers of the launch");
-  if (warp < 8) {
+  if (warp < C::kSoftmax) {
     reg_take<C::kRegsSoftmax>();
     // ------------------------------------------------------------------ softmax: thread = row
-    const int X = warp >> 2, row = threadIdx.x;  // row of the item
+    const int X = warp >> 2, row = threadIdx.x;  // of the item
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + lane_base + X * 128, to = tmem + lane_base + kOCol + X * D;
     // The warp's 32 rows of the queries' shared memory, reached row by row (lane = row) or with D / 8 lanes to a
-    // row (kPair rows at a time); a row's 16-byte chunks are swizzled as its MMA operand wants them.
-    constexpr int kChunks = D / 8, kPair = 32 / kChunks;
+    // row (kPer rows at a time); a row's 16-byte chunks are swizzled as its MMA operand wants them.
+    constexpr int kChunks = D / 8, kPer = 32 / kChunks, kSteps = 32 / kPer;
     uint8_t* const q_rows = qs + X * C::kQ + (warp & 3) * 32 * 128;
     auto chunk_at = [&](int r, int k) { return q_rows + (k >> 3) * kSub + r * 128 + (((k & 7) ^ (r & 7)) << 4); };
     const int my_chunk = lane % kChunks, my_row = lane / kChunks;
@@ -130,68 +140,60 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1) prefill_kernel(con
       const Item& it = walk->it;
       const int kt0 = it.kt0, tiles = it.kt1 - it.kt0;
       const bool active = X * 128 < it.rows, there = row < it.rows;
-      const int base = it.kv - it.n;
-      const int token = (it.row0 + (there ? row : 0)) / a.group;  // of the sequence's new ones
       // ---- queries: coalesced, largest value of each row to 2^14; fp16 then holds all bits of bf16
-      bool odd = false;  // the row has a NaN or an infinity
-      float mult = 0.0f;
+      uint32_t amax = 0;  // of the thread's row
       if (active) {
-        uint4 w[32 / kPair];
+        const uint16_t* qp = a.q + static_cast<int64_t>(it.tok0) * a.q_token + static_cast<int64_t>(it.head) * a.group * D + 8 * my_chunk;
+#pragma unroll 1
+        for (int i0 = 0; i0 < kSteps; i0 += 8) {  // (8 loads in flight; rolled, as cold code costs its fetch)
+          uint4 w[8];
 #pragma unroll
-        for (int i = 0; i < 32 / kPair; ++i) {
-          const int r = (warp & 7) * 32 + i * kPair + my_row;
-          const int packed = it.row0 + r, tk = packed / a.group, hq = it.head * a.group + packed - tk * a.group;
-          w[i] = r < it.rows ? *reinterpret_cast<const uint4*>(a.q + static_cast<int64_t>(it.tok0 + tk) * a.q_token +
-                                                               static_cast<int64_t>(hq) * D + 8 * my_chunk)
-                             : make_uint4(0, 0, 0, 0);
+          for (int i = 0; i < 8; ++i) {
+            const int r = warp * 32 + (i0 + i) * kPer + my_row, packed = it.row0 + r, tk = a.token_of(packed);
+            w[i] = r < it.rows ? *reinterpret_cast<const uint4*>(qp + tk * a.q_token + (packed - tk * a.group) * D) : make_uint4(0, 0, 0, 0);
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const uint32_t v[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+            uint32_t top = 0;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) top = max(top, max(v[e] & 0x7FFFu, (v[e] >> 16) & 0x7FFFu));
+#pragma unroll
+            for (int off = kChunks / 2; off >= 1; off >>= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, off));
+            const uint32_t got = __shfl_sync(0xFFFFFFFFu, top, (lane % kPer) * kChunks);
+            if (lane / kPer == i0 + i) amax = got;
+            const bool bad = top >= 0x7F80u;
+            const float shrink = copysignf(row_shrink(top), a.scale_log2);
+            uint32_t f[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) f[e] = bad ? 0u : pack_f16(bf16_lo(v[e]) * shrink, bf16_hi(v[e]) * shrink);
+            *reinterpret_cast<uint4*>(chunk_at((i0 + i) * kPer + my_row, my_chunk)) = make_uint4(f[0], f[1], f[2], f[3]);
+          }
         }
-        uint32_t amax = 0;  // of the lane's own row
-#pragma unroll
-        for (int i = 0; i < 32 / kPair; ++i) {
-          const uint32_t v[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-          uint32_t top = 0;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) top = max(top, max(v[e] & 0x7FFFu, (v[e] >> 16) & 0x7FFFu));
-#pragma unroll
-          for (int off = kChunks / 2; off >= 1; off >>= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, off));
-          const uint32_t got = __shfl_sync(0xFFFFFFFFu, top, (lane % kPair) * kChunks);
-          if (lane / kPair == i) amax = got;
-          const bool bad = top >= 0x7F80u;
-          const float shrink = copysignf(row_shrink(top), a.scale_log2);
-          uint32_t f[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) f[e] = bad ? 0u : pack_f16(bf16_lo(v[e]) * shrink, bf16_hi(v[e]) * shrink);
-          *reinterpret_cast<uint4*>(chunk_at(i * kPair + my_row, my_chunk)) = make_uint4(f[0], f[1], f[2], f[3]);
-        }
-        odd = amax >= 0x7F80u;
-        mult = row_mult(amax, fabsf(a.scale_log2));
       }
+      const bool odd = amax >= 0x7F80u;  // the row has a NaN or an infinity
+      const float mult = row_mult(amax, fabsf(a.scale_log2));
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(qfull);
-      int lim, low;
-      unsigned long long bits = 0;
-      if (a.tree) {
-        lim = it.kv;
-        low = 0;
-        bits = there ? a.tree[it.tok0 + token] : 0ull;
-      } else {
-        lim = min(max(base + token + 1, 0), it.kv);
-        low = a.window > 0 ? max(base + token + 1 - a.window, 0) : 0;
-      }
       int all_lo, all_hi;  // positions that every row of the item sees
       {
-        const int i0 = it.row0 / a.group, i1 = (it.row0 + it.rows - 1) / a.group;
+        const int i0 = a.token_of(it.row0), i1 = a.token_of(it.row0 + it.rows - 1), base = it.kv - it.n;
         all_hi = a.tree ? max(base, 0) : min(max(base + i0 + 1, 0), it.kv);
         all_lo = a.window > 0 ? max(base + i1 + 1 - a.window, 0) : 0;
       }
-      // Which of 16 keys from key j0 on the row sees (bit e: key j0 + e).
+      // Which of 16 keys from key j0 on the row sees (bit e: key j0 + e).  (What it needs is taken up anew each time:
+      // few tiles have masks.)
       auto sees = [&](int j0, float keys) {
+        const int base = it.kv - it.n, token = a.token_of(it.row0 + (row < it.rows ? row : 0));
+        const int lim = a.tree ? it.kv : min(max(base + token + 1, 0), it.kv);
+        const int low = a.window > 0 ? max(base + token + 1 - a.window, 0) : 0;
         uint32_t see = 0xFFFFu;
         if (lim - j0 < 16) see = lim > j0 ? (1u << (lim - j0)) - 1u : 0u;
         if (low > j0) see = low - j0 < 16 ? see & ~((1u << (low - j0)) - 1u) : 0u;
         if (a.tree && j0 + 16 > base) {  // from base on as the tree's word says
           const int d = j0 - base;
+          const unsigned long long bits = row < it.rows ? a.tree[it.tok0 + token] : 0ull;
           const uint32_t word = d >= 64 ? 0u : d >= 0 ? static_cast<uint32_t>(bits >> d) : static_cast<uint32_t>(bits << -d) | ((1u << -d) - 1u);
           see &= word;
         }
@@ -203,32 +205,50 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1) prefill_kernel(con
         for (int n = 0; n < tiles; ++n) {
           const int tt = t + n;
           ok = ok && wait_bar(metafull + tt % kMeta, (tt / kMeta) & 1, abort_flag, a.err);
+          const TileMeta& md = meta[tt % kMeta];
+          // what the groups of keys bring, read ahead of the scores: factor, exponent, inverse scale
+          constexpr int kGroups = kBigPages ? 2 : 8, kPairs = 64 / kGroups;  // groups with scales of their own, pairs of keys in each
+          float gm[kGroups], ge[kGroups], gu[kGroups];
+#pragma unroll
+          for (int g = 0; g < kGroups; ++g) {
+            const float4 v = md.group[g * 8 / kGroups];
+            gm[g] = fminf(mult * v.x, 3e38f);
+            ge[g] = v.y;
+            gu[g] = v.z;
+          }
+          const bool whole_tile = md.whole[0] != 0;
           ok = ok && wait_bar(sfull + X, ns & 1, abort_flag, a.err);
           ok = __all_sync(0xFFFFFFFFu, ok);
           if (!ok) break;
           ++ns;
           tc_fence_after();
-          const TileMeta& md = meta[tt % kMeta];
           const int key0 = (kt0 + n) * kKeys;
-          // The loops below stay rolled: four roles share the instruction cache, and a fully unrolled tile (8 KB
-          // of straight code a pass) left the warps waiting for instructions.
-          const bool plain = key0 + kKeys <= all_hi && key0 >= all_lo && md.whole[0] != 0;
+          const bool plain = key0 + kKeys <= all_hi && key0 >= all_lo && whole_tile;
           float top = -INFINITY;
+          float s[4][32];
           if (plain) {
-#pragma unroll 1
-            for (int h = 0; h < 2; ++h) {  // 64 keys
-              float s0[32], s1[32];
-              tmem_ld32(ts + h * 64, s0);
-              tmem_ld32(ts + h * 64 + 32, s1);
-              tmem_wait_ld();
+            tmem_ld32(ts, s[0]);
+            tmem_ld32(ts + 32, s[1]);
+            tmem_wait_ld();
+            tmem_ld32(ts + 64, s[2]);
+            tmem_ld32(ts + 96, s[3]);
+            float x = -INFINITY;
 #pragma unroll
-              for (int g = 0; g < 4; ++g) {
-                const float* sg = (g < 2 ? s0 : s1) + 16 * (g & 1);
-                float x = sg[0];
+            for (int g = 0; g < 8; ++g) {
+              if (g == 4) tmem_wait_ld();
+              const float* sg = s[g >> 1] + 16 * (g & 1);
+              float y = max3(sg[0], sg[1], sg[2]);
+              x = max3(x, sg[3], sg[4]);
 #pragma unroll
-                for (int e = 1; e < 15; e += 2) x = max3(x, sg[e], sg[e + 1]);
-                const float4 gm = md.group[4 * h + g];
-                top = fmaxf(top, fmaf(fmaxf(x, sg[15]), fminf(mult * gm.x, 3e38f), gm.y));
+              for (int e = 5; e < 13; e += 4) {
+                y = max3(y, sg[e], sg[e + 1]);
+                x = max3(x, sg[e + 2], sg[e + 3]);
+              }
+              y = max3(y, sg[13], sg[14]);
+              x = max3(x, y, sg[15]);
+              if (!kBigPages || g % 4 == 3) {
+                top = fmaxf(top, fmaf(x, gm[g * kGroups / 8], ge[g * kGroups / 8]));
+                x = -INFINITY;
               }
             }
           } else {
@@ -237,14 +257,14 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1) prefill_kernel(con
               float sg[16];
               tmem_ld16(ts + g * 16, reinterpret_cast<uint32_t*>(sg));
               tmem_wait_ld();
-              const float4 gm = md.group[g];
-              const uint32_t see = sees(key0 + 16 * g, gm.w);
+              const float4 gv = md.group[g];
+              const uint32_t see = sees(key0 + 16 * g, gv.w);
               float x = -INFINITY;
 #pragma unroll
               for (int e = 0; e < 16; ++e)
                 if (see >> e & 1u) x = fmaxf(x, sg[e]);
               // (-inf times a factor 0 would be NaN: a group that the row does not see stays out)
-              if (see) top = fmaxf(top, fmaf(x, fminf(mult * gm.x, 3e38f), gm.y));
+              if (see) top = fmaxf(top, fmaf(x, fminf(mult * gv.x, 3e38f), gv.y));
             }
           }
           if (__any_sync(0xFFFFFFFFu, top > m + kSlack)) {
@@ -266,38 +286,28 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1) prefill_kernel(con
             }
           }
           if (plain && !far) {
-#pragma unroll 1
-            for (int h = 0; h < 2; ++h) {
-              float s0[32], s1[32];
-              tmem_ld32(ts + h * 64, s0);
-              tmem_ld32(ts + h * 64 + 32, s1);
-              tmem_wait_ld();
+            // pair e of the row: exponents at step e, exponentials kLag0 pairs later, packed and summed kLag1 pairs later
+            constexpr int kLag0 = 2, kLag1 = 8;
+            uint64_t mm = 0, bb = 0, sum = 0;
+            uint32_t p[16];
 #pragma unroll
-              for (int c = 0; c < 2; ++c) {
-                float* sc = c == 0 ? s0 : s1;
-                const float4 ga = md.group[4 * h + 2 * c], gb = md.group[4 * h + 2 * c + 1];
-                const float ma = fminf(mult * ga.x, 3e38f), mb = fminf(mult * gb.x, 3e38f);
-                const float ba = ga.y - m, bb = gb.y - m;
-#pragma unroll
-                for (int e = 0; e < 16; e += 2) {
-                  fma_pair(sc[e], sc[e + 1], ma, ba);
-                  fma_pair(sc[16 + e], sc[17 + e], mb, bb);
-                }
-#pragma unroll
-                for (int e = 0; e < 32; ++e) sc[e] = ex2(sc[e]);
-                uint32_t p[16];
-#pragma unroll
-                for (int e = 0; e < 16; ++e) p[e] = pack_f16(sc[2 * e], sc[2 * e + 1]);
-                tmem_st16(ts + h * 32 + c * 16, p);
-                float la = sc[0], lb = sc[1], lc = sc[16], ld = sc[17];
-#pragma unroll
-                for (int e = 2; e < 16; e += 2) {
-                  add_pair(la, lb, sc[e], sc[e + 1]);
-                  add_pair(lc, ld, sc[16 + e], sc[17 + e]);
-                }
-                l = fmaf(la + lb, ga.z, l);
-                l = fmaf(lc + ld, gb.z, l);
+            for (int e = 0; e < 64 + kLag1; ++e) {
+              const int x = e - kLag0, f = e - kLag1;
+              if (e < 64 && e % kPairs == 0) {
+                mm = twice(gm[e / kPairs]);
+                bb = twice(ge[e / kPairs] - m);
               }
+              if (e < 64) exponents(s[e / 16][2 * e % 32], s[e / 16][2 * e % 32 + 1], mm, bb);
+              if (x >= 0 && x < 64) ex2_in_order(s[x / 16][2 * x % 32]);
+              if (f >= 0) {
+                p[f % 16] = pack_and_add(s[f / 16][2 * f % 32], s[f / 16][2 * f % 32 + 1], sum);
+                if (f % kPairs == kPairs - 1) {
+                  l = fmaf(both(sum), gu[f / kPairs], l);
+                  sum = 0;
+                }
+              }
+              if (x >= 0 && x < 64) ex2_in_order(s[x / 16][2 * x % 32 + 1]);
+              if (f >= 0 && f % 16 == 15) tmem_st16(ts + f / 16 * 16, p);
             }
           } else {
 #pragma unroll 1
@@ -305,16 +315,16 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1) prefill_kernel(con
               float sg[16];
               tmem_ld16(ts + g * 16, reinterpret_cast<uint32_t*>(sg));
               tmem_wait_ld();
-              const float4 gm = md.group[g];
-              const uint32_t see = sees(key0 + 16 * g, gm.w);
-              const float mg = fminf(mult * gm.x, 3e38f);
+              const float4 gv = md.group[g];
+              const uint32_t see = sees(key0 + 16 * g, gv.w);
+              const float mg = fminf(mult * gv.x, 3e38f);
               float sum = 0.0f;
 #pragma unroll
               for (int e = 0; e < 16; ++e) {  // (scores rounded as the maximum was)
-                sg[e] = see >> e & 1u ? ex2(fmaf(sg[e], mg, gm.y) - m) : 0.0f;
+                sg[e] = see >> e & 1u ? ex2(fmaf(sg[e], mg, gv.y) - m) : 0.0f;
                 sum += sg[e];
               }
-              l = fmaf(sum, gm.z, l);
+              l = fmaf(sum, gv.z, l);
               uint32_t p[8];
 #pragma unroll
               for (int e = 0; e < 8; ++e) p[e] = pack_f16(sg[2 * e], sg[2 * e + 1]);
@@ -340,19 +350,18 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1) prefill_kernel(con
       // Rows in shared memory (the queries are used up) -> out, a row's chunks by neighbouring lanes.
       auto store_rows = [&]() {
         __syncwarp();
+        uint16_t* op = a.out + static_cast<int64_t>(it.tok0) * a.out_token + static_cast<int64_t>(it.head) * a.group * D + 8 * my_chunk;
 #pragma unroll 4
-        for (int i = 0; i < 32 / kPair; ++i) {
-          const int r = warp * 32 + i * kPair + my_row;
-          const int packed = it.row0 + r, tk = packed / a.group, hq = it.head * a.group + packed - tk * a.group;
-          const uint4 w = *reinterpret_cast<const uint4*>(chunk_at(i * kPair + my_row, my_chunk));
-          if (r < it.rows)
-            *reinterpret_cast<uint4*>(a.out + static_cast<int64_t>(it.tok0 + tk) * a.out_token + static_cast<int64_t>(hq) * D + 8 * my_chunk) = w;
+        for (int i = 0; i < kSteps; ++i) {
+          const int r = warp * 32 + i * kPer + my_row, packed = it.row0 + r, tk = a.token_of(packed);
+          const uint4 w = *reinterpret_cast<const uint4*>(chunk_at(my_row + i * kPer, my_chunk));
+          if (r < it.rows) *reinterpret_cast<uint4*>(op + tk * a.out_token + (packed - tk * a.group) * D) = w;
         }
         __syncwarp();
       };
       auto store_lse = [&](float mm, float ll) {
         if (a.lse && there) {
-          const int hq = it.head * a.group + it.row0 + row - token * a.group;
+          const int token = a.token_of(it.row0 + row), hq = it.head * a.group + it.row0 + row - token * a.group;
           a.lse[static_cast<int64_t>(it.tok0 + token) * a.heads_q + hq] = ll == 0.0f ? -INFINITY : (mm + log2f(ll)) * 0.693147180559945f;
         }
       };
@@ -361,7 +370,6 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1) prefill_kernel(con
 #pragma unroll 1
         for (int c = 0; c < D; c += 32) {
           float o[32];
-          __syncwarp();
           tmem_ld32(to + c, o);
           tmem_wait_ld();
           if (whole) {
@@ -375,8 +383,7 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1) prefill_kernel(con
           } else {
 #pragma unroll
             for (int e = 0; e < 8; ++e)  // [channel / 4][row]: consecutive rows are consecutive addresses
-              *reinterpret_cast<float4*>(slot + (static_cast<int64_t>(c / 4 + e) * kRows + row) * 4) =
-                  make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+              *reinterpret_cast<float4*>(slot + ((c / 4 + e) * kRows + row) * 4) = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
           }
         }
         if (whole) {
@@ -416,12 +423,13 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1) prefill_kernel(con
             float4 acc[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) acc[e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 2
             for (int k = c0; k <= c1; ++k) {
               const float* p = part(k);
               const float f = ex2(__ldcg(p + kRows * D + 2 * row) - mm);
 #pragma unroll
               for (int e = 0; e < 8; ++e) {
-                const float4 v = __ldcg(reinterpret_cast<const float4*>(p + (static_cast<int64_t>(c / 4 + e) * kRows + row) * 4));
+                const float4 v = __ldcg(reinterpret_cast<const float4*>(p + ((c / 4 + e) * kRows + row) * 4));
                 acc[e].x = fmaf(v.x, f, acc[e].x);
                 acc[e].y = fmaf(v.y, f, acc[e].y);
                 acc[e].z = fmaf(v.z, f, acc[e].z);
@@ -445,63 +453,70 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1) prefill_kernel(con
         if (flags[2]) break;
       }
     }
-  } else if (warp < 12) {
+  } else {
     reg_give<C::kRegsOther>();
-    // ------------------------------------------------------------------ converters
-    const int cw = warp - 8;
-    int i = 0;
-    bool ok = true;
-    while (ok && walk_next(walk)) {
-      const Item& it = walk->it;
-      for (int kt = it.kt0; ok && kt < it.kt1; ++kt) {
-        const int kv_in = it.kv - kt * kKeys;  // slots from here on hold anything
-        for (int side = 0; side < 2; ++side, ++i) {
-          const int st = i % kNR, sc = i % kNC;
-          ok = ok && wait_bar(rawfull + st, (i / kNR) & 1, abort_flag, a.err);
-          if (i >= kNC) ok = ok && wait_bar(convempty + sc, ((i / kNC) - 1) & 1, abort_flag, a.err);
-          ok = __all_sync(0xFFFFFFFFu, ok);
-          if (!ok) break;
-          const uint8_t* src = raw + st * C::kRaw;
-          uint8_t* dst = conv + sc * C::kConv;
-          const TileMeta& md = meta[(i >> 1) % kMeta];
-          // a quarter warp takes two keys; D = 128: the first key's chunks of one half, the second's of the other
-          const int quad = lane & 3, sub = (lane >> 2) & 1;
-          const bool all = md.whole[0] != 0 && kv_in >= kKeys;
+    if (warp >= C::kConv0) {
+      // ------------------------------------------------------------------ converters
+      const int cw = warp - C::kConv0;
+      int i = 0;
+      bool ok = true;
+      while (ok && walk_next(walk)) {
+        const Item& it = walk->it;
+        for (int kt = it.kt0; ok && kt < it.kt1; ++kt) {
+          const int kv_in = it.kv - kt * kKeys;  // slots from here on hold anything
+          for (int side = 0; side < 2; ++side, ++i) {
+            const int st = i % kNR, sc = i % kNC;
+            ok = ok && wait_bar(rawfull + st, (i / kNR) & 1, abort_flag, a.err);
+            if (i >= kNC) ok = ok && wait_bar(convempty + sc, ((i / kNC) - 1) & 1, abort_flag, a.err);
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            if (!ok) break;
+            const uint8_t* src = raw + st * C::kRaw;
+            uint8_t* dst = conv + sc * C::kConv;
+            const TileMeta& md = meta[(i >> 1) % kMeta];
+            // a quarter warp takes two keys; D = 128: the first key's chunks of one half, the second's of the other
+            const int quad = lane & 3, sub = (lane >> 2) & 1;
+            const bool all = md.whole[0] != 0 && kv_in >= kKeys;
+            // 16 steps of 8 keys, two or three to a warp; all loads first
+            constexpr int kMine = (kKeys / 8 + C::kConvs - 1) / C::kConvs;
+            uint4 w[kMine][C::kHalves];
 #pragma unroll
-          for (int step = 0; step < kKeys / 32; ++step) {  // 8 keys of this warp's 32
-            const int key = cw * 32 + step * 8 + 2 * (lane >> 3) + sub;
-            const bool live = all || (md.group[key >> 4].w != 0.0f && key < kv_in);
+            for (int n = 0; n < kMine; ++n) {
+              const int step = cw + n * C::kConvs, key = step * 8 + 2 * (lane >> 3) + sub;
+              if (n < kMine - 1 || step < kKeys / 8) {
+                const bool live = all || (md.group[key >> 4].w != 0.0f && key < kv_in);
 #pragma unroll
-            for (int h = 0; h < C::kHalves; ++h) {
-              const int half = C::kHalves == 2 ? (h ^ sub) : 0;
-              uint4 w = *reinterpret_cast<const uint4*>(src + key * D + half * 64 + quad * 16);
-              if (!live) w = make_uint4(0, 0, 0, 0);
-              uint4 lo, hi;
-              lo.x = e4m3x2_to_f16x2(w.x);
-              lo.y = e4m3x2_to_f16x2(w.x >> 16);
-              lo.z = e4m3x2_to_f16x2(w.y);
-              lo.w = e4m3x2_to_f16x2(w.y >> 16);
-              hi.x = e4m3x2_to_f16x2(w.z);
-              hi.y = e4m3x2_to_f16x2(w.z >> 16);
-              hi.z = e4m3x2_to_f16x2(w.w);
-              hi.w = e4m3x2_to_f16x2(w.w >> 16);
-              uint8_t* row = dst + half * kSub + key * 128;
-              *reinterpret_cast<uint4*>(row + (((2 * quad) ^ (key & 7)) << 4)) = lo;
-              *reinterpret_cast<uint4*>(row + (((2 * quad + 1) ^ (key & 7)) << 4)) = hi;
+                for (int h = 0; h < C::kHalves; ++h) {
+                  const int half = C::kHalves == 2 ? (h ^ sub) : 0;
+                  w[n][h] = live ? *reinterpret_cast<const uint4*>(src + key * D + half * 64 + quad * 16) : make_uint4(0, 0, 0, 0);
+                }
+              }
             }
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(rawempty + st);
-            mbar_arrive(convfull + sc);
+#pragma unroll
+            for (int n = 0; n < kMine; ++n) {
+              const int step = cw + n * C::kConvs, key = step * 8 + 2 * (lane >> 3) + sub;
+              if (n < kMine - 1 || step < kKeys / 8) {
+#pragma unroll
+                for (int h = 0; h < C::kHalves; ++h) {
+                  const int half = C::kHalves == 2 ? (h ^ sub) : 0;
+                  const uint4 v = w[n][h];
+                  uint8_t* row = dst + half * kSub + key * 128;
+                  *reinterpret_cast<uint4*>(row + (((2 * quad) ^ (key & 7)) << 4)) =
+                      make_uint4(e4m3x2_to_f16x2(v.x), e4m3x2_to_f16x2(v.x >> 16), e4m3x2_to_f16x2(v.y), e4m3x2_to_f16x2(v.y >> 16));
+                  *reinterpret_cast<uint4*>(row + (((2 * quad + 1) ^ (key & 7)) << 4)) =
+                      make_uint4(e4m3x2_to_f16x2(v.z), e4m3x2_to_f16x2(v.z >> 16), e4m3x2_to_f16x2(v.w), e4m3x2_to_f16x2(v.w >> 16));
+                }
+              }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive(rawempty + st);
+              mbar_arrive(convfull + sc);
+            }
           }
         }
       }
-    }
-  } else {
-    reg_give<C::kRegsOther>();
-    if (warp == 12) {
+    } else if (warp == C::kCopy) {
       // ------------------------------------------------------------------ copies
       const int P = a.c.page, per_tile = kKeys / P;
       const uint32_t seg_bytes = P * D;
@@ -550,7 +565,7 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1) prefill_kernel(con
       // nothing may still be copying into shared memory when the CTA exits
       for (int i = issued > kNR ? issued - kNR : 0; i < issued; ++i) wait_bar_final(rawfull + i % kNR, (i / kNR) & 1, a.err);
       __syncwarp();
-    } else if (warp == 13) {
+    } else {
       // ------------------------------------------------------------------ MMA issue
       // One lane feeds the tensor core, so an MMA may cost it at most the 64 cycles that it runs: the warp stays
       // together up to the elected lane's MMAs, which keeps descriptors (bases plus constants) in uniform registers.
@@ -618,6 +633,7 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1) prefill_kernel(con
           wait_all(pfull, np0++ & 1);
           if (!ok) break;
           values(0, vs, n == 0);
+          if (!both) commit(convempty + vs);
           if (more) {
             ks = take();
             if (!ok) break;
@@ -627,9 +643,9 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1) prefill_kernel(con
             wait_all(pfull + 1, np1++ & 1);
             if (!ok) break;
             values(1, vs, n == 0);
+            commit(convempty + vs);  // (before the scores: a commit waits for all MMAs issued so far)
             if (more) scores(1, ks);
           }
-          commit(convempty + vs);
           if (more) commit(convempty + ks);
         }
         if (ok) {
@@ -650,7 +666,7 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1) prefill_kernel(con
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  if (warp == 13) {
+  if (warp == C::kMma) {
     tc_fence_after();
     tmem_dealloc(tmem, kCols);
   }

@@ -33,7 +33,13 @@ struct AttArgs {
   float* partial;         // [grid][2][rows * (D + 2)]
   int64_t q_token, out_token;
   int heads_q, group, window;
+  uint32_t group_mul, group_shift;  // row / group = row * group_mul >> group_shift, rows below 2^31
+  int max_tiles;          // row tiles of a sequence of max_tok tokens
   float scale_log2;       // scale * log2(e)
+
+  __device__ int token_of(int packed) const {
+    return static_cast<int>(static_cast<uint64_t>(static_cast<uint32_t>(packed)) * group_mul >> group_shift);
+  }
 };
 
 // One item as the kernels walk it.
@@ -61,6 +67,7 @@ template <int kRows, int kKeys>
 struct Walk {
   const int2* seq;
   int B, heads, group, window;
+  uint32_t group_mul, group_shift;
   bool tree;
   long long u, u1;
   Item it;
@@ -72,36 +79,32 @@ struct Walk {
     return (n * group + kRows - 1) / kRows;
   }
   __device__ void tile_range(int n, int kv, int t, int& lo, int& hi) const {
-    const int i0 = t * kRows / group, i1 = (min((t + 1) * kRows, n * group) - 1) / group;
+    const uint32_t r0 = t * kRows, r1 = min((t + 1) * kRows, n * group) - 1;
+    const int i0 = static_cast<int>(static_cast<uint64_t>(r0) * group_mul >> group_shift);
+    const int i1 = static_cast<int>(static_cast<uint64_t>(r1) * group_mul >> group_shift);
     key_range(i0, i1, kv - n, kv, tree, window, lo, hi);
   }
-  // Units of sequence b.
-  __device__ long long units(int b) const {
+  // Units of row tile t of sequence b (0 beyond its last).
+  __device__ long long units(int b, int t) const {
     int n;
-    const int nt = tiles(b, n);
-    long long s = 0;
-    for (int t = 0; t < nt; ++t) {
-      int lo, hi;
-      tile_range(n, seq[b].y, t, lo, hi);
-      s += static_cast<long long>(key_tiles<kKeys>(lo, hi)) * heads;
-    }
-    return s;
+    if (t >= tiles(b, n)) return 0;
+    int lo, hi;
+    tile_range(n, seq[b].y, t, lo, hi);
+    return static_cast<long long>(key_tiles<kKeys>(lo, hi)) * heads;
   }
-  // Positions the walk at sequence b, which begins at unit `before` <= u.
-  __device__ void start(int b, long long before) {
+  // Positions the walk at a row tile that begins at unit `before` <= u.
+  __device__ void start(int b, int tile, long long before) {
     it.b = b;
-    it.tile = -1;
+    it.tile = tile - 1;
     first = before;
     nk = 0;
-    int n;
-    left_ = tiles(b, n);
-    it.n = n;
+    left_ = tiles(b, it.n);
   }
   // The next part of this run, or false.
   __device__ bool next() {
     if (u >= u1) return false;
-    while (it.tile < 0 || u >= first + static_cast<long long>(nk) * heads) {
-      if (it.tile >= 0) first += static_cast<long long>(nk) * heads;
+    while (nk == 0 || u >= first + static_cast<long long>(nk) * heads) {
+      first += static_cast<long long>(nk) * heads;
       ++it.tile;
       while (it.tile >= left_) {
         if (++it.b >= B) return false;
@@ -143,7 +146,7 @@ __device__ __forceinline__ bool walk_next(Walk<kRows, kKeys>* w) {
 struct ScanShared {
   long long warp_sum[32];
   long long total, before;
-  int b, runs;
+  int b, tile, runs;
 };
 
 // Fills seq (all threads), shares the units out and positions the walk for this CTA.  Ends with a barrier.
@@ -164,12 +167,24 @@ __device__ __forceinline__ void share_out(const AttArgs& a, int2* seq, ScanShare
   w.B = B;
   w.heads = a.c.heads;
   w.group = a.group;
+  w.group_mul = a.group_mul;
+  w.group_shift = a.group_shift;
   w.window = a.window;
   w.tree = a.tree != nullptr;
-  const int per = (B + kThreads - 1) / kThreads;
-  const int b0 = threadIdx.x * per;
+  // (sequence, row tile) pairs, a run of them per thread; sequences of fewer tiles leave gaps
+  const long long pairs = static_cast<long long>(B) * a.max_tiles;
+  const int per = static_cast<int>((pairs + kThreads - 1) / kThreads);
+  const long long e0 = static_cast<long long>(threadIdx.x) * per, e1 = e0 + per < pairs ? e0 + per : pairs;
+  int b = e0 < pairs ? static_cast<int>(e0 / a.max_tiles) : 0, tile = static_cast<int>(e0 - static_cast<long long>(b) * a.max_tiles);
+  const int b_first = b, tile_first = tile;
   long long mine = 0;
-  for (int b = b0; b < min(b0 + per, B); ++b) mine += w.units(b);
+  for (long long e = e0; e < e1; ++e) {
+    mine += w.units(b, tile);
+    if (++tile == a.max_tiles) {
+      tile = 0;
+      ++b;
+    }
+  }
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   long long incl = mine;
 #pragma unroll
@@ -189,9 +204,15 @@ __device__ __forceinline__ void share_out(const AttArgs& a, int2* seq, ScanShare
   w.u = c < runs ? c * total / runs : 0;
   w.u1 = c < runs ? (c + 1) * total / runs : 0;
   if (w.u < w.u1 && w.u >= before && w.u < before + mine) {  // (one thread)
-    int b = b0;
-    for (long long n; w.u >= before + (n = w.units(b)); ++b) before += n;
+    b = b_first;
+    tile = tile_first;
+    for (long long n; w.u >= before + (n = w.units(b, tile)); before += n)
+      if (++tile == a.max_tiles) {
+        tile = 0;
+        ++b;
+      }
     sh->b = b;
+    sh->tile = tile;
     sh->before = before;
   }
   if (threadIdx.x == 0) {
@@ -199,7 +220,7 @@ __device__ __forceinline__ void share_out(const AttArgs& a, int2* seq, ScanShare
     sh->runs = static_cast<int>(runs);
   }
   __syncthreads();
-  if (w.u < w.u1) w.start(sh->b, sh->before);
+  if (w.u < w.u1) w.start(sh->b, sh->tile, sh->before);
 }
 
 // The run that holds unit u.
@@ -249,21 +270,38 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   return r;
 }
 
-// (x, y) * m + b on both halves of a register pair.
-__device__ __forceinline__ void fma_pair(float& x, float& y, float m, float b) {
-  asm("{\n\t.reg .b64 v, f, c;\n\t"
-      "mov.b64 v, {%0, %1};\n\tmov.b64 f, {%2, %2};\n\tmov.b64 c, {%3, %3};\n\t"
-      "fma.rn.f32x2 v, v, f, c;\n\tmov.b64 {%0, %1}, v;\n\t}"
-      : "+f"(x), "+f"(y)
-      : "f"(m), "f"(b));
+// A pair of scores x, y -> exponents x m + b, y m + b; a pair of probabilities packed to fp16 and added to a running
+// pair of sums.  Volatile, so the order in which a row's pairs go through stays as written: exponentials run on a
+// pipe of their own at 4 cycles a warp, and the packing and summing of pairs whose exponentials are back go between.
+__device__ __forceinline__ uint64_t twice(float x) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %1};" : "=l"(r) : "f"(x));
+  return r;
 }
-// (x, y) += (u, v).
-__device__ __forceinline__ void add_pair(float& x, float& y, float u, float v) {
-  asm("{\n\t.reg .b64 a, b;\n\t"
-      "mov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %3};\n\t"
-      "add.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
+__device__ __forceinline__ void exponents(float& x, float& y, uint64_t m, uint64_t b) {
+  asm volatile(
+      "{\n\t.reg .b64 v;\n\t"
+      "mov.b64 v, {%0, %1};\n\t"
+      "fma.rn.f32x2 v, v, %2, %3;\n\tmov.b64 {%0, %1}, v;\n\t}"
       : "+f"(x), "+f"(y)
-      : "f"(u), "f"(v));
+      : "l"(m), "l"(b));
+}
+__device__ __forceinline__ void ex2_in_order(float& x) { asm volatile("ex2.approx.ftz.f32 %0, %0;" : "+f"(x)); }
+__device__ __forceinline__ uint32_t pack_and_add(float x, float y, uint64_t& sum) {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .b64 v;\n\t"
+      "cvt.rn.f16x2.f32 %0, %3, %2;\n\t"
+      "mov.b64 v, {%2, %3};\n\t"
+      "add.rn.f32x2 %1, %1, v;\n\t}"
+      : "=r"(p), "+l"(sum)
+      : "f"(x), "f"(y));
+  return p;
+}
+__device__ __forceinline__ float both(uint64_t pair) {
+  float x, y;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(pair));
+  return x + y;
 }
 
 __device__ __forceinline__ float max3(float x, float y, float z) {
