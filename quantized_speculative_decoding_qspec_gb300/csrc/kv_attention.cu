@@ -46,7 +46,7 @@ using namespace qspec;
 using namespace qspec::att;
 
 extern "C" size_t qspec_kv_attention_workspace_size(void) {
-  const size_t few = max_grid(2) * slot_bytes(DecodeCfg<128, 2>::kRows), many = max_grid(1) * slot_bytes(PrefillCfg<128>::kRows);
+  const size_t few = max_grid(4) * slot_bytes(DecodeCfg<128, 1>::kRows), many = max_grid(1) * slot_bytes(PrefillCfg<128>::kRows);
   return kTicketBytes + (few > many ? few : many);
 }
 

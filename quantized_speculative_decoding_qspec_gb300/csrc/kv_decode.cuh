@@ -12,10 +12,13 @@
 //    so pages of different scales share one accumulator and fp16 rounds relative to the largest weight.
 //  * m only moves when a score exceeds it by more than 2^15 (fp16 has the room), which one vote per 16
 //    keys decides; the common step has no shuffles.
-//  * A producer warp streams tiles of 64 keys through a ring with bulk copies (a page and head is one
-//    contiguous run of bytes), page ids and exponents fetched 32 segments at a time.
-// Four warps share a tile (16 keys each); with more than 16 rows a second set of four takes the next 16.
-// Each warp sums its own keys; the sums meet in shared memory once per item.
+//  * Every warp streams its own keys: 16 of each tile of 64, three stages of 16-byte asynchronous copies that only
+//    the warp itself waits for.  A step is a chain of some 2000 cycles of latency, so the warps on an SM set the
+//    rate: 16 of them without a producer or a barrier in the loop, where a ring shared by a CTA (8 consumer
+//    warps, bulk copies) reached 59% of the measured bandwidth.  The copies place the 16-byte chunks so that
+//    the fragment loads are free of bank conflicts (see copy_step).
+// With more than 16 rows a second set of four warps takes the next 16 and the two warps of a key group share
+// their stages.  Each warp sums its own keys; the sums meet in shared memory once per item.
 #pragma once
 
 #include "kv_sched.cuh"
@@ -27,25 +30,21 @@ template <int D, int RG>
 struct DecodeCfg {
   static constexpr int kRows = 16 * RG;
   static constexpr int kKeys = 64;
-  static constexpr int kConsumers = 128 * RG;
-  static constexpr int kThreads = kConsumers + 32;
-  static constexpr int kCtas = RG == 1 ? 2 : 1;              // resident per SM
-  static constexpr int kSide = kKeys * D;                    // bytes of a tile's keys or values
-  static constexpr int kStages = (RG == 1 ? 4 : 8) * (128 / D);
+  static constexpr int kThreads = 128 * RG;
+  static constexpr int kCtas = 4 / RG;           // resident per SM
+  static constexpr int kStages = 3;
+  static constexpr int kSide = 16 * D;           // bytes of 16 keys or values
+  static constexpr int kRing = 4 * kStages * 2 * kSide;
   static constexpr int kRowPad = D + (D / 32) * 4 * (D == 128 ? 1 : 2);  // floats of a merge row: conflict-free
-  static constexpr int kMerge = 4 * RG * 16 * kRowPad * 4;   // bytes
-  static constexpr int kSmem = 128 + kStages * 2 * kSide + kMerge + kStages * 64 + 4096;
+  static constexpr int kMerge = 4 * RG * 16 * kRowPad * 4;               // takes the ring's place between items
+  static constexpr int kSmem = 128 + (kRing > kMerge ? kRing : kMerge) + RG * D * 32 + 2048;
 };
 
-struct StageMeta {
-  int ek[4], ev[4];  // per 16 keys; ek = kBadGroup: nothing there
-};
-
-__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint4& a, uint32_t b0, uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+      : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
 }
 
 template <int D, int RG>
@@ -53,265 +52,294 @@ __global__ void __launch_bounds__(DecodeCfg<D, RG>::kThreads, DecodeCfg<D, RG>::
   using C = DecodeCfg<D, RG>;
   using namespace ptx;
   constexpr int kRows = C::kRows, kKeys = C::kKeys, kS = C::kStages, kSide = C::kSide, kPad = C::kRowPad;
-  constexpr int kSteps = D / 16;   // k16 steps of a score
   constexpr int kTiles = D / 8;    // n8 tiles of the output
+  constexpr int kHalves = D / 64;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = smem_raw + ((128u - (smem_u32(smem_raw) & 127u)) & 127u);
-  float* merge = reinterpret_cast<float*>(ring + kS * 2 * kSide);  // [4 RG warps][16][kPad]
-  StageMeta* meta = reinterpret_cast<StageMeta*>(merge + 4 * RG * 16 * kPad);
-  uint64_t* full = reinterpret_cast<uint64_t*>(meta + kS);
-  uint64_t* empty = full + kS;
-  float2* ml = reinterpret_cast<float2*>(empty + kS);  // [4 RG][16] running maximum and sum of each warp's rows
-  ScanShared* scan = reinterpret_cast<ScanShared*>(ml + 4 * RG * 16);
-  volatile int* flags = reinterpret_cast<volatile int*>(scan + 1);  // abort, last to arrive, abort as the item ended
-  int2* seq = reinterpret_cast<int2*>(scan + 1) + 2;
-  volatile int* abort_flag = flags;
+  float* merge = reinterpret_cast<float*>(ring);  // [4 RG warps][16][kPad], between items
+  uint4* qfrag = reinterpret_cast<uint4*>(ring + (C::kRing > C::kMerge ? C::kRing : C::kMerge));  // [RG][D / 16][32]
+  float2* ml = reinterpret_cast<float2*>(qfrag + RG * D * 2);  // [4 RG][16] running maximum and sum of each warp's rows
+  Walk<kRows, kKeys>* walk = reinterpret_cast<Walk<kRows, kKeys>*>(ml + 4 * RG * 16);
+  ScanShared* scan = reinterpret_cast<ScanShared*>(walk + 1);
+  int* flags = reinterpret_cast<int*>(scan + 1);  // more items; last to arrive
+  int2* seq = reinterpret_cast<int2*>(flags + 4);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < kS; ++i) {
-      mbar_init(full + i, 1);
-      mbar_init(empty + i, 4 * RG);
-    }
-    flags[0] = 0;
-    fence_mbar_init();
-  }
   grid_launch_dependents();
   grid_dependency_wait();
-  Walk<kRows, kKeys> walk;
-  share_out<C::kThreads>(a, seq, scan, walk);
-  const long long run0 = walk.u;
-
-  if (warp == 4 * RG) {
-    // ------------------------------------------------------------------ producer
-    const int seg_keys = min(a.c.page, kKeys), per_tile = kKeys / seg_keys;
-    const uint32_t seg_bytes = seg_keys * D;
-    int s = 0;
-    while (walk.next()) {
-      const Item& it = walk.it;
-      SegBatch sb;
-      for (int kt = it.kt0; kt < it.kt1; ++kt, ++s) {
-        const int seg = kt * per_tile;
-        if (sb.seg0 < 0 || seg >= sb.seg0 + 32) sb = load_segs(a, it, seg, seg_keys);
-        const int st = s % kS;
-        const bool ok = s < kS || wait_bar(empty + st, ((s / kS) - 1) & 1, abort_flag, a.err);
-        if (!__all_sync(0xFFFFFFFFu, ok)) break;
-        const int l0 = seg - sb.seg0;
-        const bool mine = lane >= l0 && lane < l0 + per_tile && sb.page >= 0;
-        if (lane < 4) meta[st].ek[lane] = kBadGroup;
-        __syncwarp();
-        if (mine) {
-          const int g0 = (lane - l0) * (seg_keys / 16);
-          for (int g = g0; g < g0 + seg_keys / 16; ++g) {
-            meta[st].ek[g] = sb.ek;
-            meta[st].ev[g] = sb.ev;
-          }
-        }
-        const uint32_t who = __ballot_sync(0xFFFFFFFFu, mine);
-        __syncwarp();
-        if (lane == 0) mbar_arrive_expect_tx(full + st, __popc(who) * 2 * seg_bytes);
-        __syncwarp();
-        if (mine) {
-          const long long key = static_cast<long long>(seg + lane - l0) * seg_keys;
-          const int64_t at = ((static_cast<int64_t>(sb.page) * a.c.heads + it.head) * a.c.page + key % a.c.page) * D;
-          uint8_t* dst = ring + st * 2 * kSide + (lane - l0) * seg_bytes;
-          bulk_load(dst, a.c.k + at, seg_bytes, full + st);
-          bulk_load(dst + kSide, a.c.v + at, seg_bytes, full + st);
-        }
-      }
-      if (__any_sync(0xFFFFFFFFu, *abort_flag)) break;
-    }
-    // nothing may still be copying into shared memory when the CTA exits
-    __syncwarp();
-    for (int t = s > kS ? s - kS : 0; t < s; ++t) wait_bar_final(full + t % kS, (t / kS) & 1, a.err);
-    return;
+  long long run0, run1;
+  {
+    Walk<kRows, kKeys> w;
+    share_out<C::kThreads>(a, seq, scan, w);
+    run0 = w.u;
+    run1 = w.u1;
+    if (threadIdx.x == 0) *walk = w;
   }
-
-  // -------------------------------------------------------------------- consumers
   const int g = lane >> 2, c = lane & 3;
   const int rg = warp >> 2, kw = warp & 3;  // row group, key group
-  constexpr int kHalves = D / 64;
-  int s = 0;
-  while (walk.next()) {
-    const Item& it = walk.it;
-    // ---- query fragments and what each of the thread's two rows sees
-    uint32_t qf[kSteps][4];
+  uint8_t* const my_ring = ring + kw * kS * 2 * kSide;
+
+  while (true) {
+    if (threadIdx.x == 0) flags[0] = walk->next();
+    __syncthreads();
+    if (!flags[0]) break;
+    const Item& it = walk->it;
+    const int kt0 = it.kt0, kt1 = it.kt1, lo = it.lo, hi = it.hi;
+
+    // ---- the warp's stream of key groups
+    // Lane l holds page and exponents of tile batch0 + l (this warp's 16 keys of it).
+    int batch0 = kt0, b_page = -1, b_exps = 0;
+    auto load_batch = [&]() {
+      b_page = -1;
+      const long long key = (static_cast<long long>(batch0) + lane) * kKeys + 16 * kw;
+      if (batch0 + lane < kt1 && key < hi && key + 16 > lo) {
+        const int page = a.b.pages[static_cast<int64_t>(it.b) * a.b.max_pages + key / a.c.page];
+        if (page >= 0 && page < a.c.n_pages) {
+          b_page = page;
+          const int64_t ph = static_cast<int64_t>(page) * a.c.heads + it.head;
+          const int ek = min(max(static_cast<int>(a.c.k_exp[ph]), kKvMinExp), kKvMaxExp);
+          const int ev = min(max(static_cast<int>(a.c.v_exp[ph]), kKvMinExp), kKvMaxExp);
+          b_exps = (ek + 64) | (ev + 64) << 8;
+        } else {
+          atomicOr(a.err, kErrInvalid);
+        }
+      }
+    };
+    // Copies the keys and values of tile kt into a stage; returns their exponents, or -1 where there is nothing.  A row's
+    // 16-byte chunk k lands at k ^ (row & 1) * 4 for keys (a quarter warp reads 4 chunks of two rows) and at
+    // k ^ (row / 2 & 3) * 2 for values (2 chunks of four row pairs); rows of 64 bytes: as they are, k ^ (row / 2 & 3).
+    auto copy_step = [&](int kt, int stage) {
+      int exps = -1;
+      if (kt < kt1) {
+        if (kt - batch0 == 32) {
+          batch0 = kt;
+          load_batch();
+        }
+        const int page = __shfl_sync(0xFFFFFFFFu, b_page, kt - batch0);
+        if (page >= 0) {
+          exps = __shfl_sync(0xFFFFFFFFu, b_exps, kt - batch0);
+          constexpr int kPerRow = D / 16, kRowsAt = 32 / kPerRow;  // lanes to a row, rows at a time
+          const int row0 = lane / kPerRow, chunk = lane % kPerRow;
+          const int slot = (kt * kKeys + 16 * kw) & (a.c.page - 1);
+          const int64_t at = ((static_cast<int64_t>(page) * a.c.heads + it.head) * a.c.page + slot + row0) * D + chunk * 16;
+          const uint32_t dst = smem_u32(my_ring + stage * 2 * kSide);
+#pragma unroll
+          for (int n = 0; n < 16 / kRowsAt; ++n) {
+            const int row = row0 + n * kRowsAt;
+            const int ck = D == 128 ? chunk ^ (row & 1) * 4 : chunk;
+            const int cv = D == 128 ? chunk ^ (row / 2 & 3) * 2 : chunk ^ (row / 2 & 3);
+            if (RG == 1 || rg == 0) copy16_async(dst + row * D + ck * 16, a.c.k + at + n * kRowsAt * D);
+            if (RG == 1 || rg == 1) copy16_async(dst + kSide + row * D + cv * 16, a.c.v + at + n * kRowsAt * D);
+          }
+        }
+      }
+      copy_group();
+      return exps;
+    };
+    load_batch();
+    int pending[kS - 1];
+#pragma unroll
+    for (int s = 0; s < kS - 1; ++s) pending[s] = copy_step(kt0 + s, s);
+
+    // ---- query fragments (each warp of a row group writes a quarter) and what each of the thread's two rows sees
     float mult[2];
     int lim[2], low[2];
     unsigned long long bits[2];
-    const int base = it.kv - it.n;
     bool odd[2];  // rows with a NaN or an infinity
+    const int base = it.kv - it.n;
+    {
+      uint32_t* qf = reinterpret_cast<uint32_t*>(qfrag + rg * D * 2);
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const int row = rg * 16 + g + 8 * r;
-      const bool there = row < it.rows;
-      const int packed = it.row0 + (there ? row : 0);
-      const int i = packed / a.group, hq = it.head * a.group + packed - i * a.group;
-      const uint16_t* qp = a.q + static_cast<int64_t>(it.tok0 + i) * a.q_token + static_cast<int64_t>(hq) * D + 16 * c;
-      uint32_t w[kHalves][8];
-      uint32_t amax = 0;
+      for (int r = 0; r < 2; ++r) {
+        const int row = rg * 16 + g + 8 * r;
+        const bool there = row < it.rows;
+        const int packed = it.row0 + (there ? row : 0);
+        const int i = a.token_of(packed), hq = it.head * a.group + packed - i * a.group;
+        const uint16_t* qp = a.q + static_cast<int64_t>(it.tok0 + i) * a.q_token + static_cast<int64_t>(hq) * D + 16 * c;
+        uint32_t w[kHalves][8];
+        uint32_t amax = 0;
 #pragma unroll
-      for (int h = 0; h < kHalves; ++h) {
-        const uint4 x = there ? *reinterpret_cast<const uint4*>(qp + 64 * h) : make_uint4(0, 0, 0, 0);
-        const uint4 y = there ? *reinterpret_cast<const uint4*>(qp + 64 * h + 8) : make_uint4(0, 0, 0, 0);
-        const uint32_t v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+        for (int h = 0; h < kHalves; ++h) {
+          const uint4 x = there ? *reinterpret_cast<const uint4*>(qp + 64 * h) : make_uint4(0, 0, 0, 0);
+          const uint4 y = there ? *reinterpret_cast<const uint4*>(qp + 64 * h + 8) : make_uint4(0, 0, 0, 0);
+          const uint32_t v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          w[h][e] = v[e];
-          amax = max(amax, max(v[e] & 0x7FFFu, (v[e] >> 16) & 0x7FFFu));
+          for (int e = 0; e < 8; ++e) {
+            w[h][e] = v[e];
+            amax = max(amax, max(v[e] & 0x7FFFu, (v[e] >> 16) & 0x7FFFu));
+          }
         }
-      }
-      amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
-      amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
-      odd[r] = amax >= 0x7F80u;
-      const float shrink = row_shrink(amax);
-      mult[r] = row_mult(amax, a.scale_log2);
+        amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
+        amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
+        odd[r] = amax >= 0x7F80u;
+        const float shrink = row_shrink(amax);
+        mult[r] = row_mult(amax, a.scale_log2);
+        // word e of half h is k-step 4 h + e / 2, register r + 2 (e & 1) of the A fragment
 #pragma unroll
-      for (int h = 0; h < kHalves; ++h)
+        for (int h = 0; h < kHalves; ++h)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const uint32_t f = odd[r] ? 0u : pack_f16(bf16_lo(w[h][e]) * shrink, bf16_hi(w[h][e]) * shrink);
-          qf[4 * h + e / 2][r + 2 * (e & 1)] = f;
+          for (int e = 0; e < 8; ++e)
+            if ((4 * h + e / 2) % 4 == kw)
+              qf[((4 * h + e / 2) * 32 + lane) * 4 + r + 2 * (e & 1)] =
+                  odd[r] ? 0u : pack_f16(bf16_lo(w[h][e]) * shrink, bf16_hi(w[h][e]) * shrink);
+        if (a.tree) {
+          lim[r] = it.kv;
+          low[r] = 0;
+          bits[r] = there ? a.tree[it.tok0 + i] : 0ull;
+        } else {
+          lim[r] = min(max(base + i + 1, 0), it.kv);
+          low[r] = a.window > 0 ? max(base + i + 1 - a.window, 0) : 0;
+          bits[r] = 0;
         }
-      if (a.tree) {
-        lim[r] = it.kv;
-        low[r] = 0;
-        bits[r] = there ? a.tree[it.tok0 + i] : 0ull;
-      } else {
-        lim[r] = min(max(base + i + 1, 0), it.kv);
-        low[r] = a.window > 0 ? max(base + i + 1 - a.window, 0) : 0;
-        bits[r] = 0;
       }
     }
     // positions that every row of the item sees: no masks there
     int all_lo, all_hi;
     {
-      const int i0 = it.row0 / a.group, i1 = (it.row0 + it.rows - 1) / a.group;
+      const int i0 = a.token_of(it.row0), i1 = a.token_of(it.row0 + it.rows - 1);
       all_hi = a.tree ? max(base, 0) : min(max(base + i0 + 1, 0), it.kv);
       all_lo = a.window > 0 ? max(base + i1 + 1 - a.window, 0) : 0;
     }
+    __syncthreads();
+    const uint4* q4 = qfrag + rg * D * 2 + lane;
 
     float o[kTiles][4];
 #pragma unroll
     for (int j = 0; j < kTiles; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.0f;
     float m[2] = {kNoMax, kNoMax}, l[2] = {0.0f, 0.0f};
 
-    for (int kt = it.kt0; kt < it.kt1; ++kt, ++s) {
-      const int st = s % kS;
-      const bool ok = __all_sync(0xFFFFFFFFu, wait_bar(full + st, (s / kS) & 1, abort_flag, a.err));
-      const int ek = meta[st].ek[kw];
+    int stage = 0;
+    for (int kt = kt0; kt < kt1; ++kt) {
+      copy_wait<kS - 2>();
+      if (RG == 1)
+        __syncwarp();
+      else
+        named_bar_sync(1 + kw, 64);  // the two warps of the key group
+      const int exps = pending[0];
+#pragma unroll
+      for (int s = 0; s + 1 < kS - 1; ++s) pending[s] = pending[s + 1];
+      pending[kS - 2] = copy_step(kt + kS - 1, stage == 0 ? kS - 1 : stage - 1);  // over the stage read last
+      const uint8_t* at_k = my_ring + stage * 2 * kSide;
+      stage = stage == kS - 1 ? 0 : stage + 1;
+      if (exps < 0) continue;
+      const int ek = (exps & 255) - 64, ev = (exps >> 8) - 64;
       const int key0 = kt * kKeys + 16 * kw;
-      if (ok && ek != kBadGroup && key0 < it.hi && key0 + 16 > it.lo) {
-        const int ev = meta[st].ev[kw];
-        const uint8_t* kp = ring + st * 2 * kSide + (16 * kw + g) * D + 16 * c;
-        float sc[2][2][4];  // [n tile][chain]
+
+      float sc[2][2][4];  // [n tile][chain]
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
+      for (int t = 0; t < 2; ++t)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) sc[t][0][e] = sc[t][1][e] = 0.0f;
+        for (int e = 0; e < 4; ++e) sc[t][0][e] = sc[t][1][e] = 0.0f;
 #pragma unroll
-          for (int h = 0; h < kHalves; ++h) {
-            const uint4 x = *reinterpret_cast<const uint4*>(kp + 8 * t * D + 64 * h);
-            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+      for (int h = 0; h < kHalves; ++h) {
+        const int chunk = D == 128 ? (4 * h + c) ^ (g & 1) * 4 : c;
+        const uint4 x = *reinterpret_cast<const uint4*>(at_k + g * D + chunk * 16);
+        const uint4 y = *reinterpret_cast<const uint4*>(at_k + (8 + g) * D + chunk * 16);
+        const uint32_t wx[4] = {x.x, x.y, x.z, x.w}, wy[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              mma_f16(sc[t][e & 1], qf[4 * h + e], e4m3x2_to_f16x2(w[e]), e4m3x2_to_f16x2(w[e] >> 16));
-          }
+        for (int e = 0; e < 4; ++e) {
+          const uint4 q = q4[(4 * h + e) * 32];
+          uint32_t b0, b1;
+          e4m3x4_to_f16x4(wx[e], b0, b1);
+          mma_f16(sc[0][e & 1], q, b0, b1);
+          e4m3x4_to_f16x4(wy[e], b0, b1);
+          mma_f16(sc[1][e & 1], q, b0, b1);
         }
-        // ---- scores: element e of tile t is row g + 8 (e / 2), key key0 + 8 t + 2 c + (e & 1)
-        float z[2][4];
-        const float mk[2] = {score_mult(mult[0], ek), score_mult(mult[1], ek)};
+      }
+      // ---- scores: element e of tile t is row g + 8 (e / 2), key key0 + 8 t + 2 c + (e & 1)
+      float z[2][4];
+      const float mk[2] = {score_mult(mult[0], ek), score_mult(mult[1], ek)};
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) z[t][e] = fmaf(sc[t][0][e] + sc[t][1][e], mk[e >> 1], static_cast<float>(ev));
+      if (key0 + 16 > all_hi || key0 < all_lo) {
 #pragma unroll
         for (int t = 0; t < 2; ++t)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) z[t][e] = fmaf(sc[t][0][e] + sc[t][1][e], mk[e >> 1], static_cast<float>(ev));
-        if (key0 + 16 > all_hi || key0 < all_lo) {
-#pragma unroll
-          for (int t = 0; t < 2; ++t)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int j = key0 + 8 * t + 2 * c + (e & 1), r = e >> 1;
-              bool see = j < lim[r] && j >= low[r];
-              if (a.tree && j >= base) see = see && j - base < 64 && (bits[r] >> (j - base) & 1ull);
-              if (!see) z[t][e] = -INFINITY;
-            }
-        }
-        const float top0 = fmaxf(fmaxf(z[0][0], z[0][1]), fmaxf(z[1][0], z[1][1]));
-        const float top1 = fmaxf(fmaxf(z[0][2], z[0][3]), fmaxf(z[1][2], z[1][3]));
-        if (__any_sync(0xFFFFFFFFu, top0 > m[0] + kSlack || top1 > m[1] + kSlack)) {
-#pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            float top = r == 0 ? top0 : top1;
-            top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
-            top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-            const float m1 = fmaxf(m[r], top);
-            const float keep = ex2(m[r] - m1);
-            m[r] = m1;
-            l[r] *= keep;
-#pragma unroll
-            for (int j = 0; j < kTiles; ++j) {
-              o[j][2 * r] *= keep;
-              o[j][2 * r + 1] *= keep;
-            }
+          for (int e = 0; e < 4; ++e) {
+            const int j = key0 + 8 * t + 2 * c + (e & 1), r = e >> 1;
+            bool see = j < lim[r] && j >= low[r];
+            if (a.tree && j >= base) see = see && j - base < 64 && (bits[r] >> (j - base) & 1ull);
+            if (!see) z[t][e] = -INFINITY;
           }
-        }
-        uint32_t pf[4];
-        {
-          float p[2][4];
+      }
+      const float top0 = fmaxf(fmaxf(z[0][0], z[0][1]), fmaxf(z[1][0], z[1][1]));
+      const float top1 = fmaxf(fmaxf(z[0][2], z[0][3]), fmaxf(z[1][2], z[1][3]));
+      if (__any_sync(0xFFFFFFFFu, top0 > m[0] + kSlack || top1 > m[1] + kSlack)) {
 #pragma unroll
-          for (int t = 0; t < 2; ++t)
+        for (int r = 0; r < 2; ++r) {
+          float top = r == 0 ? top0 : top1;
+          top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+          top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+          const float m1 = fmaxf(m[r], top);
+          const float keep = ex2(m[r] - m1);
+          m[r] = m1;
+          l[r] *= keep;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) p[t][e] = ex2(z[t][e] - m[e >> 1]);
-          const float unit = exp2_int(-ev);
-          l[0] = fmaf(p[0][0] + p[0][1] + p[1][0] + p[1][1], unit, l[0]);
-          l[1] = fmaf(p[0][2] + p[0][3] + p[1][2] + p[1][3], unit, l[1]);
-          pf[0] = pack_f16(p[0][0], p[0][1]);
-          pf[1] = pack_f16(p[0][2], p[0][3]);
-          pf[2] = pack_f16(p[1][0], p[1][1]);
-          pf[3] = pack_f16(p[1][2], p[1][3]);
-        }
-        // ---- values: channels [g * kTiles, + kTiles) of keys 2c, 2c + 1, 2c + 8, 2c + 9
-        const uint8_t* vp = ring + st * 2 * kSide + kSide + (16 * kw + 2 * c) * D + g * kTiles;
-        uint32_t v[4][kTiles / 4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint8_t* at = vp + ((k & 1) + 8 * (k >> 1)) * D;
-          if (D == 128) {
-            const uint4 x = *reinterpret_cast<const uint4*>(at);
-            v[k][0] = x.x;
-            v[k][1] = x.y;
-            v[k][kTiles / 4 - 2] = x.z;
-            v[k][kTiles / 4 - 1] = x.w;
-          } else {
-            const uint2 x = *reinterpret_cast<const uint2*>(at);
-            v[k][0] = x.x;
-            v[k][1] = x.y;
+          for (int j = 0; j < kTiles; ++j) {
+            o[j][2 * r] *= keep;
+            o[j][2 * r + 1] *= keep;
           }
-        }
-        if (key0 + 16 > it.kv) {  // slots behind the end hold anything, NaN codes included
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            if (key0 + 2 * c + (k & 1) + 8 * (k >> 1) >= it.kv)
-#pragma unroll
-              for (int w = 0; w < kTiles / 4; ++w) v[k][w] = 0;
-        }
-#pragma unroll
-        for (int w = 0; w < kTiles / 4; ++w) {
-          // bytes (key 0, key 1) of two channels per word
-          const uint32_t a0 = __byte_perm(v[0][w], v[1][w], 0x5140), a1 = __byte_perm(v[0][w], v[1][w], 0x7362);
-          const uint32_t b0 = __byte_perm(v[2][w], v[3][w], 0x5140), b1 = __byte_perm(v[2][w], v[3][w], 0x7362);
-          mma_f16(o[4 * w + 0], pf, e4m3x2_to_f16x2(a0), e4m3x2_to_f16x2(b0));
-          mma_f16(o[4 * w + 1], pf, e4m3x2_to_f16x2(a0 >> 16), e4m3x2_to_f16x2(b0 >> 16));
-          mma_f16(o[4 * w + 2], pf, e4m3x2_to_f16x2(a1), e4m3x2_to_f16x2(b1));
-          mma_f16(o[4 * w + 3], pf, e4m3x2_to_f16x2(a1 >> 16), e4m3x2_to_f16x2(b1 >> 16));
         }
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(empty + st);
-      if (!ok) break;
+      uint4 pf;
+      {
+        float p[2][4];
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) p[t][e] = ex2(z[t][e] - m[e >> 1]);
+        const float unit = exp2_int(-ev);
+        l[0] = fmaf(p[0][0] + p[0][1] + p[1][0] + p[1][1], unit, l[0]);
+        l[1] = fmaf(p[0][2] + p[0][3] + p[1][2] + p[1][3], unit, l[1]);
+        pf = make_uint4(pack_f16(p[0][0], p[0][1]), pack_f16(p[0][2], p[0][3]), pack_f16(p[1][0], p[1][1]), pack_f16(p[1][2], p[1][3]));
+      }
+      // ---- values: channels [g * kTiles, + kTiles) of keys 2c, 2c + 1, 2c + 8, 2c + 9 (row / 2 & 3 = c for all four)
+      const uint8_t* at_v = at_k + kSide + 2 * c * D + (D == 128 ? (g ^ 2 * c) * 16 : (g / 2 ^ c) * 16 + (g & 1) * 8);
+      uint32_t v[4][kTiles / 4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint8_t* at = at_v + ((k & 1) + 8 * (k >> 1)) * D;
+        if (D == 128) {
+          const uint4 x = *reinterpret_cast<const uint4*>(at);
+          v[k][0] = x.x;
+          v[k][1] = x.y;
+          v[k][kTiles / 4 - 2] = x.z;
+          v[k][kTiles / 4 - 1] = x.w;
+        } else {
+          const uint2 x = *reinterpret_cast<const uint2*>(at);
+          v[k][0] = x.x;
+          v[k][1] = x.y;
+        }
+      }
+      if (key0 + 16 > it.kv) {  // slots behind the end hold anything, NaN codes included
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (key0 + 2 * c + (k & 1) + 8 * (k >> 1) >= it.kv)
+#pragma unroll
+            for (int w = 0; w < kTiles / 4; ++w) v[k][w] = 0;
+      }
+#pragma unroll
+      for (int w = 0; w < kTiles / 4; ++w) {
+        // bytes (key 0, key 1) of two channels per word
+        const uint32_t a0 = __byte_perm(v[0][w], v[1][w], 0x5140), a1 = __byte_perm(v[0][w], v[1][w], 0x7362);
+        const uint32_t b0 = __byte_perm(v[2][w], v[3][w], 0x5140), b1 = __byte_perm(v[2][w], v[3][w], 0x7362);
+        uint32_t x0, x1, y0, y1;
+        e4m3x4_to_f16x4(a0, x0, x1);
+        e4m3x4_to_f16x4(b0, y0, y1);
+        mma_f16(o[4 * w + 0], pf, x0, y0);
+        mma_f16(o[4 * w + 1], pf, x1, y1);
+        e4m3x4_to_f16x4(a1, x0, x1);
+        e4m3x4_to_f16x4(b1, y0, y1);
+        mma_f16(o[4 * w + 2], pf, x0, y0);
+        mma_f16(o[4 * w + 3], pf, x1, y1);
+      }
     }
+    copy_wait<0>();
 
-    // ---- the four key groups of each row meet in shared memory
+    // ---- the four key groups of each row meet in shared memory, where the ring was
+    __syncthreads();
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       l[r] += __shfl_xor_sync(0xFFFFFFFFu, l[r], 1);
@@ -328,7 +356,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, RG>::kThreads, DecodeCfg<D, RG>::
               make_float4(o[j][2 * r + e], o[j + 1][2 * r + e], o[j + 2][2 * r + e], o[j + 3][2 * r + e]);
         }
     }
-    named_bar_sync(1, C::kConsumers);
+    __syncthreads();
     const int row = threadIdx.x >> 3, part = threadIdx.x & 7;  // row of the item, 4-channel chunks part + 8 k
     const int w0 = (row >> 4) * 4;
     constexpr int kChunks = D / 32;
@@ -360,8 +388,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, RG>::kThreads, DecodeCfg<D, RG>::
       }
     }
     bool done = true;
-    const long long end = walk.u1;
-    if (it.ub < run0 || it.ue > end) {
+    if (it.ub < run0 || it.ue > run1) {
       // ---- part of an item: leave it in the workspace; the last part to arrive adds all of them
       constexpr int kSlot = kRows * (D + 2);
       const int c0 = owner_of(it.ub, scan), c1 = owner_of(it.ue - 1, scan);
@@ -372,15 +399,13 @@ __global__ void __launch_bounds__(DecodeCfg<D, RG>::kThreads, DecodeCfg<D, RG>::
         if (part == 0) *reinterpret_cast<float2*>(slot + kRows * D + 2 * row) = make_float2(mm, ll);
       }
       __threadfence();
-      named_bar_sync(1, C::kConsumers);
+      __syncthreads();
       if (threadIdx.x == 0) {
-        const unsigned int n = static_cast<unsigned int>(c1 - c0);
-        const bool last = atomicAdd(a.tickets + c0, 1u) == n;
+        const bool last = atomicAdd(a.tickets + c0, 1u) == static_cast<unsigned int>(c1 - c0);
         if (last) a.tickets[c0] = 0;
         flags[1] = last;
-        flags[2] = *abort_flag;  // (one reading for all warps: they leave together)
       }
-      named_bar_sync(1, C::kConsumers);
+      __syncthreads();
       done = flags[1] != 0;
       if (done && row < it.rows) {
         __threadfence();
@@ -408,13 +433,9 @@ __global__ void __launch_bounds__(DecodeCfg<D, RG>::kThreads, DecodeCfg<D, RG>::
           }
         }
       }
-    } else {
-      if (threadIdx.x == 0) flags[2] = *abort_flag;
-      named_bar_sync(1, C::kConsumers);  // the merge buffer is read: the next item may fill it
     }
-    if (flags[2]) break;
     if (done && row < it.rows) {
-      const int packed = it.row0 + row, i = packed / a.group;
+      const int packed = it.row0 + row, i = a.token_of(packed);
       const int64_t t = it.tok0 + i;
       const int hq = it.head * a.group + packed - i * a.group;
       const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
@@ -426,6 +447,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, RG>::kThreads, DecodeCfg<D, RG>::
       if (a.lse && part == 0)
         a.lse[t * a.heads_q + hq] = ll == 0.0f ? -INFINITY : (mm + log2f(ll)) * 0.693147180559945f;
     }
+    __syncthreads();  // the item and the merge buffer are read: the next item may take their places
   }
 }
 
