@@ -601,7 +601,7 @@ qspec_status qspec_kv_attention(const qspec_kv_cache* cache, const qspec_kv_batc
  *   bias_ids   [B, n_bias] int32 (negative: unused entry; the last entry of an id that is repeated counts) and
  *              bias [B, n_bias] fp32, or both NULL
  *   mask       [B, rows, ceil(V/32)] uint32: bit v mod 32 of word v / 32 allows token v, or NULL
- *   1 <= rows <= QSPEC_MAX_GAMMA + 1, 2 <= V <= 2^24, B*rows*V < 2^40, B <= 65535; logits and out 16-byte
+ *   1 <= rows <= QSPEC_MAX_GAMMA + 1, 2 <= V <= 2^24, B*rows*V < 2^40, B <= 65535, n_bias <= 65535; logits and out 16-byte
  *   aligned, the other arrays 4-byte aligned.
  * Ids outside [0, V), lengths outside [0, hist_stride] (limited to it), prompt_len > hist_len and a repetition
  * penalty that is not > 0 (taken as 1) make the next qspec_check_status return QSPEC_ERR_INVALID_ARG; such

@@ -65,7 +65,7 @@ extern "C" qspec_status qspec_kv_attention(const qspec_kv_cache* cache, const qs
   if ((tree && (reinterpret_cast<uintptr_t>(tree) & 7u)) || !aligned4(lse) || !aligned16(ws)) return QSPEC_ERR_MISALIGNED;
   if (!ws || ws_bytes < qspec_kv_attention_workspace_size()) return QSPEC_ERR_WORKSPACE;
   const int64_t rows = static_cast<int64_t>(batch->max_tok) * (heads_q / cache->heads);
-  if (rows > 0x7FFFFF00) return QSPEC_ERR_UNSUPPORTED_SHAPE;
+  if (rows > 0x7FFFFF00 || batch->B * ((rows + 15) / 16) >= (int64_t(1) << 30)) return QSPEC_ERR_UNSUPPORTED_SHAPE;
   AttArgs a{*cache, *batch, q, out, lse, reinterpret_cast<const unsigned long long*>(tree), linear_error_word()};
   if (!a.err) return QSPEC_ERR_CUDA;
   a.tickets = static_cast<unsigned int*>(ws);

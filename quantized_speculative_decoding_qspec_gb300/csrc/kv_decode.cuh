@@ -88,9 +88,10 @@ __global__ void __launch_bounds__(DecodeCfg<D, RG>::kThreads, DecodeCfg<D, RG>::
 
     // ---- the warp's stream of key groups
     // Lane l holds page and exponents of tile batch0 + l (this warp's 16 keys of it).
-    int batch0 = kt0, b_page = -1, b_exps = 0;
+    int batch0 = kt0, b_page = -1, b_exps = 0, b_before = 0;  // b_before: the exponents of the batch before
     auto load_batch = [&]() {
       b_page = -1;
+      b_before = b_exps;
       const long long key = (static_cast<long long>(batch0) + lane) * kKeys + 16 * kw;
       if (batch0 + lane < kt1 && key < hi && key + 16 > lo) {
         const int page = a.b.pages[static_cast<int64_t>(it.b) * a.b.max_pages + key / a.c.page];
@@ -105,11 +106,12 @@ __global__ void __launch_bounds__(DecodeCfg<D, RG>::kThreads, DecodeCfg<D, RG>::
         }
       }
     };
-    // Copies the keys and values of tile kt into a stage; returns their exponents, or -1 where there is nothing.  A row's
+    // Copies the keys and values of tile kt into a stage; returns whether there are any.  (Their exponents are looked at
+    // when the stage is read: the copies need not wait for them.)  A row's
     // 16-byte chunk k lands at k ^ (row & 1) * 4 for keys (a quarter warp reads 4 chunks of two rows) and at
     // k ^ (row / 2 & 3) * 2 for values (2 chunks of four row pairs); rows of 64 bytes: as they are, k ^ (row / 2 & 3).
     auto copy_step = [&](int kt, int stage) {
-      int exps = -1;
+      bool any = false;
       if (kt < kt1) {
         if (kt - batch0 == 32) {
           batch0 = kt;
@@ -117,7 +119,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, RG>::kThreads, DecodeCfg<D, RG>::
         }
         const int page = __shfl_sync(0xFFFFFFFFu, b_page, kt - batch0);
         if (page >= 0) {
-          exps = __shfl_sync(0xFFFFFFFFu, b_exps, kt - batch0);
+          any = true;
           constexpr int kPerRow = D / 16, kRowsAt = 32 / kPerRow;  // lanes to a row, rows at a time
           const int row0 = lane / kPerRow, chunk = lane % kPerRow;
           const int slot = (kt * kKeys + 16 * kw) & (a.c.page - 1);
@@ -134,10 +136,25 @@ __global__ void __launch_bounds__(DecodeCfg<D, RG>::kThreads, DecodeCfg<D, RG>::
         }
       }
       copy_group();
-      return exps;
+      return any;
     };
+    // the queries' loads go out first, then the stream's: one latency for both
+    uint4 qw[2][kHalves][2];
+    int q_tok[2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int row = rg * 16 + g + 8 * r, packed = it.row0 + (row < it.rows ? row : 0);
+      q_tok[r] = a.token_of(packed);
+      const uint16_t* qp = a.q + static_cast<int64_t>(it.tok0 + q_tok[r]) * a.q_token +
+                           static_cast<int64_t>(it.head * a.group + packed - q_tok[r] * a.group) * D + 16 * c;
+#pragma unroll
+      for (int h = 0; h < kHalves; ++h) {
+        qw[r][h][0] = *reinterpret_cast<const uint4*>(qp + 64 * h);
+        qw[r][h][1] = *reinterpret_cast<const uint4*>(qp + 64 * h + 8);
+      }
+    }
     load_batch();
-    int pending[kS - 1];
+    bool pending[kS - 1];
 #pragma unroll
     for (int s = 0; s < kS - 1; ++s) pending[s] = copy_step(kt0 + s, s);
 
@@ -153,15 +170,13 @@ __global__ void __launch_bounds__(DecodeCfg<D, RG>::kThreads, DecodeCfg<D, RG>::
       for (int r = 0; r < 2; ++r) {
         const int row = rg * 16 + g + 8 * r;
         const bool there = row < it.rows;
-        const int packed = it.row0 + (there ? row : 0);
-        const int i = a.token_of(packed), hq = it.head * a.group + packed - i * a.group;
-        const uint16_t* qp = a.q + static_cast<int64_t>(it.tok0 + i) * a.q_token + static_cast<int64_t>(hq) * D + 16 * c;
+        const int i = q_tok[r];
         uint32_t w[kHalves][8];
         uint32_t amax = 0;
 #pragma unroll
         for (int h = 0; h < kHalves; ++h) {
-          const uint4 x = there ? *reinterpret_cast<const uint4*>(qp + 64 * h) : make_uint4(0, 0, 0, 0);
-          const uint4 y = there ? *reinterpret_cast<const uint4*>(qp + 64 * h + 8) : make_uint4(0, 0, 0, 0);
+          const uint4 x = there ? qw[r][h][0] : make_uint4(0, 0, 0, 0);
+          const uint4 y = there ? qw[r][h][1] : make_uint4(0, 0, 0, 0);
           const uint32_t v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
@@ -215,13 +230,14 @@ __global__ void __launch_bounds__(DecodeCfg<D, RG>::kThreads, DecodeCfg<D, RG>::
         __syncwarp();
       else
         named_bar_sync(1 + kw, 64);  // the two warps of the key group
-      const int exps = pending[0];
+      const bool any = pending[0];
 #pragma unroll
       for (int s = 0; s + 1 < kS - 1; ++s) pending[s] = pending[s + 1];
       pending[kS - 2] = copy_step(kt + kS - 1, stage == 0 ? kS - 1 : stage - 1);  // over the stage read last
       const uint8_t* at_k = my_ring + stage * 2 * kSide;
       stage = stage == kS - 1 ? 0 : stage + 1;
-      if (exps < 0) continue;
+      if (!any) continue;
+      const int exps = __shfl_sync(0xFFFFFFFFu, kt >= batch0 ? b_exps : b_before, (kt - batch0) & 31);
       const int ek = (exps & 255) - 64, ev = (exps >> 8) - 64;
       const int key0 = kt * kKeys + 16 * kw;
 
@@ -393,7 +409,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, RG>::kThreads, DecodeCfg<D, RG>::
       // long sequence is cut into many parts, so parts meet in groups of kFan first: the last of a group leaves the
       // group's sum in the slot of its first part.  (One sequence of 131072 positions has 76 parts a head; read by one
       // CTA they took 10 of 66 us.)
-      constexpr int kSlot = kRows * (D + 2), kFan = 9;
+      constexpr int kSlot = kRows * (D + 2), kFan = 9, kAtOnce = 5;  // (a full group's loads in two goes)
       const int c0 = owner_of(it.ub, scan), c1 = owner_of(it.ue - 1, scan), me = blockIdx.x;
       auto slot_of = [&](int k) { return a.partial + (static_cast<int64_t>(k) * 2 + (k == c0 ? 1 : 0)) * kSlot; };
       auto leave = [&](int k) {
@@ -406,38 +422,52 @@ __global__ void __launch_bounds__(DecodeCfg<D, RG>::kThreads, DecodeCfg<D, RG>::
       };
       // Arrives; true for the last of n, which then sees what the others left.
       auto last_of = [&](unsigned int* ticket, int n) {
-        __threadfence();
-        __syncthreads();
+        __syncthreads();  // (the release below covers what the barrier made this thread see)
         if (threadIdx.x == 0) {
-          const bool last = atomicAdd(ticket, 1u) == static_cast<unsigned int>(n - 1);
+          const bool last = add_acq_rel(ticket, 1u) == static_cast<unsigned int>(n - 1);
           if (last) *ticket = 0;
           flags[1] = last;
         }
         __syncthreads();
-        const bool last = flags[1] != 0;
-        if (last) __threadfence();
-        return last;
+        return flags[1] != 0;
       };
       auto add_up = [&](int first, int step, int end) {  // the slots of first, first + step, ... before end
         if (row >= it.rows) return;
         mm = kNoMax;
-        for (int k = first; k < end; k += step) mm = fmaxf(mm, __ldcg(slot_of(k) + kRows * D + 2 * row));
         ll = 0.0f;
 #pragma unroll
         for (int e = 0; e < kChunks; ++e) acc[e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 3
-        for (int k = first; k < end; k += step) {
-          const float* p = slot_of(k);
-          const float2 x = __ldcg(reinterpret_cast<const float2*>(p + kRows * D + 2 * row));
-          const float f = ex2(x.x - mm);
-          ll = fmaf(x.y, f, ll);
+        for (int k0 = first; k0 < end; k0 += kAtOnce * step) {
+          float2 x[kAtOnce];
+          float4 v[kAtOnce][kChunks];
 #pragma unroll
-          for (int e = 0; e < kChunks; ++e) {
-            const float4 v = __ldcg(reinterpret_cast<const float4*>(p + row * D + 4 * (part + 8 * e)));
-            acc[e].x = fmaf(v.x, f, acc[e].x);
-            acc[e].y = fmaf(v.y, f, acc[e].y);
-            acc[e].z = fmaf(v.z, f, acc[e].z);
-            acc[e].w = fmaf(v.w, f, acc[e].w);
+          for (int j = 0; j < kAtOnce; ++j) {
+            const float* p = slot_of(min(k0 + j * step, end - 1 - (end - 1 - first) % step));
+            x[j] = __ldcg(reinterpret_cast<const float2*>(p + kRows * D + 2 * row));
+#pragma unroll
+            for (int e = 0; e < kChunks; ++e) v[j][e] = __ldcg(reinterpret_cast<const float4*>(p + row * D + 4 * (part + 8 * e)));
+          }
+          float m1 = mm;
+#pragma unroll
+          for (int j = 0; j < kAtOnce; ++j)
+            if (k0 + j * step < end) m1 = fmaxf(m1, x[j].x);
+          const float keep = ex2(mm - m1);
+          mm = m1;
+          ll *= keep;
+#pragma unroll
+          for (int e = 0; e < kChunks; ++e) acc[e] = make_float4(acc[e].x * keep, acc[e].y * keep, acc[e].z * keep, acc[e].w * keep);
+#pragma unroll
+          for (int j = 0; j < kAtOnce; ++j) {
+            if (k0 + j * step >= end) continue;
+            const float f = ex2(x[j].x - mm);
+            ll = fmaf(x[j].y, f, ll);
+#pragma unroll
+            for (int e = 0; e < kChunks; ++e) {
+              acc[e].x = fmaf(v[j][e].x, f, acc[e].x);
+              acc[e].y = fmaf(v[j][e].y, f, acc[e].y);
+              acc[e].z = fmaf(v[j][e].z, f, acc[e].z);
+              acc[e].w = fmaf(v[j][e].w, f, acc[e].w);
+            }
           }
         }
       };

@@ -398,10 +398,9 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1) prefill_kernel(con
       if (lane == 0) mbar_arrive(ofree);
       if (!whole) {
         const int c0 = owner_of(it.ub, scan), c1 = owner_of(it.ue - 1, scan);
-        __threadfence();
         named_bar_sync(1, 256);
         if (threadIdx.x == 0) {
-          const bool last = atomicAdd(a.tickets + c0, 1u) == static_cast<unsigned int>(c1 - c0);
+          const bool last = add_acq_rel(a.tickets + c0, 1u) == static_cast<unsigned int>(c1 - c0);
           if (last) a.tickets[c0] = 0;
           flags[1] = last;
           flags[2] = *abort_flag;  // (one reading for all warps: they leave together)
@@ -409,7 +408,6 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1) prefill_kernel(con
         named_bar_sync(1, 256);
         if (flags[2]) break;
         if (flags[1] && active) {
-          __threadfence();
           auto part = [&](int k) { return a.partial + (static_cast<int64_t>(k) * 2 + (k == c0 ? 1 : 0)) * kSlot; };
           float mm = kNoMax, ll = 0.0f;
           for (int k = c0; k <= c1; ++k) mm = fmaxf(mm, __ldcg(part(k) + kRows * D + 2 * row));

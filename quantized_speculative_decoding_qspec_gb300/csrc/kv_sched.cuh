@@ -62,6 +62,12 @@ __device__ __forceinline__ int key_tiles(int lo, int hi) {
   return max((hi + kKeys - 1) / kKeys - lo / kKeys, 1);
 }
 
+// n / d of non-negative numbers; the 64-bit division, some hundreds of cycles, only where the numbers need it.
+__device__ __forceinline__ long long quotient(long long n, long long d) {
+  if (((n | d) >> 32) == 0) return static_cast<uint32_t>(n) / static_cast<uint32_t>(d);
+  return n / d;
+}
+
 // Sequences in shared memory: seq[b] = {first new token, cache length, or -1 for one that is left out}, b <= B.
 template <int kRows, int kKeys>
 struct Walk {
@@ -119,7 +125,7 @@ struct Walk {
       nk = key_tiles<kKeys>(it.lo, it.hi);
     }
     const long long r = u - first;
-    it.head = static_cast<int>(r / nk);
+    it.head = static_cast<int>(quotient(r, nk));
     it.ub = first + static_cast<long long>(it.head) * nk;
     it.ue = it.ub + nk;
     const int base = it.lo / kKeys;
@@ -172,13 +178,13 @@ __device__ __forceinline__ void share_out(const AttArgs& a, int2* seq, ScanShare
   w.window = a.window;
   w.tree = a.tree != nullptr;
   // (sequence, row tile) pairs, a run of them per thread; sequences of fewer tiles leave gaps
-  const long long pairs = static_cast<long long>(B) * a.max_tiles;
-  const int per = static_cast<int>((pairs + kThreads - 1) / kThreads);
-  const long long e0 = static_cast<long long>(threadIdx.x) * per, e1 = e0 + per < pairs ? e0 + per : pairs;
-  int b = e0 < pairs ? static_cast<int>(e0 / a.max_tiles) : 0, tile = static_cast<int>(e0 - static_cast<long long>(b) * a.max_tiles);
+  const uint32_t pairs = static_cast<uint32_t>(B) * a.max_tiles;  // (below 2^30)
+  const uint32_t per = (pairs + kThreads - 1) / kThreads;
+  const uint32_t e0 = threadIdx.x * per, e1 = min(e0 + per, pairs);
+  int b = e0 < pairs ? e0 / static_cast<uint32_t>(a.max_tiles) : 0, tile = e0 - b * a.max_tiles;
   const int b_first = b, tile_first = tile;
   long long mine = 0;
-  for (long long e = e0; e < e1; ++e) {
+  for (uint32_t e = e0; e < e1; ++e) {
     mine += w.units(b, tile);
     if (++tile == a.max_tiles) {
       tile = 0;
@@ -201,8 +207,8 @@ __device__ __forceinline__ void share_out(const AttArgs& a, int2* seq, ScanShare
   }
   // as many runs as CTAs, none of them empty; CTAs beyond the last run have no work
   const long long runs = total < gridDim.x ? total : gridDim.x, c = blockIdx.x;
-  w.u = c < runs ? c * total / runs : 0;
-  w.u1 = c < runs ? (c + 1) * total / runs : 0;
+  w.u = c < runs ? quotient(c * total, runs) : 0;
+  w.u1 = c < runs ? quotient((c + 1) * total, runs) : 0;
   if (w.u < w.u1 && w.u >= before && w.u < before + mine) {  // (one thread)
     b = b_first;
     tile = tile_first;
@@ -225,7 +231,15 @@ __device__ __forceinline__ void share_out(const AttArgs& a, int2* seq, ScanShare
 
 // The run that holds unit u.
 __device__ __forceinline__ int owner_of(long long u, const ScanShared* sh) {
-  return static_cast<int>(((u + 1) * sh->runs - 1) / sh->total);
+  return static_cast<int>(quotient((u + 1) * sh->runs - 1, sh->total));
+}
+
+// Adds to a counter that other CTAs share: what this CTA wrote (or saw through a barrier) before is visible to whoever
+// reads the sum, and what earlier adders had written is visible afterwards.
+__device__ __forceinline__ unsigned int add_acq_rel(unsigned int* p, unsigned int v) {
+  unsigned int old;
+  asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], %2;" : "=r"(old) : "l"(p), "r"(v) : "memory");
+  return old;
 }
 
 __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatile int* abort_flag, unsigned int* err) {

@@ -5,8 +5,10 @@
 // written once (2 + 2 bytes, and a mask bit), which bounds it.  A block owns a range of the vocabulary of one
 // sequence for all its rows: it counts the history's tokens of that range in shared memory (integer
 // atomics, so the order does not matter; history and bias list come from L2 once per range), and every
-// thread then walks the rows of its 8 tokens, adding the draft tokens in registers as it goes.  Logits that
-// nothing touches keep their bits.
+// thread then walks the rows of its 8 tokens, adding the draft tokens in registers as it goes.  Few tokens
+// are touched but most warps have some, so the arithmetic runs only for those of the 8 places that some
+// lane of the warp needs, with what history and bias do to a token worked out once for all rows.  Logits
+// that nothing touches keep their bits.
 #include "kv_internal.h"
 
 namespace qspec {
@@ -31,22 +33,35 @@ struct LogitsArgs {
   int rows, V, n_bias, range;  // range: tokens per block
 };
 
+// What a token's history and bias do to its logit: z > 0 ? z * up : z * down where it was seen, then - sub.
 struct Penalty {
-  float rep, freq, pres;
+  float rep, inv, freq, pres;
+  __device__ float sub(uint32_t count, float bias) const {
+    const uint32_t c = count & ~kSeen;
+    return (c ? fmaf(freq, static_cast<float>(c), pres) : 0.0f) - bias;
+  }
+  __device__ float adjust(float z, bool seen, float sub) const {
+    if (seen) z *= z > 0.0f ? inv : rep;
+    return z - sub;
+  }
 };
 
-__device__ __forceinline__ float adjust(float z, uint32_t count, float bias, const Penalty& p) {
-  if (count & kSeen) z = z > 0.0f ? z / p.rep : z * p.rep;
-  const uint32_t c = count & ~kSeen;
-  if (c) z -= p.freq * static_cast<float>(c) + p.pres;
-  return z + bias;
+// Bits 0 .. 7 of `bits` -> masks of the halves of four words of two logits each.
+__device__ __forceinline__ void spread(uint32_t bits, uint32_t (&m)[4]) {
+#pragma unroll
+  for (int n = 0; n < 2; ++n) {
+    const uint32_t x = (bits >> (4 * n) & 15u) * (0x00204081u << 7) & 0x80808080u;  // bit k to the top of byte k
+    asm("prmt.b32 %0, %1, 0, 0x9988;" : "=r"(m[2 * n]) : "r"(x));                // which fills its half
+    asm("prmt.b32 %0, %1, 0, 0xBBAA;" : "=r"(m[2 * n + 1]) : "r"(x));
+  }
 }
+__device__ __forceinline__ uint32_t choose(uint32_t m, uint32_t x, uint32_t y) { return (x & m) | (y & ~m); }
 
-// kVec tokens per thread and step: 8 (V a multiple of 8, 16-byte accesses) or 1.
+// kVec tokens per thread and step: 8 (V a multiple of 8, 16-byte accesses, four rows' loads at once) or 1.
 template <int kVec>
-__global__ void __launch_bounds__(kThreads) logits_kernel(const LogitsArgs a) {
-  extern __shared__ uint32_t count[];  // [range] kSeen | occurrences, then [range] 1 + bias entry
-  uint32_t* entry = count + a.range;
+__global__ void __launch_bounds__(kThreads, 4) logits_kernel(const LogitsArgs a) {
+  extern __shared__ __align__(16) uint32_t count[];  // [range] kSeen | occurrences; [range] 16-bit 1 + bias entry
+  uint16_t* entry = reinterpret_cast<uint16_t*>(count + a.range);
   __shared__ int32_t sdraft[QSPEC_MAX_GAMMA];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -55,23 +70,22 @@ __global__ void __launch_bounds__(kThreads) logits_kernel(const LogitsArgs a) {
   const int nv = min(a.V - v0, a.range);
   bool bad = false;
 
-  for (int i = threadIdx.x; i < nv; i += kThreads) {
-    count[i] = 0;
-    if (a.n_bias) entry[i] = 0;
-  }
+  const int words = a.range / 4 + (a.n_bias ? a.range / 8 : 0);  // of 16 bytes
+  for (int i = threadIdx.x; i < words; i += kThreads) reinterpret_cast<uint4*>(count)[i] = make_uint4(0, 0, 0, 0);
   const int n_draft = a.draft ? a.rows - 1 : 0;
   if (threadIdx.x < n_draft) {
     const int32_t t = a.draft[static_cast<int64_t>(b) * n_draft + threadIdx.x];
     bad |= t < 0 || t >= a.V;
     sdraft[threadIdx.x] = t;
   }
-  Penalty p{1.0f, 0.0f, 0.0f};
+  Penalty p{1.0f, 1.0f, 0.0f, 0.0f};
   if (a.pen) {
-    p = Penalty{a.pen[3 * b], a.pen[3 * b + 1], a.pen[3 * b + 2]};
+    p = Penalty{a.pen[3 * b], 1.0f, a.pen[3 * b + 1], a.pen[3 * b + 2]};
     if (!(p.rep > 0.0f)) {
       bad = true;
       p.rep = 1.0f;
     }
+    p.inv = 1.0f / p.rep;
   }
   __syncthreads();
   if (a.hist && a.pen) {
@@ -79,85 +93,153 @@ __global__ void __launch_bounds__(kThreads) logits_kernel(const LogitsArgs a) {
     bad |= len < 0 || len > a.hist_stride || prompt < 0 || prompt > len;
     len = static_cast<int>(min(static_cast<int64_t>(max(len, 0)), a.hist_stride));
     const int32_t* h = a.hist + static_cast<int64_t>(b) * a.hist_stride;
-    auto add = [&](int i, int32_t t) {
-      bad |= t < 0 || t >= a.V;
-      const uint32_t at = static_cast<uint32_t>(t) - static_cast<uint32_t>(v0);
-      if (at < static_cast<uint32_t>(nv)) {
-        atomicOr(count + at, kSeen);
-        if (i >= prompt) atomicAdd(count + at, 1u);
+    constexpr int kAtOnce = 8;
+    for (int i0 = threadIdx.x; i0 < len; i0 += kAtOnce * kThreads) {
+      int32_t t[kAtOnce];
+#pragma unroll
+      for (int k = 0; k < kAtOnce; ++k) t[k] = i0 + k * kThreads < len ? h[i0 + k * kThreads] : v0 + nv;  // (of another block)
+#pragma unroll
+      for (int k = 0; k < kAtOnce; ++k) {
+        const int i = i0 + k * kThreads;
+        bad |= i < len && (t[k] < 0 || t[k] >= a.V);
+        const uint32_t at = static_cast<uint32_t>(t[k]) - static_cast<uint32_t>(v0);
+        if (at < static_cast<uint32_t>(nv)) {
+          atomicOr(count + at, kSeen);
+          if (i >= prompt) atomicAdd(count + at, 1u);
+        }
       }
-    };
-    int i = threadIdx.x;
-    for (; i + 3 * kThreads < len; i += 4 * kThreads) {
-      const int32_t t0 = h[i], t1 = h[i + kThreads], t2 = h[i + 2 * kThreads], t3 = h[i + 3 * kThreads];
-      add(i, t0);
-      add(i + kThreads, t1);
-      add(i + 2 * kThreads, t2);
-      add(i + 3 * kThreads, t3);
     }
-    for (; i < len; i += kThreads) add(i, h[i]);
   }
   const float* bias = a.bias + static_cast<int64_t>(b) * a.n_bias;
   for (int i = threadIdx.x; i < a.n_bias; i += kThreads) {
     const int32_t t = a.bias_ids[static_cast<int64_t>(b) * a.n_bias + i];
     bad |= t >= a.V;
     const uint32_t at = static_cast<uint32_t>(t) - static_cast<uint32_t>(v0);
-    if (t >= 0 && at < static_cast<uint32_t>(nv)) atomicMax(entry + at, static_cast<uint32_t>(i) + 1u);
+    if (t >= 0 && at < static_cast<uint32_t>(nv)) {  // the last entry of an id counts
+      uint32_t* word = reinterpret_cast<uint32_t*>(entry) + (at >> 1);
+      const uint32_t shift = 16 * (at & 1u);
+      uint32_t old = *word, seen;
+      do {
+        seen = old;
+        if ((seen >> shift & 0xFFFFu) >= static_cast<uint32_t>(i) + 1u) break;
+        old = atomicCAS(word, seen, (seen & ~(0xFFFFu << shift)) | (static_cast<uint32_t>(i) + 1u) << shift);
+      } while (old != seen);
+    }
   }
   if (bad && blockIdx.x == 0) atomicOr(a.err, kErrInvalid);  // (every block of the sequence sees the same lists)
   __syncthreads();
 
-  const int words = (a.V + 31) / 32;
-  const bool pen = a.pen != nullptr;
-  for (int i = threadIdx.x * kVec; i < nv; i += kThreads * kVec) {
-    uint32_t c[kVec];
-    float bs[kVec];
-    bool touched = false;
+  const int mask_words = (a.V + 31) / 32;
+  uint32_t drafted = 0;  // bit r: row r is the first to count a draft token of this block's range
+  if (a.pen)
+    for (int r = 1; r <= n_draft; ++r)
+      if (static_cast<uint32_t>(sdraft[r - 1]) - static_cast<uint32_t>(v0) < static_cast<uint32_t>(nv)) drafted |= 1u << r;
+  const int64_t row0 = static_cast<int64_t>(b) * a.rows;
+  if (kVec == 8) {
+    for (int i0 = (threadIdx.x & ~31) * 8; i0 < nv; i0 += kThreads * 8) {  // 256 tokens of a warp
+      const int lane = threadIdx.x & 31, i = i0 + 8 * lane;
+      const bool in = i < nv;
+      uint32_t seen = 0, touched = 0;  // bit e: token i + e
+      float sub[8];
+      auto bias_of = [&](int e) {
+        const uint32_t at = a.n_bias ? entry[i + e] : 0u;
+        return at ? bias[at - 1] : 0.0f;
+      };
 #pragma unroll
-    for (int e = 0; e < kVec; ++e) {
-      c[e] = count[i + e];
-      const uint32_t at = a.n_bias ? entry[i + e] : 0u;
-      bs[e] = at ? bias[at - 1] : 0.0f;
-      touched |= c[e] != 0 || at != 0;
-    }
-    const int64_t row0 = static_cast<int64_t>(b) * a.rows;
-    for (int r = 0; r < a.rows; ++r) {
-      if (pen && r > 0 && r <= n_draft) {
-        const uint32_t at = static_cast<uint32_t>(sdraft[r - 1]) - static_cast<uint32_t>(v0 + i);
-        if (at < kVec) {
-          touched = true;
+      for (int e = 0; e < 8; ++e) sub[e] = 0.0f;
+      if (in) {
+        const uint4 lo = *reinterpret_cast<const uint4*>(count + i), hi = *reinterpret_cast<const uint4*>(count + i + 4);
+        const uint4 w = a.n_bias ? *reinterpret_cast<const uint4*>(entry + i) : make_uint4(0, 0, 0, 0);
+        const uint32_t c[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w}, at[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-          for (int e = 0; e < kVec; ++e)
-            if (at == e) c[e] = (c[e] | kSeen) + 1u;
-        }
-      }
-      const int64_t off = (row0 + r) * a.V + v0 + i;
-      uint32_t allowed = 0xFFu;
-      if (a.mask) {
-        const uint8_t* m = reinterpret_cast<const uint8_t*>(a.mask + (row0 + r) * words);
-        allowed = kVec == 8 ? m[(v0 + i) >> 3] : (m[(v0 + i) >> 3] >> ((v0 + i) & 7)) & 1u;
-      }
-      if (kVec == 8) {
-        uint4 w = *reinterpret_cast<const uint4*>(a.logits + off);
-        uint32_t* u = reinterpret_cast<uint32_t*>(&w);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          if (touched) {
-            const int l = 2 * e, h = l + 1;
-            if (c[l] || bs[l] != 0.0f)
-              u[e] = (u[e] & 0xFFFF0000u) | f32_to_bf16_bits(adjust(bf16_lo(u[e]), c[l], bs[l], p));
-            if (c[h] || bs[h] != 0.0f)
-              u[e] = (u[e] & 0xFFFFu) | static_cast<uint32_t>(f32_to_bf16_bits(adjust(bf16_hi(u[e]), c[h], bs[h], p))) << 16;
+        for (int e = 0; e < 8; ++e) {
+          if (c[e]) seen |= 1u << e;
+          if (c[e] || (at[e / 2] >> (16 * (e & 1)) & 0xFFFFu)) {
+            touched |= 1u << e;
+            sub[e] = p.sub(c[e], bias_of(e));
           }
-          if (!(allowed >> (2 * e) & 1u)) u[e] = (u[e] & 0xFFFF0000u) | 0xFF80u;
-          if (!(allowed >> (2 * e + 1) & 1u)) u[e] = (u[e] & 0xFFFFu) | 0xFF800000u;
         }
-        *reinterpret_cast<uint4*>(a.out + off) = w;
-      } else {
-        uint16_t w = a.logits[off];
-        if (c[0] || bs[0] != 0.0f) w = f32_to_bf16_bits(adjust(bf16_lo(w), c[0], bs[0], p));
-        if (!(allowed & 1u)) w = 0xFF80u;
-        a.out[off] = w;
+      }
+      uint32_t any = __reduce_or_sync(0xFFFFFFFFu, touched);  // the places that some lane of the warp has touched
+      uint32_t tm[4];
+      spread(touched, tm);
+      const uint16_t* src = a.logits + row0 * a.V + v0 + i;
+      uint16_t* dst = a.out + row0 * a.V + v0 + i;
+      const uint8_t* bits = reinterpret_cast<const uint8_t*>(a.mask) + row0 * mask_words * 4 + ((v0 + i) >> 3);
+      for (int r0 = 0; r0 < a.rows; r0 += 4) {
+        uint4 w[4];
+        uint32_t allowed[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          if (in && r0 + q < a.rows) {
+            w[q] = ld_stream_v4(src + static_cast<int64_t>(r0 + q) * a.V);
+            if (a.mask) allowed[q] = bits[static_cast<int64_t>(r0 + q) * mask_words * 4];
+          }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int r = r0 + q;
+          if (r >= a.rows) break;
+          if (drafted >> r & 1u) {
+            const uint32_t at = static_cast<uint32_t>(sdraft[r - 1]) - static_cast<uint32_t>(v0 + i0);
+            if (at < 256u) {  // the row before drafted one of the warp's tokens
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                if (at == static_cast<uint32_t>(8 * lane + e)) {
+                  const uint32_t c = (count[i + e] | kSeen) + 1u;  // (the entry is this thread's)
+                  count[i + e] = c;
+                  sub[e] = p.sub(c, bias_of(e));
+                  seen |= 1u << e;
+                  touched |= 1u << e;
+                }
+              any = __reduce_or_sync(0xFFFFFFFFu, touched);
+              spread(touched, tm);
+            }
+          }
+          uint32_t u[4] = {w[q].x, w[q].y, w[q].z, w[q].w};
+          if (any) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (any >> (2 * e) & 3u) {
+                const float lo = p.adjust(bf16_lo(u[e]), seen >> (2 * e) & 1u, sub[2 * e]);
+                const float hi = p.adjust(bf16_hi(u[e]), seen >> (2 * e + 1) & 1u, sub[2 * e + 1]);
+                u[e] = choose(tm[e], pack_bf16(lo, hi), u[e]);  // (untouched ones keep their bits)
+              }
+          }
+          if (a.mask) {
+            uint32_t m[4];
+            spread(allowed[q], m);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) u[e] = choose(m[e], u[e], 0xFF80FF80u);
+          }
+          if (in) *reinterpret_cast<uint4*>(dst + static_cast<int64_t>(r) * a.V) = make_uint4(u[0], u[1], u[2], u[3]);
+        }
+      }
+    }
+  } else {
+    for (int i = threadIdx.x; i < nv; i += kThreads) {
+      uint32_t c = count[i];
+      const uint32_t at = a.n_bias ? entry[i] : 0u;
+      const float bs = at ? bias[at - 1] : 0.0f;
+      for (int r0 = 0; r0 < a.rows; r0 += 4) {
+        uint16_t w[4];
+        uint32_t allowed[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          if (r0 + q < a.rows) {
+            const int64_t row = row0 + r0 + q;
+            w[q] = a.logits[row * a.V + v0 + i];
+            allowed[q] = a.mask ? reinterpret_cast<const uint8_t*>(a.mask + row * mask_words)[(v0 + i) >> 3] >> ((v0 + i) & 7) : 1u;
+          }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int r = r0 + q;
+          if (r >= a.rows) break;
+          if ((drafted >> r & 1u) && sdraft[r - 1] == v0 + i) c = (c | kSeen) + 1u;
+          uint16_t x = w[q];
+          if (c || at) x = f32_to_bf16_bits(p.adjust(bf16_lo(x), c != 0, p.sub(c, bs)));
+          if (!(allowed[q] & 1u)) x = 0xFF80u;
+          a.out[(row0 + r) * a.V + v0 + i] = x;
+        }
       }
     }
   }
@@ -176,19 +258,24 @@ extern "C" qspec_status qspec_logits_adjust(const uint16_t* logits, int32_t B, i
   if (!logits || !out || B <= 0 || rows <= 0 || V <= 0) return QSPEC_ERR_INVALID_ARG;
   if (!hist != !hist_len || (hist && hist_stride <= 0) || (prompt_len && !hist)) return QSPEC_ERR_INVALID_ARG;
   if (!bias_ids != !bias || (bias && n_bias <= 0)) return QSPEC_ERR_INVALID_ARG;
-  if (rows > QSPEC_MAX_GAMMA + 1 || V < 2 || V > QSPEC_MAX_V || B > 65535 ||
+  if (!bias) n_bias = 0;
+  if (rows > QSPEC_MAX_GAMMA + 1 || n_bias > 65535 || V < 2 || V > QSPEC_MAX_V || B > 65535 ||
       int64_t(B) * rows * int64_t(V) >= (int64_t(1) << 40) || hist_stride > 0x7FFFFFFF)
     return QSPEC_ERR_UNSUPPORTED_SHAPE;
   if (!aligned16(logits) || !aligned16(out) || !aligned4(draft_tok) || !aligned4(hist) || !aligned4(hist_len) ||
       !aligned4(prompt_len) || !aligned4(penalties) || !aligned4(bias_ids) || !aligned4(bias) || !aligned4(mask))
     return QSPEC_ERR_MISALIGNED;
   LogitsArgs a{logits, out, draft_tok, hist, hist_len, prompt_len, penalties, bias_ids, bias, mask,
-               linear_error_word(), hist_stride, rows, V, bias ? n_bias : 0};
+               linear_error_word(), hist_stride, rows, V, n_bias};
   if (!a.err) return QSPEC_ERR_CUDA;
-  a.range = 2048;
+  // Every block reads its sequence's whole history, so ranges are as long as leaves four blocks an SM ([64, 8, 152064]
+  // with histories of 8192: 8192 tokens against 2048: ); one sequence's rows take the shortest.
+  a.range = 1024;
+  while (a.range < 4096 && static_cast<int64_t>(B) * ((V + 2 * a.range - 1) / (2 * a.range)) >= 4 * num_sms()) a.range *= 2;
   const dim3 grid((V + a.range - 1) / a.range, B);
-  const size_t smem = sizeof(uint32_t) * a.range * (a.n_bias ? 2 : 1);
+  const size_t smem = static_cast<size_t>(a.range) * (a.n_bias ? 6 : 4);  // at most 48 KB
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (V % 8 == 0) return launch_pdl(logits_kernel<8>, grid, dim3(kThreads), smem, s, a);
-  return launch_pdl(logits_kernel<1>, grid, dim3(kThreads), smem, s, a);
+  auto kernel = V % 8 == 0 ? logits_kernel<8> : logits_kernel<1>;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 8192 * 6) != cudaSuccess) return QSPEC_ERR_CUDA;
+  return launch_pdl(kernel, grid, dim3(kThreads), smem, s, a);
 }
