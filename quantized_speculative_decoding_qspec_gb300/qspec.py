@@ -32,6 +32,7 @@ _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
 _I32 = ctypes.c_int32
 _F64 = ctypes.c_double
+_bf16, _int32, _f32 = torch.bfloat16, torch.int32, torch.float32
 SIGNATURES = {
     "qspec_pack_weights": (ctypes.c_int, [_P, _I64, _I64, _P, _P, _P]),
     "qspec_linear_workspace_size": (ctypes.c_size_t, [_I64, _I64, _I64]),
@@ -107,8 +108,8 @@ def _ptr(t):
 
 
 def _stream(stream):
-    if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+    if stream is None:  # (the handle itself: a Stream object would cost more than the rest of a small call)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
@@ -429,13 +430,15 @@ def qspec_verify_tree_greedy(tgt_logits, tree_tok, tree_parent, accept_len, out_
 
 def _rows(t, heads, dim, name):
     """Pointer and token stride of a [T, heads, dim] GPU tensor whose tokens are contiguous rows."""
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim:
-        raise ValueError(f"{name} must be [T, {heads}, {dim}], got {list(t.shape)}")
-    if (dim > 1 and t.stride(2) != 1) or (heads > 1 and t.stride(1) != dim):
+    shape = t.shape
+    if len(shape) != 3 or shape[1] != heads or shape[2] != dim:
+        raise ValueError(f"{name} must be [T, {heads}, {dim}], got {list(shape)}")
+    strides = t.stride()
+    if (dim > 1 and strides[2] != 1) or (heads > 1 and strides[1] != dim):
         raise ValueError(f"the heads of a token of {name} must be contiguous")
     if not t.is_cuda:
         raise ValueError("tensor must live on the GPU")
-    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else heads * dim
+    return t.data_ptr(), strides[0] if shape[0] > 1 else heads * dim
 
 
 class RotaryPlan(ctypes.Structure):
@@ -473,27 +476,26 @@ class Rotary:
         self.turns = turns.to(device)
         self.rot, self.interleaved = int(rot), bool(interleaved)
         self.plan = RotaryPlan(_ptr(self.turns), self.rot, int(self.interleaved), self.mult, 0)
-
-    def _ref(self):
-        return ctypes.addressof(self.plan)
+        self.ref = ctypes.addressof(self.plan)
 
 
 def qspec_rotary(x, pos, rotary, out, inverse=False, stream=None):
     """Rotate x bf16 [T, heads, dim] (any token and head strides) by pos int32 [T] into out (may be x)."""
-    _dt(x, torch.bfloat16, "x"); _dt(out, torch.bfloat16, "out"); _dt(pos, torch.int32, "pos")
-    if x.dim() != 3 or out.shape != x.shape:
+    _dt(x, _bf16, "x"); _dt(out, _bf16, "out"); _dt(pos, _int32, "pos")
+    shape = x.shape
+    if len(shape) != 3 or out.shape != shape:
         raise ValueError("x and out must be [T, heads, dim]")
-    T, H, D = x.shape
-    for name, t in (("x", x), ("out", out)):
-        if not t.is_cuda:
-            raise ValueError("tensor must live on the GPU")
-        if D > 1 and t.stride(2) != 1:
-            raise ValueError(f"the values of a head of {name} must be contiguous")
+    T, H, D = shape
+    xs, os_ = x.stride(), out.stride()
+    if not (x.is_cuda and out.is_cuda):
+        raise ValueError("tensor must live on the GPU")
+    if D > 1 and (xs[2] != 1 or os_[2] != 1):
+        raise ValueError("the values of a head of x and of out must be contiguous")
     _need(pos, T, "pos")
-    xs = [x.stride(0) if T > 1 else 0, x.stride(1) if H > 1 else 0]
-    os_ = [out.stride(0) if T > 1 else 0, out.stride(1) if H > 1 else 0]
-    _check("qspec_rotary", load().qspec_rotary(x.data_ptr(), *xs, _ptr(pos), T, H, D, rotary._ref(), int(inverse),
-                                               out.data_ptr(), *os_, _stream(stream)))
+    xt, ot = (xs[0], os_[0]) if T > 1 else (0, 0)
+    xh, oh = (xs[1], os_[1]) if H > 1 else (0, 0)
+    _check("qspec_rotary", load().qspec_rotary(x.data_ptr(), xt, xh, _ptr(pos), T, H, D, rotary.ref, 1 if inverse else 0,
+                                               out.data_ptr(), ot, oh, _stream(stream)))
 
 
 class KVCacheDesc(ctypes.Structure):
@@ -523,6 +525,7 @@ class KVCache:
         _need(k_exp, n * self.heads, "k_exp"); _need(v_exp, n * self.heads, "v_exp")
         self.k, self.v, self.k_exp, self.v_exp = k, v, k_exp, v_exp
         self.desc = KVCacheDesc(_ptr(k), _ptr(v), _ptr(k_exp), _ptr(v_exp), n, self.heads, self.page, self.dim, 0)
+        self.ref = ctypes.addressof(self.desc)
 
     def values(self, which="k"):
         """The cached values as fp32 [pages, heads, page, dim] (a torch expression, for inspection)."""
@@ -554,18 +557,19 @@ class KVBatch:
         _need(cu_tok, B + 1, "cu_tok"); _need(kv_len, B, "kv_len")
         self.cu_tok, self.kv_len, self.pages = cu_tok, kv_len, pages
         self.desc = KVBatchDesc(_ptr(cu_tok), _ptr(kv_len), _ptr(pages), B, max_pages, int(max_tok), 0, 0)
+        self._address, self._T = ctypes.addressof(self.desc), 0
 
-    def _ref(self, T):
-        self.desc.T = T
-        return ctypes.addressof(self.desc)
+    def ref(self, T):
+        """Address of the descriptor for a step of T new tokens."""
+        if T != self._T:
+            self.desc.T = self._T = T
+        return self._address
 
 
 def qspec_kv_append(cache, batch, k, v, rotary=None, pos=None, q=None, q_out=None, stream=None):
     """Write the step's k and v (bf16 [T, heads, dim]) into the cache; rotate k and q [T, heads_q, dim] (into
     q_out, q itself when omitted) with a Rotary at pos int32 [T] (cache positions when omitted)."""
-    for name, t in (("k", k), ("v", v), ("q", q), ("q_out", q_out)):
-        _dt(t, torch.bfloat16, name)
-    _dt(pos, torch.int32, "pos")
+    _dt(k, _bf16, "k"); _dt(v, _bf16, "v"); _dt(q, _bf16, "q"); _dt(q_out, _bf16, "q_out"); _dt(pos, _int32, "pos")
     T = k.shape[0]
     if v.shape[0] != T or (q is not None and q.shape[0] != T):
         raise ValueError("k, v and q must have the same number of tokens")
@@ -581,9 +585,8 @@ def qspec_kv_append(cache, batch, k, v, rotary=None, pos=None, q=None, q_out=Non
         qp, qs = _rows(q, hq, cache.dim, "q")
         qop, qos = _rows(q_out, hq, cache.dim, "q_out")
     _check("qspec_kv_append",
-           load().qspec_kv_append(ctypes.addressof(cache.desc), batch._ref(T), kp, ks, vp, vs,
-                                  rotary._ref() if rotary is not None else None, _ptr(pos), qp or None, qs, hq,
-                                  qop or None, qos, _stream(stream)))
+           load().qspec_kv_append(cache.ref, batch.ref(T), kp, ks, vp, vs, rotary.ref if rotary is not None else None,
+                                  _ptr(pos), qp or None, qs, hq, qop or None, qos, _stream(stream)))
 
 
 def qspec_kv_attention_workspace_size():
@@ -598,16 +601,16 @@ def new_kv_attention_workspace(device="cuda"):
 def qspec_kv_attention(cache, batch, q, out, ws, scale=None, window=0, tree=None, lse=None, stream=None):
     """out = causal attention of q (bf16 [T, heads_q, dim]) over the cache; scale defaults to dim^-0.5, tree:
     int64 [T] words of visible new tokens, lse: fp32 [T, heads_q]."""
-    _dt(q, torch.bfloat16, "q"); _dt(out, torch.bfloat16, "out"); _dt(tree, torch.int64, "tree")
-    _dt(lse, torch.float32, "lse"); _dt(ws, torch.uint8, "ws")
-    T, hq = q.shape[0], q.shape[1]
+    _dt(q, _bf16, "q"); _dt(out, _bf16, "out"); _dt(tree, torch.int64, "tree"); _dt(lse, _f32, "lse")
+    _dt(ws, torch.uint8, "ws")
+    T, hq = q.shape[:2]
     if out.shape != q.shape:
         raise ValueError("out must have the shape of q")
     _need(tree, T, "tree"); _need(lse, T * hq, "lse")
     qp, qs = _rows(q, hq, cache.dim, "q")
     op, os_ = _rows(out, hq, cache.dim, "out")
     _check("qspec_kv_attention",
-           load().qspec_kv_attention(ctypes.addressof(cache.desc), batch._ref(T), qp, qs, hq,
+           load().qspec_kv_attention(cache.ref, batch.ref(T), qp, qs, hq,
                                      cache.dim ** -0.5 if scale is None else float(scale), int(window), _ptr(tree), op,
                                      os_, _ptr(lse), _ptr(ws), ws.numel(), _stream(stream)))
 
@@ -615,11 +618,9 @@ def qspec_kv_attention(cache, batch, q, out, ws, scale=None, window=0, tree=None
 def qspec_logits_adjust(logits, out, draft_tok=None, hist=None, hist_len=None, prompt_len=None, penalties=None,
                         bias_ids=None, bias=None, mask=None, stream=None):
     """Penalties, biases and a grammar mask on logits bf16 [B, rows, V] into out (may be logits)."""
-    _dt(logits, torch.bfloat16, "logits"); _dt(out, torch.bfloat16, "out")
-    for name, t in (("draft_tok", draft_tok), ("hist", hist), ("hist_len", hist_len), ("prompt_len", prompt_len),
-                    ("bias_ids", bias_ids), ("mask", mask)):
-        _dt(t, torch.int32, name)
-    _dt(penalties, torch.float32, "penalties"); _dt(bias, torch.float32, "bias")
+    _dt(logits, _bf16, "logits"); _dt(out, _bf16, "out"); _dt(draft_tok, _int32, "draft_tok"); _dt(hist, _int32, "hist")
+    _dt(hist_len, _int32, "hist_len"); _dt(prompt_len, _int32, "prompt_len"); _dt(bias_ids, _int32, "bias_ids")
+    _dt(mask, _int32, "mask"); _dt(penalties, _f32, "penalties"); _dt(bias, _f32, "bias")
     B, rows, V = logits.shape
     n_bias = bias_ids.shape[1] if bias_ids is not None else 0
     _need(out, B * rows * V, "out"); _need(draft_tok, B * (rows - 1), "draft_tok"); _need(hist_len, B, "hist_len")
