@@ -54,13 +54,13 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const RotaryArgs a)
   __syncthreads();
   constexpr int kChunk = kMode == kHalf ? 16 : 8;
   const int rot_items = kMode >= kAny ? half : a.rot / kChunk;
-  const unsigned int n = static_cast<unsigned int>(nt) * nh * a.items;
-  for (unsigned int e = threadIdx.x; e < n; e += kRotThreads) {
-    const unsigned int r = e / a.items, j = e - r * a.items;
-    const unsigned int t = r / nh, h = r - t * nh;
-    const uint16_t* x = a.x + (t0 + t) * a.x_token + static_cast<int64_t>(h0 + h) * a.x_head;
-    uint16_t* o = a.out + (t0 + t) * a.out_token + static_cast<int64_t>(h0 + h) * a.out_head;
-    if (kMode >= kAny) {
+  if (kMode >= kAny) {
+    const unsigned int n = static_cast<unsigned int>(nt) * nh * a.items;
+    for (unsigned int e = threadIdx.x; e < n; e += kRotThreads) {
+      const unsigned int r = e / a.items, j = e - r * a.items;
+      const unsigned int t = r / nh, h = r - t * nh;
+      const uint16_t* x = a.x + (t0 + t) * a.x_token + static_cast<int64_t>(h0 + h) * a.x_head;
+      uint16_t* o = a.out + (t0 + t) * a.out_token + static_cast<int64_t>(h0 + h) * a.out_head;
       if (j >= rot_items) {
         const int d = a.rot + (j - rot_items);
         o[d] = x[d];
@@ -70,31 +70,67 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const RotaryArgs a)
       const uint32_t w = rotate_lo_hi(x[da] | static_cast<uint32_t>(x[db]) << 16, cs[t * half + j]);
       o[da] = static_cast<uint16_t>(w);
       o[db] = static_cast<uint16_t>(w >> 16);
-    } else if (j >= rot_items) {
-      const int d = a.rot + 8 * (j - rot_items);
-      *reinterpret_cast<uint4*>(o + d) = *reinterpret_cast<const uint4*>(x + d);
-    } else if (kMode == kInter) {
-      const uint4 v = *reinterpret_cast<const uint4*>(x + 8 * j);
-      const float4* c = reinterpret_cast<const float4*>(cs + t * half + 4 * j);  // (rot / 2 is a multiple of 4)
-      const float4 c0 = c[0], c1 = c[1];
-      *reinterpret_cast<uint4*>(o + 8 * j) =
-          make_uint4(rotate_lo_hi(v.x, make_float2(c0.x, c0.y)), rotate_lo_hi(v.y, make_float2(c0.z, c0.w)),
-                     rotate_lo_hi(v.z, make_float2(c1.x, c1.y)), rotate_lo_hi(v.w, make_float2(c1.z, c1.w)));
-    } else {
-      const uint4 va = *reinterpret_cast<const uint4*>(x + 8 * j);
-      const uint4 vb = *reinterpret_cast<const uint4*>(x + half + 8 * j);
-      const uint32_t wa[4] = {va.x, va.y, va.z, va.w}, wb[4] = {vb.x, vb.y, vb.z, vb.w};
-      const float4* c = reinterpret_cast<const float4*>(cs + t * half + 8 * j);
-      uint32_t ra[4], rb[4];
+    }
+    return;
+  }
+  // A thread keeps its item j of a head and walks the (token, head) rows, `rows` of them at a time over the block;
+  // kAtOnce rows' loads are in flight before the first is rotated.
+  const int rows = kRotThreads / a.items, lane_row = threadIdx.x / a.items, j = threadIdx.x - lane_row * a.items;
+  if (lane_row >= rows) return;
+  const bool rotates = j < rot_items;
+  const int d0 = rotates ? 8 * j : a.rot + 8 * (j - rot_items), d1 = half + d0;  // (d1: kHalf)
+  const int64_t pair = kMode == kHalf && rotates ? 1 : 0;
+  constexpr int kAtOnce = kMode == kHalf ? 2 : 4;
+  int t = 0, h = lane_row;
+  while (h >= nh) {
+    h -= nh;
+    ++t;
+  }
+  while (t < nt) {
+    uint4 va[kAtOnce], vb[kAtOnce];
+    int tt[kAtOnce], hh[kAtOnce];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float4 q = c[i];
-        const float a0 = bf16_lo(wa[i]), a1 = bf16_hi(wa[i]), b0 = bf16_lo(wb[i]), b1 = bf16_hi(wb[i]);
-        ra[i] = pack_bf16(a0 * q.x - b0 * q.y, a1 * q.z - b1 * q.w);
-        rb[i] = pack_bf16(a0 * q.y + b0 * q.x, a1 * q.w + b1 * q.z);
+    for (int k = 0; k < kAtOnce; ++k) {
+      tt[k] = t;
+      hh[k] = h;
+      if (t < nt) {
+        const uint16_t* x = a.x + (t0 + t) * a.x_token + static_cast<int64_t>(h0 + h) * a.x_head;
+        va[k] = *reinterpret_cast<const uint4*>(x + d0);
+        if (pair) vb[k] = *reinterpret_cast<const uint4*>(x + d1);
       }
-      *reinterpret_cast<uint4*>(o + 8 * j) = make_uint4(ra[0], ra[1], ra[2], ra[3]);
-      *reinterpret_cast<uint4*>(o + half + 8 * j) = make_uint4(rb[0], rb[1], rb[2], rb[3]);
+      h += rows;
+      while (h >= nh) {
+        h -= nh;
+        ++t;
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) {
+      if (tt[k] >= nt) break;
+      uint16_t* o = a.out + (t0 + tt[k]) * a.out_token + static_cast<int64_t>(h0 + hh[k]) * a.out_head;
+      if (!rotates) {
+        *reinterpret_cast<uint4*>(o + d0) = va[k];
+      } else if (kMode == kInter) {
+        const float4* c = reinterpret_cast<const float4*>(cs + tt[k] * half + 4 * j);  // (rot / 2 is a multiple of 4)
+        const float4 c0 = c[0], c1 = c[1];
+        const uint4 v = va[k];
+        *reinterpret_cast<uint4*>(o + d0) =
+            make_uint4(rotate_lo_hi(v.x, make_float2(c0.x, c0.y)), rotate_lo_hi(v.y, make_float2(c0.z, c0.w)),
+                       rotate_lo_hi(v.z, make_float2(c1.x, c1.y)), rotate_lo_hi(v.w, make_float2(c1.z, c1.w)));
+      } else {
+        const uint32_t wa[4] = {va[k].x, va[k].y, va[k].z, va[k].w}, wb[4] = {vb[k].x, vb[k].y, vb[k].z, vb[k].w};
+        const float4* c = reinterpret_cast<const float4*>(cs + tt[k] * half + 8 * j);
+        uint32_t ra[4], rb[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float4 q = c[i];
+          const float a0 = bf16_lo(wa[i]), a1 = bf16_hi(wa[i]), b0 = bf16_lo(wb[i]), b1 = bf16_hi(wb[i]);
+          ra[i] = pack_bf16(a0 * q.x - b0 * q.y, a1 * q.z - b1 * q.w);
+          rb[i] = pack_bf16(a0 * q.y + b0 * q.x, a1 * q.w + b1 * q.z);
+        }
+        *reinterpret_cast<uint4*>(o + d0) = make_uint4(ra[0], ra[1], ra[2], ra[3]);
+        *reinterpret_cast<uint4*>(o + d1) = make_uint4(rb[0], rb[1], rb[2], rb[3]);
+      }
     }
   }
 }
