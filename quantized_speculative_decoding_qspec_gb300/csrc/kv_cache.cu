@@ -4,18 +4,17 @@
 // smallest e with amax <= 448 * 2^e.  Power-of-two scales make both directions exact but for the one
 // rounding to e4m3, and a page that has to grow is quantised again by an exact shift.  Each value is read
 // once (2 bytes) and its code written once (1 byte); memory bounds long appends, launch latency short
-// ones.  A block owns one side (keys or values) of one (sequence, touched page, head): it holds the page's new
-// values in registers (at most 4 items of 16), so the maximum, the rounding and the writes need one
+// ones.  A block owns one side (keys or values) of one (sequence, touched page) and up to four heads: it holds the page's new
+// values in registers (at most 8 items of 16 a thread), so the maximum, the rounding and the writes need one
 // pass over memory and no block waits for another.  Further blocks of the same launch rotate the queries
-// of the page's tokens, up to 4 heads each, with the cosines of a token computed once for them.
+// of the page's tokens, up to 8 heads each, with the cosines of a token computed once for them.
 #include "kv_internal.h"
 
 namespace qspec {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMaxItems = 4;  // 128 slots * 128 values / 16 per item / 256 threads
-constexpr int kHeadsPerQ = 4;
+constexpr int kHeadsPerQ = 8;  // in passes of 4
 
 struct AppendArgs {
   qspec_kv_cache c;
@@ -105,13 +104,15 @@ __device__ __forceinline__ int exp_of_amax(uint32_t bits) {
   return min(max(e, kKvMinExp), kKvMaxExp);
 }
 
-template <int D>
+// NI: items of a head per thread at most (page * D / 16 values over 256 threads); HB: heads of a block, whose tokens' cosines
+// are computed once for all of them.
+template <int D, int NI, int HB>
 __global__ void __launch_bounds__(kThreads) append_kernel(const AppendArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   constexpr int kPerTok = D / 16;  // items of a token and head
   const int b = blockIdx.x / a.pages_per_seq, jp = blockIdx.x - b * a.pages_per_seq;
-  const int head = blockIdx.y, role = blockIdx.z;
+  const int head0 = blockIdx.y * HB, heads = min(HB, a.c.heads - head0), role = blockIdx.z;
   const SeqSpan sp = seq_span(a.b, a.c.page, b);
   if (!sp.ok || sp.n > sp.kv) {
     if (threadIdx.x == 0) atomicOr(a.err, kErrInvalid);
@@ -128,34 +129,33 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendArgs a) {
 
   if (role >= 2) {
     // ------------------------------------------------------------------ queries
-    const int h0 = head * a.group + (role - 2) * kHeadsPerQ;
-    const int nh = min(kHeadsPerQ, a.group - (role - 2) * kHeadsPerQ);
+    const int h0 = head0 * a.group + (role - 2) * kHeadsPerQ;
+    const int nh = min(kHeadsPerQ, (head0 + heads) * a.group - h0);
     for (int i = threadIdx.x; i < n * kPerTok; i += kThreads) {
       const int t = i / kPerTok, j = i - t * kPerTok;
       int d0, d1;
       item_chunks(j, a.rot, half, d0, d1);
       const uint16_t* src = a.q + static_cast<int64_t>(tok + t) * a.q_token + static_cast<int64_t>(h0) * D;
       uint16_t* dst = a.q_out + static_cast<int64_t>(tok + t) * a.q_out_token + static_cast<int64_t>(h0) * D;
-      uint4 v[kHeadsPerQ][2];
+      float2 cs[8];
+      if (a.turns) item_angles(a, j, a.pos ? a.pos[tok + t] : first + t, cs);
+#pragma unroll 1
+      for (int g = 0; g < nh; g += 4) {
+        uint4 v[4][2];
 #pragma unroll
-      for (int h = 0; h < kHeadsPerQ; ++h)
-        if (h < nh) {
-          v[h][0] = *reinterpret_cast<const uint4*>(src + h * D + d0);
-          v[h][1] = *reinterpret_cast<const uint4*>(src + h * D + d1);
-        }
-      if (a.turns) {
-        float2 cs[8];
-        item_angles(a, j, a.pos ? a.pos[tok + t] : first + t, cs);
+        for (int h = 0; h < 4; ++h)
+          if (g + h < nh) {
+            v[h][0] = *reinterpret_cast<const uint4*>(src + (g + h) * D + d0);
+            v[h][1] = *reinterpret_cast<const uint4*>(src + (g + h) * D + d1);
+          }
 #pragma unroll
-        for (int h = 0; h < kHeadsPerQ; ++h)
-          if (h < nh) item_rotate(cs, half, a.rot, j, v[h][0], v[h][1]);
+        for (int h = 0; h < 4; ++h)
+          if (g + h < nh) {
+            if (a.turns) item_rotate(cs, half, a.rot, j, v[h][0], v[h][1]);
+            *reinterpret_cast<uint4*>(dst + (g + h) * D + d0) = v[h][0];
+            *reinterpret_cast<uint4*>(dst + (g + h) * D + d1) = v[h][1];
+          }
       }
-#pragma unroll
-      for (int h = 0; h < kHeadsPerQ; ++h)
-        if (h < nh) {
-          *reinterpret_cast<uint4*>(dst + h * D + d0) = v[h][0];
-          *reinterpret_cast<uint4*>(dst + h * D + d1) = v[h][1];
-        }
     }
     return;
   }
@@ -166,93 +166,116 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendArgs a) {
     if (threadIdx.x == 0) atomicOr(a.err, kErrInvalid);
     return;
   }
-  const int64_t ph = static_cast<int64_t>(page) * a.c.heads + head;
-  uint8_t* codes = (role == 0 ? a.c.k : a.c.v) + ph * P * D;
+  const int64_t ph = static_cast<int64_t>(page) * a.c.heads + head0;
+  uint8_t* codes = (role == 0 ? a.c.k : a.c.v) + ph * P * D;  // of the block's first head; P * D to the next
   int8_t* exp_at = (role == 0 ? a.c.k_exp : a.c.v_exp) + ph;
-  const uint16_t* src = (role == 0 ? a.k : a.v) + static_cast<int64_t>(head) * D;
+  const uint16_t* src = (role == 0 ? a.k : a.v) + static_cast<int64_t>(head0) * D;
   const int64_t stride = role == 0 ? a.k_token : a.v_token;
   const bool rotate = role == 0 && a.turns != nullptr;
   const int items = n * kPerTok;
 
-  uint4 v[kMaxItems][2];
+  uint4 v[NI][HB][2];
 #pragma unroll
-  for (int it = 0; it < kMaxItems; ++it) {
+  for (int it = 0; it < NI; ++it) {
     const int i = it * kThreads + threadIdx.x;
     if (i < items) {
       const int t = i / kPerTok, j = i - t * kPerTok;
       int d0, d1;
       item_chunks(j, a.rot, half && rotate, d0, d1);
       const uint16_t* s = src + static_cast<int64_t>(tok + t) * stride;
-      v[it][0] = *reinterpret_cast<const uint4*>(s + d0);
-      v[it][1] = *reinterpret_cast<const uint4*>(s + d1);
+#pragma unroll
+      for (int h = 0; h < HB; ++h)
+        if (h < heads) {
+          v[it][h][0] = *reinterpret_cast<const uint4*>(s + h * D + d0);
+          v[it][h][1] = *reinterpret_cast<const uint4*>(s + h * D + d1);
+        }
     }
   }
   const bool begun = first == pg * P;  // slot 0 is among the new ones
-  const int old = begun ? kKvMinExp : min(max(static_cast<int>(*exp_at), kKvMinExp), kKvMaxExp);
-  uint32_t amax = 0;
+  int old[HB];
+#pragma unroll
+  for (int h = 0; h < HB; ++h)
+    old[h] = begun || h >= heads ? kKvMinExp : min(max(static_cast<int>(exp_at[h]), kKvMinExp), kKvMaxExp);
+  uint32_t amax[HB] = {};
   bool bad = false;
 #pragma unroll
-  for (int it = 0; it < kMaxItems; ++it) {
+  for (int it = 0; it < NI; ++it) {
     const int i = it * kThreads + threadIdx.x;
     if (i < items) {
-      if (rotate) {
-        const int t = i / kPerTok, j = i - t * kPerTok;
-        float2 cs[8];
-        item_angles(a, j, a.pos ? a.pos[tok + t] : first + t, cs);
-        item_rotate(cs, half, a.rot, j, v[it][0], v[it][1]);
-      }
-      uint32_t* w = reinterpret_cast<uint32_t*>(&v[it][0]);
+      float2 cs[8];
+      const int t = i / kPerTok, j = i - t * kPerTok;
+      if (rotate) item_angles(a, j, a.pos ? a.pos[tok + t] : first + t, cs);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) amax = max(amax, amax_finite(w[e], bad));
+      for (int h = 0; h < HB; ++h)
+        if (h < heads) {
+          if (rotate) item_rotate(cs, half, a.rot, j, v[it][h][0], v[it][h][1]);
+          uint32_t* w = reinterpret_cast<uint32_t*>(&v[it][h][0]);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) amax[h] = max(amax[h], amax_finite(w[e], bad));
+        }
     }
   }
-  __shared__ uint32_t sh[kThreads / 32];
-  amax = __reduce_max_sync(0xFFFFFFFFu, amax);
-  if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = amax;
+  __shared__ uint32_t sh[HB][kThreads / 32];
+#pragma unroll
+  for (int h = 0; h < HB; ++h) {
+    amax[h] = __reduce_max_sync(0xFFFFFFFFu, amax[h]);
+    if ((threadIdx.x & 31) == 0) sh[h][threadIdx.x >> 5] = amax[h];
+  }
   if (bad) atomicOr(a.err, kErrInvalid);
   __syncthreads();
 #pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) amax = max(amax, sh[w]);
-  const int e = max(old, exp_of_amax(amax));
+  for (int h = 0; h < HB; ++h) {
+    if (h >= heads) break;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) amax[h] = max(amax[h], sh[h][w]);
+    const int e = max(old[h], exp_of_amax(amax[h]));
+    uint8_t* at_head = codes + h * P * D;
 
-  if (!begun && e > old) {  // the page grows: its other slots again
-    const float shrink = exp2_int(old - e);
-    for (int i = threadIdx.x; i < P * kPerTok; i += kThreads) {
-      const int slot = i / kPerTok + pg * P;
-      if (slot >= first && slot < last) continue;
-      uint4* at = reinterpret_cast<uint4*>(codes) + i;
-      uint4 c = *at;
-      uint32_t* w = reinterpret_cast<uint32_t*>(&c);
+    if (!begun && e > old[h]) {  // the page grows: its other slots again
+      const float shrink = exp2_int(old[h] - e);
+      for (int i = threadIdx.x; i < P * kPerTok; i += kThreads) {
+        const int slot = i / kPerTok + pg * P;
+        if (slot >= first && slot < last) continue;
+        uint4* at = reinterpret_cast<uint4*>(at_head) + i;
+        uint4 c = *at;
+        uint32_t* w = reinterpret_cast<uint32_t*>(&c);
 #pragma unroll
-      for (int m = 0; m < 4; ++m) {
-        const float2 lo = e4m3x2_to_f32(w[m] & 0xFFFFu), hi = e4m3x2_to_f32(w[m] >> 16);
-        w[m] = f32_to_e4m3x2(lo.x * shrink, lo.y * shrink) | f32_to_e4m3x2(hi.x * shrink, hi.y * shrink) << 16;
-      }
-      *at = c;
-    }
-  }
-  const float inv = exp2_int(-e);
-#pragma unroll
-  for (int it = 0; it < kMaxItems; ++it) {
-    const int i = it * kThreads + threadIdx.x;
-    if (i < items) {
-      const int t = i / kPerTok, j = i - t * kPerTok;
-      int d0, d1;
-      item_chunks(j, a.rot, half && rotate, d0, d1);
-      uint8_t* dst = codes + (first - pg * P + t) * D;
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const uint32_t* w = reinterpret_cast<const uint32_t*>(&v[it][c]);
-        uint2 o;
-        o.x = f32_to_e4m3x2(bf16_lo(w[0]) * inv, bf16_hi(w[0]) * inv) |
-              f32_to_e4m3x2(bf16_lo(w[1]) * inv, bf16_hi(w[1]) * inv) << 16;
-        o.y = f32_to_e4m3x2(bf16_lo(w[2]) * inv, bf16_hi(w[2]) * inv) |
-              f32_to_e4m3x2(bf16_lo(w[3]) * inv, bf16_hi(w[3]) * inv) << 16;
-        *reinterpret_cast<uint2*>(dst + (c == 0 ? d0 : d1)) = o;
+        for (int m = 0; m < 4; ++m) {
+          const float2 lo = e4m3x2_to_f32(w[m] & 0xFFFFu), hi = e4m3x2_to_f32(w[m] >> 16);
+          w[m] = f32_to_e4m3x2(lo.x * shrink, lo.y * shrink) | f32_to_e4m3x2(hi.x * shrink, hi.y * shrink) << 16;
+        }
+        *at = c;
       }
     }
+    const float inv = exp2_int(-e);
+#pragma unroll
+    for (int it = 0; it < NI; ++it) {
+      const int i = it * kThreads + threadIdx.x;
+      if (i < items) {
+        const int t = i / kPerTok, j = i - t * kPerTok;
+        int d0, d1;
+        item_chunks(j, a.rot, half && rotate, d0, d1);
+        uint8_t* dst = at_head + (first - pg * P + t) * D;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const uint32_t* w = reinterpret_cast<const uint32_t*>(&v[it][h][c]);
+          uint2 o;
+          o.x = f32_to_e4m3x2(bf16_lo(w[0]) * inv, bf16_hi(w[0]) * inv) |
+                f32_to_e4m3x2(bf16_lo(w[1]) * inv, bf16_hi(w[1]) * inv) << 16;
+          o.y = f32_to_e4m3x2(bf16_lo(w[2]) * inv, bf16_hi(w[2]) * inv) |
+                f32_to_e4m3x2(bf16_lo(w[3]) * inv, bf16_hi(w[3]) * inv) << 16;
+          *reinterpret_cast<uint2*>(dst + (c == 0 ? d0 : d1)) = o;
+        }
+      }
+    }
+    if (threadIdx.x == 0) exp_at[h] = static_cast<int8_t>(e);
   }
-  if (threadIdx.x == 0) *exp_at = static_cast<int8_t>(e);
+}
+
+template <int D, int NI, int HB>
+qspec_status launch_append(const AppendArgs& a, unsigned int blocks, cudaStream_t s) {
+  const dim3 grid(blocks, (a.c.heads + HB - 1) / HB, 2 + (HB * a.group + kHeadsPerQ - 1) / kHeadsPerQ);
+  return launch_pdl(append_kernel<D, NI, HB>, grid, dim3(kThreads), 0, s, a);
 }
 
 }  // namespace
@@ -293,8 +316,12 @@ extern "C" qspec_status qspec_kv_append(const qspec_kv_cache* cache, const qspec
   a.pages_per_seq = (batch->max_tok + cache->page - 2) / cache->page + 1;  // a span of max_tok tokens touches at most
   const int64_t blocks = static_cast<int64_t>(batch->B) * a.pages_per_seq;
   if (blocks > 0x7FFFFFFF) return QSPEC_ERR_UNSUPPORTED_SHAPE;
-  const dim3 grid(static_cast<unsigned int>(blocks), cache->heads, 2 + (a.group + kHeadsPerQ - 1) / kHeadsPerQ);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (cache->dim == 128) return launch_pdl(append_kernel<128>, grid, dim3(kThreads), 0, s, a);
-  return launch_pdl(append_kernel<64>, grid, dim3(kThreads), 0, s, a);
+  // Heads to a block: as many (4 at most) as 64 registers of values a thread hold; the cosines of a token are
+  // computed once for them (about 10000 tokens, 32 + 8 + 8 heads: 46 us with one head to a block, 43 with four).
+  const unsigned int n = static_cast<unsigned int>(blocks);
+  if (cache->dim == 128)
+    return cache->page == 128 ? launch_append<128, 4, 2>(a, n, s) : cache->page == 64 ? launch_append<128, 2, 4>(a, n, s)
+                                                                                      : launch_append<128, 1, 4>(a, n, s);
+  return cache->page == 128 ? launch_append<64, 2, 4>(a, n, s) : launch_append<64, 1, 4>(a, n, s);
 }
