@@ -7,7 +7,7 @@ namespace att {
 namespace {
 
 // The workspace: tickets, then two partial items per CTA.  Its layout does not depend on the call's shape.
-constexpr size_t kTicketBytes = 16384;  // two a CTA
+constexpr size_t kTicketBytes = 24576;  // three a CTA
 constexpr int kMaxGrid = 2048;
 constexpr size_t slot_bytes(int rows) { return sizeof(float) * 2 * rows * (128 + 2); }  // of a CTA, heads of 128
 

@@ -478,7 +478,8 @@ __global__ void __launch_bounds__(DecodeCfg<D, RG>::kThreads, DecodeCfg<D, RG>::
         if (done) add_up(c0, 1, c1 + 1);
       } else {
         const int first = c0 + (me - c0) / kFan * kFan, end = min(first + kFan, c1 + 1);
-        done = last_of(a.tickets + gridDim.x + first, end - first);
+        // (a run can be the first of one item and a later one of the item before: two sets of tickets)
+        done = last_of(a.tickets + (first == c0 ? 1 : 2) * gridDim.x + first, end - first);
         if (done) {
           add_up(first, 1, end);
           leave(first);

@@ -29,7 +29,7 @@ struct AttArgs {
   float* lse;
   const unsigned long long* tree;
   unsigned int* err;
-  unsigned int* tickets;  // [2][grid]
+  unsigned int* tickets;  // [3][grid]
   float* partial;         // [grid][2][rows * (D + 2)]
   int64_t q_token, out_token;
   int heads_q, group, window;

@@ -55,6 +55,24 @@ def test_attention(tok, kv, Hq, H, P, D):
     q.qspec_check_status()
 
 
+@pytest.mark.parametrize("seed", range(6))
+def test_items_cut_into_many_parts(seed):
+    """Sequences whose tiles are spread over more CTAs than meet at once, at lengths that move the cuts about; the
+    same numbers again from the same workspace."""
+    q = lib()
+    g = torch.Generator().manual_seed(100 + seed)
+    B = 4 + 2 * seed
+    kv = torch.randint(900, 1500, (B,), generator=g).tolist()
+    bt = ref.Batch(200 + seed, [2] * B, kv, 8, 64, 64)
+    qq = queries(20 + seed, bt.T, 8, 64)
+    ws = q.new_kv_attention_workspace()
+    a = run(q, bt, qq, ws=ws)
+    check(a, bt, qq)
+    for _ in range(3):
+        b = run(q, bt, qq, ws=ws)
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
 @pytest.mark.parametrize("window", [1, 2, 16, 63, 64, 65, 129, 100000])
 @pytest.mark.parametrize("tok,kv,Hq,H,P,D", [([4, 1], [200, 333], 4, 2, 16, 64), ([140], [300], 4, 1, 64, 128)])
 def test_window(tok, kv, Hq, H, P, D, window):
