@@ -144,22 +144,26 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1) prefill_kernel(con
       uint32_t amax = 0;  // of the thread's row
       if (active) {
         const uint16_t* qp = a.q + static_cast<int64_t>(it.tok0) * a.q_token + static_cast<int64_t>(it.head) * a.group * D + 8 * my_chunk;
+        int tk = a.token_of(it.row0 + warp * 32 + my_row), in_group = it.row0 + warp * 32 + my_row - tk * a.group;
 #pragma unroll 1
         for (int i0 = 0; i0 < kSteps; i0 += 8) {  // (8 loads in flight; rolled, as cold code costs its fetch)
           uint4 w[8];
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            const int r = warp * 32 + (i0 + i) * kPer + my_row, packed = it.row0 + r, tk = a.token_of(packed);
-            w[i] = r < it.rows ? *reinterpret_cast<const uint4*>(qp + tk * a.q_token + (packed - tk * a.group) * D) : make_uint4(0, 0, 0, 0);
+            const bool real = warp * 32 + (i0 + i) * kPer + my_row < it.rows;
+            w[i] = real ? *reinterpret_cast<const uint4*>(qp + tk * a.q_token + in_group * D) : make_uint4(0, 0, 0, 0);
+            in_group += kPer;
+            while (in_group >= a.group) {
+              in_group -= a.group;
+              ++tk;
+            }
           }
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const uint32_t v[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-            uint32_t top = 0;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) top = max(top, max(v[e] & 0x7FFFu, (v[e] >> 16) & 0x7FFFu));
-#pragma unroll
-            for (int off = kChunks / 2; off >= 1; off >>= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, off));
+            const uint32_t pair = __vmaxu2(__vmaxu2(v[0] & 0x7FFF7FFFu, v[1] & 0x7FFF7FFFu), __vmaxu2(v[2] & 0x7FFF7FFFu, v[3] & 0x7FFF7FFFu));
+            uint32_t top = max(pair & 0xFFFFu, pair >> 16);
+            top = __reduce_max_sync(((1u << kChunks) - 1u) << (lane / kChunks * kChunks), top);  // of the lanes of a row
             const uint32_t got = __shfl_sync(0xFFFFFFFFu, top, (lane % kPer) * kChunks);
             if (lane / kPer == i0 + i) amax = got;
             const bool bad = top >= 0x7F80u;
@@ -182,20 +186,28 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1) prefill_kernel(con
         all_hi = a.tree ? max(base, 0) : min(max(base + i0 + 1, 0), it.kv);
         all_lo = a.window > 0 ? max(base + i1 + 1 - a.window, 0) : 0;
       }
-      // Which of 16 keys from key j0 on the row sees (bit e: key j0 + e).  (What it needs is taken up anew each time:
-      // few tiles have masks.)
-      auto sees = [&](int j0, float keys) {
-        const int base = it.kv - it.n, token = a.token_of(it.row0 + (row < it.rows ? row : 0));
-        const int lim = a.tree ? it.kv : min(max(base + token + 1, 0), it.kv);
-        const int low = a.window > 0 ? max(base + token + 1 - a.window, 0) : 0;
+      // What a row sees, taken up anew for each tile with masks (few have any, and registers are short), and which of 16
+      // keys from key j0 on that is (bit e: key j0 + e).
+      struct Sight {
+        int base, lim, low;
+        unsigned long long bits;
+      };
+      auto sight = [&]() {
+        Sight v;
+        const int token = a.token_of(it.row0 + (row < it.rows ? row : 0));
+        v.base = it.kv - it.n;
+        v.lim = a.tree ? it.kv : min(max(v.base + token + 1, 0), it.kv);
+        v.low = a.window > 0 ? max(v.base + token + 1 - a.window, 0) : 0;
+        v.bits = a.tree && row < it.rows ? a.tree[it.tok0 + token] : 0ull;
+        return v;
+      };
+      auto sees = [&](const Sight& v, int j0, float keys) {
         uint32_t see = 0xFFFFu;
-        if (lim - j0 < 16) see = lim > j0 ? (1u << (lim - j0)) - 1u : 0u;
-        if (low > j0) see = low - j0 < 16 ? see & ~((1u << (low - j0)) - 1u) : 0u;
-        if (a.tree && j0 + 16 > base) {  // from base on as the tree's word says
-          const int d = j0 - base;
-          const unsigned long long bits = row < it.rows ? a.tree[it.tok0 + token] : 0ull;
-          const uint32_t word = d >= 64 ? 0u : d >= 0 ? static_cast<uint32_t>(bits >> d) : static_cast<uint32_t>(bits << -d) | ((1u << -d) - 1u);
-          see &= word;
+        if (v.lim - j0 < 16) see = v.lim > j0 ? (1u << (v.lim - j0)) - 1u : 0u;
+        if (v.low > j0) see = v.low - j0 < 16 ? see & ~((1u << (v.low - j0)) - 1u) : 0u;
+        if (a.tree && j0 + 16 > v.base) {  // from base on as the tree's word says
+          const int d = j0 - v.base;
+          see &= d >= 64 ? 0u : d >= 0 ? static_cast<uint32_t>(v.bits >> d) : static_cast<uint32_t>(v.bits << -d) | ((1u << -d) - 1u);
         }
         return keys != 0.0f ? see : 0u;
       };
@@ -252,13 +264,14 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1) prefill_kernel(con
               }
             }
           } else {
+            const Sight v = sight();
 #pragma unroll 1
             for (int g = 0; g < 8; ++g) {
               float sg[16];
               tmem_ld16(ts + g * 16, reinterpret_cast<uint32_t*>(sg));
               tmem_wait_ld();
               const float4 gv = md.group[g];
-              const uint32_t see = sees(key0 + 16 * g, gv.w);
+              const uint32_t see = sees(v, key0 + 16 * g, gv.w);
               float x = -INFINITY;
 #pragma unroll
               for (int e = 0; e < 16; ++e)
@@ -310,13 +323,14 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1) prefill_kernel(con
               if (f >= 0 && f % 16 == 15) tmem_st16(ts + f / 16 * 16, p);
             }
           } else {
+            const Sight v = sight();
 #pragma unroll 1
             for (int g = 0; g < 8; ++g) {
               float sg[16];
               tmem_ld16(ts + g * 16, reinterpret_cast<uint32_t*>(sg));
               tmem_wait_ld();
               const float4 gv = md.group[g];
-              const uint32_t see = sees(key0 + 16 * g, gv.w);
+              const uint32_t see = sees(v, key0 + 16 * g, gv.w);
               const float mg = fminf(mult * gv.x, 3e38f);
               float sum = 0.0f;
 #pragma unroll
@@ -359,17 +373,12 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1) prefill_kernel(con
         }
         __syncwarp();
       };
-      auto store_lse = [&](float mm, float ll) {
-        if (a.lse && there) {
-          const int token = a.token_of(it.row0 + row), hq = it.head * a.group + it.row0 + row - token * a.group;
-          a.lse[static_cast<int64_t>(it.tok0 + token) * a.heads_q + hq] = ll == 0.0f ? -INFINITY : (mm + log2f(ll)) * 0.693147180559945f;
-        }
-      };
       if (ok && active) {
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;
 #pragma unroll 1
         for (int c = 0; c < D; c += 32) {
           float o[32];
+          __syncwarp();
           tmem_ld32(to + c, o);
           tmem_wait_ld();
           if (whole) {
@@ -380,7 +389,7 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1) prefill_kernel(con
               for (int e = 0; e < 4; ++e) w[e] = pack_bf16(o[8 * k + 2 * e] * inv, o[8 * k + 2 * e + 1] * inv);
               *reinterpret_cast<uint4*>(chunk_at(lane, c / 8 + k)) = make_uint4(w[0], w[1], w[2], w[3]);
             }
-          } else {
+          } else if (there) {
 #pragma unroll
             for (int e = 0; e < 8; ++e)  // [channel / 4][row]: consecutive rows are consecutive addresses
               *reinterpret_cast<float4*>(slot + ((c / 4 + e) * kRows + row) * 4) = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
@@ -388,8 +397,11 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1) prefill_kernel(con
         }
         if (whole) {
           store_rows();
-          store_lse(m, l);
-        } else {
+          if (a.lse && there) {
+            const int token = a.token_of(it.row0 + row), hq = it.head * a.group + it.row0 + row - token * a.group;
+            a.lse[static_cast<int64_t>(it.tok0 + token) * a.heads_q + hq] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.693147180559945f;
+          }
+        } else if (there) {
           *reinterpret_cast<float2*>(slot + kRows * D + 2 * row) = make_float2(m, l);
         }
       }
@@ -407,41 +419,54 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1) prefill_kernel(con
         }
         named_bar_sync(1, 256);
         if (flags[2]) break;
-        if (flags[1] && active) {
-          auto part = [&](int k) { return a.partial + (static_cast<int64_t>(k) * 2 + (k == c0 ? 1 : 0)) * kSlot; };
-          float mm = kNoMax, ll = 0.0f;
-          for (int k = c0; k <= c1; ++k) mm = fmaxf(mm, __ldcg(part(k) + kRows * D + 2 * row));
-          for (int k = c0; k <= c1; ++k) {
-            const float2 x = __ldcg(reinterpret_cast<const float2*>(part(k) + kRows * D + 2 * row));
-            ll = fmaf(x.y, ex2(x.x - mm), ll);
-          }
-          const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
-#pragma unroll 1
-          for (int c = 0; c < D; c += 32) {
-            float4 acc[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) acc[e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 2
+        if (flags[1]) {
+          // all 256 threads add the parts up: `span` threads take the rows (a power of two, so that a warp reads neighbours), as
+          // many as fit share the channels of a row
+          int span = 32;
+          while (span < it.rows) span *= 2;
+          const int r = threadIdx.x & (span - 1), c_first = threadIdx.x / span, c_step = 256 / span;
+          if (r < it.rows) {
+            auto part = [&](int k) { return a.partial + (static_cast<int64_t>(k) * 2 + (k == c0 ? 1 : 0)) * kSlot; };
+            float mm = kNoMax, ll = 0.0f;
+#pragma unroll 4
+            for (int k = c0; k <= c1; ++k) mm = fmaxf(mm, __ldcg(part(k) + kRows * D + 2 * r));
+#pragma unroll 4
             for (int k = c0; k <= c1; ++k) {
-              const float* p = part(k);
-              const float f = ex2(__ldcg(p + kRows * D + 2 * row) - mm);
-#pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                const float4 v = __ldcg(reinterpret_cast<const float4*>(p + ((c / 4 + e) * kRows + row) * 4));
-                acc[e].x = fmaf(v.x, f, acc[e].x);
-                acc[e].y = fmaf(v.y, f, acc[e].y);
-                acc[e].z = fmaf(v.z, f, acc[e].z);
-                acc[e].w = fmaf(v.w, f, acc[e].w);
-              }
+              const float2 x = __ldcg(reinterpret_cast<const float2*>(part(k) + kRows * D + 2 * r));
+              ll = fmaf(x.y, ex2(x.x - mm), ll);
             }
+            const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
+            const int tk = a.token_of(it.row0 + r), hq = it.head * a.group + it.row0 + r - tk * a.group;
+            uint16_t* op = a.out + static_cast<int64_t>(it.tok0 + tk) * a.out_token + static_cast<int64_t>(hq) * D;
+            constexpr int kBatch = 4;  // of four channels
+#pragma unroll 1
+            for (int c = c_first; c < D / 4; c += kBatch * c_step) {
+              float4 acc[kBatch];
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              *reinterpret_cast<uint4*>(chunk_at(lane, c / 8 + k)) =
-                  make_uint4(pack_bf16(acc[2 * k].x * inv, acc[2 * k].y * inv), pack_bf16(acc[2 * k].z * inv, acc[2 * k].w * inv),
-                             pack_bf16(acc[2 * k + 1].x * inv, acc[2 * k + 1].y * inv), pack_bf16(acc[2 * k + 1].z * inv, acc[2 * k + 1].w * inv));
+              for (int e = 0; e < kBatch; ++e) acc[e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+              for (int k = c0; k <= c1; ++k) {
+                const float* p = part(k);
+                const float f = ex2(__ldcg(p + kRows * D + 2 * r) - mm);
+#pragma unroll
+                for (int e = 0; e < kBatch; ++e)
+                  if (c + e * c_step < D / 4) {
+                    const float4 v = __ldcg(reinterpret_cast<const float4*>(p + ((c + e * c_step) * kRows + r) * 4));
+                    acc[e].x = fmaf(v.x, f, acc[e].x);
+                    acc[e].y = fmaf(v.y, f, acc[e].y);
+                    acc[e].z = fmaf(v.z, f, acc[e].z);
+                    acc[e].w = fmaf(v.w, f, acc[e].w);
+                  }
+              }
+#pragma unroll
+              for (int e = 0; e < kBatch; ++e)
+                if (c + e * c_step < D / 4)
+                  *reinterpret_cast<uint2*>(op + 4 * (c + e * c_step)) =
+                      make_uint2(pack_bf16(acc[e].x * inv, acc[e].y * inv), pack_bf16(acc[e].z * inv, acc[e].w * inv));
+            }
+            if (a.lse && c_first == 0)
+              a.lse[static_cast<int64_t>(it.tok0 + tk) * a.heads_q + hq] = ll == 0.0f ? -INFINITY : (mm + log2f(ll)) * 0.693147180559945f;
           }
-          store_rows();
-          store_lse(mm, ll);
         }
       } else {
         // the flags are taken up again by the next item, in step

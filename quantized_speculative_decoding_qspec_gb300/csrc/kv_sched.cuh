@@ -205,7 +205,8 @@ __device__ __forceinline__ void share_out(const AttArgs& a, int2* seq, ScanShare
     if (i < warp) before += sh->warp_sum[i];
     total += sh->warp_sum[i];
   }
-  // as many runs as CTAs, none of them empty; CTAs beyond the last run have no work
+  // as many runs as CTAs, none of them empty; CTAs beyond the last run have no work.  (Runs of some tiles at least
+  // were slower: what an item costs to take up and leave is better paid by many CTAs at once.)
   const long long runs = total < gridDim.x ? total : gridDim.x, c = blockIdx.x;
   w.u = c < runs ? quotient(c * total, runs) : 0;
   w.u1 = c < runs ? quotient((c + 1) * total, runs) : 0;
