@@ -513,7 +513,7 @@ typedef struct {
  *     cu_tok  [B+1] int32, from 0 non-decreasing to at most T;  kv_len [B] int32;  pages [B, max_pages] int32
  * (all three DEVICE, 4-byte aligned; only the entries of pages that kv_len reaches are read).
  * max_tok: at least the largest number of new tokens of one sequence.  1 <= B <= QSPEC_KV_MAX_B,
- * 1 <= T < 2^31, 1 <= max_tok <= T, max_pages * page < 2^31.
+ * 1 <= T < 2^31, 1 <= max_tok <= T, max_pages * page <= 2^30.
  * A sequence whose numbers are out of range, and a page id outside [0, n_pages), touch no memory outside
  * the arrays: the call leaves the sequence out (a bad page: its tokens), and the next
  * qspec_check_status returns QSPEC_ERR_INVALID_ARG.

@@ -95,7 +95,7 @@ inline qspec_status check_kv(const qspec_kv_cache* c, const qspec_kv_batch* b) {
     return QSPEC_ERR_INVALID_ARG;
   if ((c->page != 16 && c->page != 32 && c->page != 64 && c->page != 128) || (c->dim != 64 && c->dim != 128) ||
       c->heads > 4096 || c->n_pages > 0x7FFFFFFF || b->B > QSPEC_KV_MAX_B || b->T > 0x7FFFFFFF || b->max_tok > b->T ||
-      static_cast<int64_t>(b->max_pages) * c->page > 0x7FFFFFFF)
+      static_cast<int64_t>(b->max_pages) * c->page > (int64_t(1) << 30))
     return QSPEC_ERR_UNSUPPORTED_SHAPE;
   if (!aligned16(c->k) || !aligned16(c->v) || !aligned4(b->cu_tok) || !aligned4(b->kv_len) || !aligned4(b->pages))
     return QSPEC_ERR_MISALIGNED;

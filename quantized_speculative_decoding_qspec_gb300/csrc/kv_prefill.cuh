@@ -163,7 +163,8 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1) prefill_kernel(con
             const uint32_t v[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
             const uint32_t pair = __vmaxu2(__vmaxu2(v[0] & 0x7FFF7FFFu, v[1] & 0x7FFF7FFFu), __vmaxu2(v[2] & 0x7FFF7FFFu, v[3] & 0x7FFF7FFFu));
             uint32_t top = max(pair & 0xFFFFu, pair >> 16);
-            top = __reduce_max_sync(((1u << kChunks) - 1u) << (lane / kChunks * kChunks), top);  // of the lanes of a row
+#pragma unroll
+            for (int off = kChunks / 2; off >= 1; off >>= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, off));
             const uint32_t got = __shfl_sync(0xFFFFFFFFu, top, (lane % kPer) * kChunks);
             if (lane / kPer == i0 + i) amax = got;
             const bool bad = top >= 0x7F80u;

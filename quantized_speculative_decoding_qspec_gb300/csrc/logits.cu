@@ -46,6 +46,13 @@ struct Penalty {
   }
 };
 
+// 16 bytes read once (not through the read-only path: `out` may be the same memory).
+__device__ __forceinline__ uint4 load_once(const void* p) {
+  uint4 r;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p) : "memory");
+  return r;
+}
+
 // Bits 0 .. 7 of `bits` -> masks of the halves of four words of two logits each.
 __device__ __forceinline__ void spread(uint32_t bits, uint32_t (&m)[4]) {
 #pragma unroll
@@ -172,7 +179,7 @@ __global__ void __launch_bounds__(kThreads, 4) logits_kernel(const LogitsArgs a)
 #pragma unroll
         for (int q = 0; q < 4; ++q)
           if (in && r0 + q < a.rows) {
-            w[q] = ld_stream_v4(src + static_cast<int64_t>(r0 + q) * a.V);
+            w[q] = load_once(src + static_cast<int64_t>(r0 + q) * a.V);
             if (a.mask) allowed[q] = bits[static_cast<int64_t>(r0 + q) * mask_words * 4];
           }
 #pragma unroll

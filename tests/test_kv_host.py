@@ -110,7 +110,7 @@ BAD_KV = [(dict(c=None), 1), (dict(b=None), 1), (dict(c=dict(k=None)), 1), (dict
           (dict(b=dict(reserved=1)), 1), (dict(c=dict(n_pages=0)), 1), (dict(c=dict(heads=0)), 1), (dict(b=dict(B=0)), 1),
           (dict(b=dict(T=0)), 1), (dict(b=dict(max_tok=0)), 1), (dict(b=dict(max_pages=0)), 1),
           (dict(c=dict(page=48)), 2), (dict(c=dict(dim=96)), 2), (dict(b=dict(B=1025)), 2), (dict(b=dict(max_tok=7)), 2),
-          (dict(b=dict(max_pages=1 << 25)), 2), (dict(c=dict(heads=4097)), 2),
+          (dict(b=dict(max_pages=1 << 25)), 2), (dict(b=dict(max_pages=(1 << 24) + 1)), 2), (dict(c=dict(heads=4097)), 2),
           (dict(c=dict(k=FAKE + 8)), 3), (dict(b=dict(kv_len=FAKE + 2)), 3)]
 
 
