@@ -234,10 +234,13 @@ __global__ void __launch_bounds__(DecodeCfg<D, RG>::kThreads, DecodeCfg<D, RG>::
       const bool any = pending[0];
 #pragma unroll
       for (int s = 0; s + 1 < kS - 1; ++s) pending[s] = pending[s + 1];
-      pending[kS - 2] = copy_step(kt + kS - 1, stage == 0 ? kS - 1 : stage - 1);  // over the stage read last
+      const int free_stage = stage == 0 ? kS - 1 : stage - 1;  // the stage read last
       const uint8_t* at_k = my_ring + stage * 2 * kSide;
       stage = stage == kS - 1 ? 0 : stage + 1;
-      if (!any) continue;
+      if (!any) {
+        pending[kS - 2] = copy_step(kt + kS - 1, free_stage);
+        continue;
+      }
       const int exps = __shfl_sync(0xFFFFFFFFu, kt >= batch0 ? b_exps : b_before, (kt - batch0) & 31);
       const int ek = (exps & 255) - 64, ev = (exps >> 8) - 64;
       const int key0 = kt * kKeys + 16 * kw;
@@ -263,6 +266,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, RG>::kThreads, DecodeCfg<D, RG>::
           mma_f16(sc[1][e & 1], q, b0, b1);
         }
       }
+      pending[kS - 2] = copy_step(kt + kS - 1, free_stage);  // (under the MMAs' latency)
       // ---- scores: element e of tile t is row g + 8 (e / 2), key key0 + 8 t + 2 c + (e & 1)
       float z[2][4];
       const float mk[2] = {score_mult(mult[0], ek), score_mult(mult[1], ek)};
