@@ -8,8 +8,10 @@
 // thread then walks the rows of its 8 tokens, adding the draft tokens in registers as it goes.  Few tokens
 // are touched but most warps have some, so the arithmetic runs only for those of the 8 places that some
 // lane of the warp needs, with what history and bias do to a token worked out once for all rows.  Logits
-// that nothing touches keep their bits.  [64, 8, 152064]: 59 us without penalties (5.2 TB/s), 82 with histories of
-// 8192, 300 biases and masks; listing the touched tokens and doing them after the copy, a lane each, took 105.
+// that nothing touches keep their bits.  A block asks for its rows' bytes in L2 before it counts (without lists 60 -> 55
+// us).  [64, 8, 152064]: 55 us without penalties (5.7 TB/s), 80 with histories of 8192, 300 biases and masks, where the
+// schedulers issue in 61% of the cycles and warps wait on L2 or on the arithmetic's results for the rest; listing the
+// touched tokens and doing them after the copy, a lane each, took 105, the adjustment in paired FMAs 84.
 #include "kv_internal.h"
 
 namespace qspec {
@@ -17,6 +19,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr uint32_t kSeen = 0x80000000u;
+constexpr uint32_t kEntry = 0xFFFF0000u;  // + entry of the bias list: a NaN that no bias is stored as
 
 struct LogitsArgs {
   const uint16_t* logits;
@@ -68,8 +71,8 @@ __device__ __forceinline__ uint32_t choose(uint32_t m, uint32_t x, uint32_t y) {
 // kVec tokens per thread and step: 8 (V a multiple of 8, 16-byte accesses) or 1.
 template <int kVec>
 __global__ void __launch_bounds__(kThreads, 4) logits_kernel(const LogitsArgs a) {
-  extern __shared__ __align__(16) uint32_t count[];  // [range] kSeen | occurrences; [range] 16-bit 1 + bias entry
-  uint16_t* entry = reinterpret_cast<uint16_t*>(count + a.range);
+  extern __shared__ __align__(16) uint32_t count[];  // [range] occurrences, kSeen for those of the prompt; [range] bias
+  uint32_t* biased = count + a.range;
   __shared__ int32_t sdraft[QSPEC_MAX_GAMMA];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -78,7 +81,12 @@ __global__ void __launch_bounds__(kThreads, 4) logits_kernel(const LogitsArgs a)
   const int nv = min(a.V - v0, a.range);
   bool bad = false;
 
-  const int words = a.range / 4 + (a.n_bias ? a.range / 8 : 0);  // of 16 bytes
+  // the rows come to L2 while the lists are counted (V and nv: multiples of 8)
+  if (kVec == 8 && threadIdx.x < a.rows)
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(a.logits + (static_cast<int64_t>(b) * a.rows + threadIdx.x) * a.V + v0),
+                 "r"(nv * 2)
+                 : "memory");
+  const int words = a.range / 4 * (a.n_bias ? 2 : 1);  // of 16 bytes
   for (int i = threadIdx.x; i < words; i += kThreads) reinterpret_cast<uint4*>(count)[i] = make_uint4(0, 0, 0, 0);
   const int n_draft = a.draft ? a.rows - 1 : 0;
   if (threadIdx.x < n_draft) {
@@ -106,14 +114,18 @@ __global__ void __launch_bounds__(kThreads, 4) logits_kernel(const LogitsArgs a)
       int32_t t[kAtOnce];
 #pragma unroll
       for (int k = 0; k < kAtOnce; ++k) t[k] = i0 + k * kThreads < len ? h[i0 + k * kThreads] : v0 + nv;  // (of another block)
+      if (blockIdx.x == 0) {  // (one block's check is enough)
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) bad |= i0 + k * kThreads < len && (t[k] < 0 || t[k] >= a.V);
+      }
 #pragma unroll
       for (int k = 0; k < kAtOnce; ++k) {
-        const int i = i0 + k * kThreads;
-        bad |= i < len && (t[k] < 0 || t[k] >= a.V);
         const uint32_t at = static_cast<uint32_t>(t[k]) - static_cast<uint32_t>(v0);
         if (at < static_cast<uint32_t>(nv)) {
-          atomicOr(count + at, kSeen);
-          if (i >= prompt) atomicAdd(count + at, 1u);
+          if (i0 + k * kThreads < prompt)
+            atomicOr(count + at, kSeen);
+          else
+            atomicAdd(count + at, 1u);
         }
       }
     }
@@ -123,19 +135,21 @@ __global__ void __launch_bounds__(kThreads, 4) logits_kernel(const LogitsArgs a)
     const int32_t t = a.bias_ids[static_cast<int64_t>(b) * a.n_bias + i];
     bad |= t >= a.V;
     const uint32_t at = static_cast<uint32_t>(t) - static_cast<uint32_t>(v0);
-    if (t >= 0 && at < static_cast<uint32_t>(nv)) {  // the last entry of an id counts
-      uint32_t* word = reinterpret_cast<uint32_t*>(entry) + (at >> 1);
-      const uint32_t shift = 16 * (at & 1u);
-      uint32_t old = *word, seen;
-      do {
-        seen = old;
-        if ((seen >> shift & 0xFFFFu) >= static_cast<uint32_t>(i) + 1u) break;
-        old = atomicCAS(word, seen, (seen & ~(0xFFFFu << shift)) | (static_cast<uint32_t>(i) + 1u) << shift);
-      } while (old != seen);
-    }
+    if (t >= 0 && at < static_cast<uint32_t>(nv)) atomicMax(biased + at, kEntry + i);
   }
   if (bad && blockIdx.x == 0) atomicOr(a.err, kErrInvalid);  // (every block of the sequence sees the same lists)
   __syncthreads();
+  if (a.n_bias) {  // the last entry of an id puts its bias in place
+    for (int i = threadIdx.x; i < a.n_bias; i += kThreads) {
+      const int32_t t = a.bias_ids[static_cast<int64_t>(b) * a.n_bias + i];
+      const uint32_t at = static_cast<uint32_t>(t) - static_cast<uint32_t>(v0);
+      if (t >= 0 && at < static_cast<uint32_t>(nv) && biased[at] == kEntry + i) {
+        const float x = bias[i];
+        biased[at] = x != x ? 0x7FFFFFFFu : __float_as_uint(x);
+      }
+    }
+    __syncthreads();
+  }
 
   const int mask_words = (a.V + 31) / 32;
   uint32_t drafted = 0;  // bit r: row r is the first to count a draft token of this block's range
@@ -150,21 +164,25 @@ __global__ void __launch_bounds__(kThreads, 4) logits_kernel(const LogitsArgs a)
       uint32_t seen = 0, touched = 0;  // bit e: token i + e
       float sub[8];
       auto bias_of = [&](int e) {
-        const uint32_t at = a.n_bias ? entry[i + e] : 0u;
-        return at ? bias[at - 1] : 0.0f;
+        return a.n_bias ? __uint_as_float(biased[i + e]) : 0.0f;
       };
 #pragma unroll
       for (int e = 0; e < 8; ++e) sub[e] = 0.0f;
       if (in) {
         const uint4 lo = *reinterpret_cast<const uint4*>(count + i), hi = *reinterpret_cast<const uint4*>(count + i + 4);
-        const uint4 w = a.n_bias ? *reinterpret_cast<const uint4*>(entry + i) : make_uint4(0, 0, 0, 0);
-        const uint32_t c[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w}, at[4] = {w.x, w.y, w.z, w.w};
+        uint4 blo = make_uint4(0, 0, 0, 0), bhi = blo;
+        if (a.n_bias) {
+          blo = *reinterpret_cast<const uint4*>(biased + i);
+          bhi = *reinterpret_cast<const uint4*>(biased + i + 4);
+        }
+        const uint32_t c[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+        const uint32_t bs[8] = {blo.x, blo.y, blo.z, blo.w, bhi.x, bhi.y, bhi.z, bhi.w};
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           if (c[e]) seen |= 1u << e;
-          if (c[e] || (at[e / 2] >> (16 * (e & 1)) & 0xFFFFu)) {
+          if (c[e] | bs[e]) {
             touched |= 1u << e;
-            sub[e] = p.sub(c[e], bias_of(e));
+            sub[e] = p.sub(c[e], __uint_as_float(bs[e]));
           }
         }
       }
@@ -227,8 +245,7 @@ __global__ void __launch_bounds__(kThreads, 4) logits_kernel(const LogitsArgs a)
   } else {
     for (int i = threadIdx.x; i < nv; i += kThreads) {
       uint32_t c = count[i];
-      const uint32_t at = a.n_bias ? entry[i] : 0u;
-      const float bs = at ? bias[at - 1] : 0.0f;
+      const uint32_t bs = a.n_bias ? biased[i] : 0u;
       for (int r0 = 0; r0 < a.rows; r0 += 4) {
         uint16_t w[4];
         uint32_t allowed[4];
@@ -245,7 +262,7 @@ __global__ void __launch_bounds__(kThreads, 4) logits_kernel(const LogitsArgs a)
           if (r >= a.rows) break;
           if ((drafted >> r & 1u) && sdraft[r - 1] == v0 + i) c = (c | kSeen) + 1u;
           uint16_t x = w[q];
-          if (c || at) x = f32_to_bf16_bits(p.adjust(bf16_lo(x), c != 0, p.sub(c, bs)));
+          if (c | bs) x = f32_to_bf16_bits(p.adjust(bf16_lo(x), c != 0, p.sub(c, __uint_as_float(bs))));
           if (!(allowed[q] & 1u)) x = 0xFF80u;
           a.out[(row0 + r) * a.V + v0 + i] = x;
         }
@@ -282,9 +299,8 @@ extern "C" qspec_status qspec_logits_adjust(const uint16_t* logits, int32_t B, i
   a.range = 1024;
   while (a.range < 4096 && static_cast<int64_t>(B) * ((V + 2 * a.range - 1) / (2 * a.range)) >= 4 * num_sms()) a.range *= 2;
   const dim3 grid((V + a.range - 1) / a.range, B);
-  const size_t smem = static_cast<size_t>(a.range) * (a.n_bias ? 6 : 4);  // at most 48 KB
+  const size_t smem = static_cast<size_t>(a.range) * (a.n_bias ? 8 : 4);  // at most 32 KB
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   auto kernel = V % 8 == 0 ? logits_kernel<8> : logits_kernel<1>;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 8192 * 6) != cudaSuccess) return QSPEC_ERR_CUDA;
   return launch_pdl(kernel, grid, dim3(kThreads), smem, s, a);
 }
