@@ -92,6 +92,22 @@ def test_infinities_nan_and_rows_without_a_token(V):
     assert bool((out[0, 1] == float("-inf")).all()) and bool((out[1] == float("-inf")).all())
 
 
+@pytest.mark.parametrize("V", [2048, 2049])
+def test_an_id_many_times_in_the_bias_list(V):
+    """The last of many entries of an id counts, at any place in the list, whatever values the others have."""
+    q = lib()
+    x, d = inputs(11, 2, 3, V, 30, 700, True)
+    d["bias_ids"] = d["bias_ids"] % 13 * 150                   # about 54 entries an id, in several ranges of tokens
+    special = [float("nan"), 0.0, -0.0, float("inf"), float("-inf"), 2.0 ** -149]
+    d["bias"][0, :6] = torch.tensor(special)                   # overruled ones
+    d["bias"][1, -6:] = torch.tensor(special)
+    d["bias_ids"][1, -6:] = torch.arange(6, dtype=torch.int32) * 150
+    out = run(q, x, d)
+    q.qspec_check_status()
+    check(out, x, d)
+    assert torch.equal(run(q, x, d).view(torch.int16), out.view(torch.int16))
+
+
 def test_long_history_counts():
     """Counts beyond 16 bits, from a history much longer than a block's threads."""
     q = lib()
