@@ -192,7 +192,7 @@ __global__ void __launch_bounds__(kThreads, 4) logits_kernel(const LogitsArgs a)
       const uint16_t* src = a.logits + row0 * a.V + v0 + i;
       uint16_t* dst = a.out + row0 * a.V + v0 + i;
       const uint8_t* bits = reinterpret_cast<const uint8_t*>(a.mask) + row0 * mask_words * 4 + ((v0 + i) >> 3);
-      constexpr int kAtOnce = 2;  // rows whose loads are in flight together (four: 84 us against 82 for [64, 8, 152064])
+      constexpr int kAtOnce = 2;  // rows whose loads are in flight together ([64, 8, 152064]: 80 us; one: 85, four: 87)
       for (int r0 = 0; r0 < a.rows; r0 += kAtOnce) {
         uint4 w[kAtOnce];
         uint32_t allowed[kAtOnce];
@@ -295,7 +295,8 @@ extern "C" qspec_status qspec_logits_adjust(const uint16_t* logits, int32_t B, i
                linear_error_word(), hist_stride, rows, V, n_bias};
   if (!a.err) return QSPEC_ERR_CUDA;
   // Every block reads its sequence's whole history, so ranges are as long as leaves four blocks an SM ([64, 8, 152064]
-  // with histories of 8192: tried with an earlier inner loop: 90 us with ranges of 4096, 97 with 2048, 100 with 8192); one sequence's rows take the shortest.
+  // with
+  // histories of 8192: 80 us with ranges of 4096, 81 with 8192); one sequence's rows take the shortest.
   a.range = 1024;
   while (a.range < 4096 && static_cast<int64_t>(B) * ((V + 2 * a.range - 1) / (2 * a.range)) >= 4 * num_sms()) a.range *= 2;
   const dim3 grid((V + a.range - 1) / a.range, B);
