@@ -295,8 +295,7 @@ extern "C" qspec_status qspec_logits_adjust(const uint16_t* logits, int32_t B, i
                linear_error_word(), hist_stride, rows, V, n_bias};
   if (!a.err) return QSPEC_ERR_CUDA;
   // Every block reads its sequence's whole history, so ranges are as long as leaves four blocks an SM ([64, 8, 152064]
-  // with
-  // histories of 8192: 80 us with ranges of 4096, 81 with 8192); one sequence's rows take the shortest.
+  // with histories of 8192: 80 us with ranges of 4096, 81 with 8192); one sequence's rows take the shortest.
   a.range = 1024;
   while (a.range < 4096 && static_cast<int64_t>(B) * ((V + 2 * a.range - 1) / (2 * a.range)) >= 4 * num_sms()) a.range *= 2;
   const dim3 grid((V + a.range - 1) / a.range, B);
