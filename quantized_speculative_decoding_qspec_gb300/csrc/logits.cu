@@ -105,24 +105,26 @@ __global__ void __launch_bounds__(kThreads, 4) logits_kernel(const LogitsArgs a)
   }
   __syncthreads();
   if (a.hist && a.pen) {
-    int len = a.hist_len[b], prompt = a.prompt_len ? a.prompt_len[b] : 0;
+    const int len = a.hist_len[b], prompt = a.prompt_len ? a.prompt_len[b] : 0;
     bad |= len < 0 || len > a.hist_stride || prompt < 0 || prompt > len;
-    len = static_cast<int>(min(static_cast<int64_t>(max(len, 0)), a.hist_stride));
+    // (unsigned indices: a history of almost 2^31 tokens and the 2048 of a step stay below 2^32)
+    const uint32_t n = static_cast<uint32_t>(min(static_cast<int64_t>(max(len, 0)), a.hist_stride));
+    const uint32_t n_prompt = static_cast<uint32_t>(max(prompt, 0));
     const int32_t* h = a.hist + static_cast<int64_t>(b) * a.hist_stride;
     constexpr int kAtOnce = 8;
-    for (int i0 = threadIdx.x; i0 < len; i0 += kAtOnce * kThreads) {
+    for (uint32_t i0 = threadIdx.x; i0 < n; i0 += kAtOnce * kThreads) {
       int32_t t[kAtOnce];
 #pragma unroll
-      for (int k = 0; k < kAtOnce; ++k) t[k] = i0 + k * kThreads < len ? h[i0 + k * kThreads] : v0 + nv;  // (of another block)
+      for (int k = 0; k < kAtOnce; ++k) t[k] = i0 + k * kThreads < n ? h[i0 + k * kThreads] : v0 + nv;  // (of another block)
       if (blockIdx.x == 0) {  // (one block's check is enough)
 #pragma unroll
-        for (int k = 0; k < kAtOnce; ++k) bad |= i0 + k * kThreads < len && (t[k] < 0 || t[k] >= a.V);
+        for (int k = 0; k < kAtOnce; ++k) bad |= i0 + k * kThreads < n && (t[k] < 0 || t[k] >= a.V);
       }
 #pragma unroll
       for (int k = 0; k < kAtOnce; ++k) {
         const uint32_t at = static_cast<uint32_t>(t[k]) - static_cast<uint32_t>(v0);
         if (at < static_cast<uint32_t>(nv)) {
-          if (i0 + k * kThreads < prompt)
+          if (i0 + k * kThreads < n_prompt)
             atomicOr(count + at, kSeen);
           else
             atomicAdd(count + at, 1u);
