@@ -50,6 +50,9 @@ struct Penalty {
   }
 };
 
+// A count and one draft token more.  (A count of 2^31 - 1 stays: it has no bit left, and fp32 rounds it to 2^31.)
+__device__ __forceinline__ uint32_t one_more(uint32_t count) { return (count | kSeen) == 0xFFFFFFFFu ? count | kSeen : (count | kSeen) + 1u; }
+
 // 16 bytes read once (not through the read-only path: `out` may be the same memory).
 __device__ __forceinline__ uint4 load_once(const void* p) {
   uint4 r;
@@ -214,7 +217,7 @@ __global__ void __launch_bounds__(kThreads, 4) logits_kernel(const LogitsArgs a)
 #pragma unroll
               for (int e = 0; e < 8; ++e)
                 if (at == static_cast<uint32_t>(8 * lane + e)) {
-                  const uint32_t c = (count[i + e] | kSeen) + 1u;  // (the entry is this thread's)
+                  const uint32_t c = one_more(count[i + e]);  // (the entry is this thread's)
                   count[i + e] = c;
                   sub[e] = p.sub(c, bias_of(e));
                   seen |= 1u << e;
@@ -262,7 +265,7 @@ __global__ void __launch_bounds__(kThreads, 4) logits_kernel(const LogitsArgs a)
         for (int q = 0; q < 4; ++q) {
           const int r = r0 + q;
           if (r >= a.rows) break;
-          if ((drafted >> r & 1u) && sdraft[r - 1] == v0 + i) c = (c | kSeen) + 1u;
+          if ((drafted >> r & 1u) && sdraft[r - 1] == v0 + i) c = one_more(c);
           uint16_t x = w[q];
           if (c | bs) x = f32_to_bf16_bits(p.adjust(bf16_lo(x), c != 0, p.sub(c, __uint_as_float(bs))));
           if (!(allowed[q] & 1u)) x = 0xFF80u;

@@ -40,3 +40,17 @@ def test_the_last_tokens_of_the_longest_history_count():
     z = torch.where(seen, torch.where(z > 0, z / rep, z * rep), z) - freq * c - pres * (c > 0)
     # half a bf16 step, and five fp32 roundings of values below 64
     assert bool(((out.view(V).double().cpu() - z).abs() <= 2.0 ** -8 * z.abs() + 5 * 64 * 2.0 ** -24).all())
+
+
+@pytest.mark.parametrize("V", [16, 9])
+def test_a_draft_token_on_top_of_the_largest_count(V):
+    q = lib()
+    hist = long_history().fill_(7)
+    x = torch.full((1, 2, V), 3.0, dtype=torch.bfloat16, device=DEV)
+    out = torch.empty_like(x)
+    q.qspec_logits_adjust(x, out, draft_tok=i32([[7]]), hist=hist, hist_len=i32([N]),
+                          penalties=torch.tensor([[1.0, 2.0 ** -31, 0.0]], device=DEV))
+    q.qspec_check_status()
+    want = torch.full((2, V), 3.0)
+    want[:, 7] = 2.0                                        # (2^31 - 1) / 2^31 and 1: the same in bf16
+    assert torch.equal(out[0].float().cpu(), want)
