@@ -479,6 +479,7 @@ typedef struct {
  *   x    bf16, value d of head h of token t at x[t * x_token + h * x_head + d]
  *   pos  [T] int32 device, 4-byte aligned; any value, negative ones included
  *   out  as x with its own strides; out may be x itself with the same strides, else no overlap
+ *        (no two of its rows may share memory: QSPEC_ERR_UNSUPPORTED_SHAPE; rows of x may)
  *   dim a multiple of 8, 8 <= dim <= 1024, rot <= dim; 1 <= heads <= 65535; strides non-negative multiples
  *   of 8 (QSPEC_ERR_MISALIGNED otherwise); T <= 2^31 - 1, every offset below 2^40
  */

@@ -135,6 +135,19 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const RotaryArgs a)
   }
 }
 
+// Whether two rows (token, head) of `dim` values share memory.  Tokens within a stride of heads, or heads within a
+// stride of tokens, are told apart at once; other layouts are looked at head by head.
+bool rows_overlap(int64_t T, int64_t heads, int64_t dim, int64_t token, int64_t head) {
+  if ((T > 1 && token < dim) || (heads > 1 && head < dim)) return true;
+  if (T == 1 || heads == 1 || token >= (heads - 1) * head + dim || head >= (T - 1) * token + dim) return false;
+  for (int64_t j = 1; j < heads; ++j) {  // head j of one token against head 0 of the k-th after it
+    const int64_t at = j * head, k = at / token;
+    if (k < T && at - k * token < dim) return true;
+    if (k + 1 < T && (k + 1) * token - at < dim) return true;
+  }
+  return false;
+}
+
 }  // namespace
 
 }  // namespace qspec
@@ -188,8 +201,9 @@ extern "C" qspec_status qspec_rotary(const uint16_t* x, int64_t x_token, int64_t
   const int64_t most = int64_t(1) << 40;
   if (x_token > most / T || out_token > most / T || x_head > most / heads || out_head > most / heads)
     return QSPEC_ERR_UNSUPPORTED_SHAPE;
-  if (!aligned16(x) || !aligned16(out) || !aligned4(pos) || x_token % 8 || x_head % 8 || out_token % 8 || out_head % 8)
-    return QSPEC_ERR_MISALIGNED;
+  if (x_token % 8 || x_head % 8 || out_token % 8 || out_head % 8) return QSPEC_ERR_MISALIGNED;
+  if (rows_overlap(T, heads, dim, out_token, out_head)) return QSPEC_ERR_UNSUPPORTED_SHAPE;
+  if (!aligned16(x) || !aligned16(out) || !aligned4(pos)) return QSPEC_ERR_MISALIGNED;
   RotaryArgs a{x, out, pos, plan->turns, x_token, x_head, out_token, out_head, T, heads, plan->rot};
   a.mult = plan->mult;
   a.sign = inverse ? -1.0f : 1.0f;

@@ -1,0 +1,37 @@
+"""Refusals around the edges of the rotary, cache, attention and logits calls (no GPU)."""
+import ctypes
+import itertools
+
+import pytest
+
+from quantized_speculative_decoding_qspec_gb300 import qspec as q
+
+FAKE = 1 << 20
+
+
+@pytest.fixture(scope="module")
+def lib():
+    import __graft_entry__ as g
+    g.build()
+    return q.load()
+
+
+def test_rotary_refuses_outputs_that_overlap(lib):
+    """Every layout of a few tokens and heads, against the rows' addresses.  (The positions' address is misaligned,
+    which is looked at afterwards: no call reaches a GPU.)"""
+    plan = ctypes.byref(q.RotaryPlan(FAKE, 8, 0, 1.0, 0))
+    D = 8
+
+    def call(T, H, token, head):
+        return lib.qspec_rotary(FAKE, 0, 0, FAKE + 2, T, H, D, plan, 0, FAKE, token, head, None)
+
+    seen = set()
+    for T, H, token, head in itertools.product((1, 2, 3, 5), (1, 2, 3, 4), range(0, 80, 8), range(0, 80, 8)):
+        rows = [t * token + h * head for t in range(T) for h in range(H)]
+        overlap = any(abs(a - b) < D for a, b in itertools.combinations(rows, 2))
+        assert call(T, H, token, head) == (2 if overlap else 3), (T, H, token, head)
+        seen.add(overlap)
+    assert seen == {True, False}
+    # the far ends of the accepted range
+    assert call(2 ** 31 - 1, 65535, 8 * 16, 8) == 2 and call(2 ** 20, 65535, 65535 * 8, 8) == 3
+    assert call(2 ** 20, 65535, 8, 2 ** 23) == 3 and call(2 ** 20, 65535, 8, 2 ** 23 - 8) == 2
