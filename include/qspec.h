@@ -574,7 +574,8 @@ qspec_status qspec_kv_append(const qspec_kv_cache* cache, const qspec_kv_batch* 
  *   out    bf16 as q with stride out_token; tokens beyond cu_tok[B] are not written
  *   lse    [T, heads_q] fp32 or NULL
  *   ws, ws_bytes  device workspace of >= qspec_kv_attention_workspace_size() bytes, zero-filled before
- *          its first use; it serves every shape and is left ready for the next call
+ *          its first use; it serves every shape and is left ready for the next call (after a wait that
+ *          ran out, QSPEC_ERR_TIMEOUT, too: only the outputs are void then)
  *   heads_q a multiple of the cache's heads, at most 128 times them; scale finite; token strides multiples of
  *   8 and at least heads_q * dim
  */

@@ -52,18 +52,18 @@ struct Item {
   long long ub, ue;    // units of the whole item
 };
 
-__device__ __forceinline__ void key_range(int i0, int i1, int base, int kv, bool tree, int window, int& lo, int& hi) {
+__host__ __device__ __forceinline__ void key_range(int i0, int i1, int base, int kv, bool tree, int window, int& lo, int& hi) {
   hi = tree ? kv : min(max(base + i1 + 1, 0), kv);
   lo = window > 0 ? max(base + i0 + 1 - window, 0) : 0;
   if (lo > hi) lo = hi;
 }
 template <int kKeys>
-__device__ __forceinline__ int key_tiles(int lo, int hi) {
+__host__ __device__ __forceinline__ int key_tiles(int lo, int hi) {
   return max((hi + kKeys - 1) / kKeys - lo / kKeys, 1);
 }
 
 // n / d of non-negative numbers; the 64-bit division, some hundreds of cycles, only where the numbers need it.
-__device__ __forceinline__ long long quotient(long long n, long long d) {
+__host__ __device__ __forceinline__ long long quotient(long long n, long long d) {
   if (((n | d) >> 32) == 0) return static_cast<uint32_t>(n) / static_cast<uint32_t>(d);
   return n / d;
 }
@@ -80,18 +80,18 @@ struct Walk {
   long long first;  // units before the current (sequence, tile)
   int nk;
 
-  __device__ int tiles(int b, int& n) const {
+  __host__ __device__ int tiles(int b, int& n) const {
     n = seq[b].y < 0 ? 0 : seq[b + 1].x - seq[b].x;
     return (n * group + kRows - 1) / kRows;
   }
-  __device__ void tile_range(int n, int kv, int t, int& lo, int& hi) const {
+  __host__ __device__ void tile_range(int n, int kv, int t, int& lo, int& hi) const {
     const uint32_t r0 = t * kRows, r1 = min((t + 1) * kRows, n * group) - 1;
     const int i0 = static_cast<int>(static_cast<uint64_t>(r0) * group_mul >> group_shift);
     const int i1 = static_cast<int>(static_cast<uint64_t>(r1) * group_mul >> group_shift);
     key_range(i0, i1, kv - n, kv, tree, window, lo, hi);
   }
   // Units of row tile t of sequence b (0 beyond its last).
-  __device__ long long units(int b, int t) const {
+  __host__ __device__ long long units(int b, int t) const {
     int n;
     if (t >= tiles(b, n)) return 0;
     int lo, hi;
@@ -99,7 +99,7 @@ struct Walk {
     return static_cast<long long>(key_tiles<kKeys>(lo, hi)) * heads;
   }
   // Positions the walk at a row tile that begins at unit `before` <= u.
-  __device__ void start(int b, int tile, long long before) {
+  __host__ __device__ void start(int b, int tile, long long before) {
     it.b = b;
     it.tile = tile - 1;
     first = before;
@@ -107,7 +107,7 @@ struct Walk {
     left_ = tiles(b, it.n);
   }
   // The next part of this run, or false.
-  __device__ bool next() {
+  __host__ __device__ bool next() {
     if (u >= u1) return false;
     while (nk == 0 || u >= first + static_cast<long long>(nk) * heads) {
       first += static_cast<long long>(nk) * heads;
@@ -135,6 +135,12 @@ struct Walk {
     u = end;
     return true;
   }
+  // The next item of the run [run0, run1) that run boundaries cut, or false.
+  __host__ __device__ bool next_cut(long long run0, long long run1) {
+    while (next())
+      if (it.ub < run0 || it.ue > run1) return true;
+    return false;
+  }
   int left_;  // row tiles of the current sequence
 };
 
@@ -154,6 +160,14 @@ struct ScanShared {
   long long total, before;
   int b, tile, runs;
 };
+
+// The first unit of run c, and the run that holds unit u.
+__host__ __device__ __forceinline__ long long run_start(long long c, const ScanShared* sh) {
+  return c < sh->runs ? quotient(c * sh->total, sh->runs) : sh->total;
+}
+__host__ __device__ __forceinline__ int owner_of(long long u, const ScanShared* sh) {
+  return static_cast<int>(quotient((u + 1) * sh->runs - 1, sh->total));
+}
 
 // Fills seq (all threads), shares the units out and positions the walk for this CTA.  Ends with a barrier.
 template <int kThreads, int kRows, int kKeys>
@@ -230,10 +244,6 @@ __device__ __forceinline__ void share_out(const AttArgs& a, int2* seq, ScanShare
   if (w.u < w.u1) w.start(sh->b, sh->tile, sh->before);
 }
 
-// The run that holds unit u.
-__device__ __forceinline__ int owner_of(long long u, const ScanShared* sh) {
-  return static_cast<int>(quotient((u + 1) * sh->runs - 1, sh->total));
-}
 
 // Adds to a counter that other CTAs share: what this CTA wrote (or saw through a barrier) before is visible to whoever
 // reads the sum, and what earlier adders had written is visible afterwards.
