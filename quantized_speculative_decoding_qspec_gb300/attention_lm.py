@@ -69,10 +69,15 @@ class Server:
     """B sequences decoded together: gamma drafted tokens and one verify pass an iteration.
 
     penalties: (repetition, frequency, presence) of every sequence, or None; allowed: int32 [ceil(V/32)]
-    words of the tokens that may be emitted, or None.
+    words of the tokens that may be emitted, or None.  A prompt has 1 to max_len tokens.
     """
 
     def __init__(self, model, prompts, gamma=3, max_len=256, penalties=None, allowed=None):
+        if not prompts or gamma < 1:
+            raise ValueError("at least one prompt and one drafted token a step")
+        for p in prompts:
+            if not 1 <= len(p) <= max_len:
+                raise ValueError(f"a prompt has 1 to {max_len} tokens, got {len(p)}")
         dev, B = model.device, len(prompts)
         self.model, self.B, self.gamma = model, B, gamma
         self.max_pages = -(-(max_len + gamma + 1) // model.cache.page)
