@@ -69,7 +69,8 @@ class Server:
     """B sequences decoded together: gamma drafted tokens and one verify pass an iteration.
 
     penalties: (repetition, frequency, presence) of every sequence, or None; allowed: int32 [ceil(V/32)]
-    words of the tokens that may be emitted, or None.  A prompt has 1 to max_len tokens.
+    words of the tokens that may be emitted, or None.  A prompt has 1 to max_len tokens; step() refuses once a
+    sequence has more than max_len in the cache, as its history and pages end behind one step more.
     """
 
     def __init__(self, model, prompts, gamma=3, max_len=256, penalties=None, allowed=None):
@@ -79,7 +80,8 @@ class Server:
             if not 1 <= len(p) <= max_len:
                 raise ValueError(f"a prompt has 1 to {max_len} tokens, got {len(p)}")
         dev, B = model.device, len(prompts)
-        self.model, self.B, self.gamma = model, B, gamma
+        self.model, self.B, self.gamma, self.max_len = model, B, gamma, max_len
+        self.longest = max(len(p) for p in prompts)  # cached positions of the longest sequence, at most
         self.max_pages = -(-(max_len + gamma + 1) // model.cache.page)
         if B * self.max_pages > model.cache.k.shape[0]:
             raise ValueError("the cache has too few pages")
@@ -126,6 +128,11 @@ class Server:
     def step(self):
         """One iteration; returns the emitted tokens [B, gamma + 1] (-1 behind the accepted ones)."""
         m, B, gamma = self.model, self.B, self.gamma
+        if self.longest > self.max_len:              # the bound first, the lengths only when it is reached
+            self.longest = int(self.kv_len.max())
+            if self.longest > self.max_len:
+                raise ValueError(f"a sequence has {self.longest} positions in the cache, beyond max_len {self.max_len}")
+        self.longest += gamma + 1
         base, length = self.kv_len.clone(), self.hist_len.clone()  # the last token of hist is not in the cache yet
         tokens = torch.empty(B, gamma + 1, dtype=torch.int32, device=m.device)
         tokens[:, 0] = self.hist[self.rows, (length - 1).long()]
