@@ -8,10 +8,10 @@
 //    indices of four MMAs (one 16-byte load) with the query fragments laid out to match; and 16 consecutive
 //    channels of its four keys as the n index of 16 MMAs, pairs of keys gathered by byte permutes.
 //  * Keys' scales multiply the fp32 scores.  Values' scales 2^ev go into the exponent: with
-//    z = score + ev and m = max z, P = 2^(z - m) weights the bare codes and l = sum P 2^-ev is the softmax sum,
+//    z = score + ev and m near max z, P = 2^(z - m) weights the bare codes and l = sum P 2^-ev is the softmax sum,
 //    so pages of different scales share one accumulator and fp16 rounds relative to the largest weight.
-//  * m only moves when a score exceeds it by more than 2^15 (fp16 has the room), which one vote per 16
-//    keys decides; the common step has no shuffles.
+//  * m is set 8 powers of two below the largest score and moves when a score exceeds it by more than 15 (fp16 has the
+//    room on both sides), which one vote per 16 keys decides; the common step has no shuffles.
 //  * Every warp streams its own keys: 16 of each tile of 64, three stages of 16-byte asynchronous copies that only
 //    the warp itself waits for.  A step is a chain of some 2000 cycles of latency, so the warps on an SM set the
 //    rate: 16 of them without a producer or a barrier in the loop, where a ring shared by a CTA (8 consumer
@@ -293,7 +293,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, RG>::kThreads, DecodeCfg<D, RG>::
           float top = r == 0 ? top0 : top1;
           top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
           top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-          const float m1 = fmaxf(m[r], top);
+          const float m1 = fmaxf(m[r], top - kLift);
           const float keep = ex2(m[r] - m1);
           m[r] = m1;
           l[r] *= keep;

@@ -9,7 +9,7 @@
 //    read along tokens (N-major B operand), so nothing is transposed.  Their lane mapping (two keys, opposite
 //    halves of the channels per quarter warp) keeps loads and stores free of bank conflicts.
 //  * Scales as in the decode kernel: 2^ek on the scores, 2^ev in the exponent, l = sum P 2^-ev.
-//  * m moves only when a score exceeds it by 2^15; then the row's O is rescaled in TMEM (S of a tile is
+//  * m, set 2^8 below the largest score, moves only when a score exceeds it by 2^15; then the row's O is rescaled in TMEM (S of a tile is
 //    complete only after the tile's last PV, so O is at rest).
 //  * What bounds a tile is the time from its scores to its P, about 1900 cycles, and back to the next scores
 //    (PV and S of the tile, about 1500): the other tile's products cover about 1000 of them.  A thread holds its
@@ -213,7 +213,7 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1) prefill_kernel(con
         return keys != 0.0f ? see : 0u;
       };
       float m = kNoMax, l = 0.0f;
-      bool far = false;  // a maximum of the warp's rows is so large that its rounding matters in an exponent
+      bool far = false;  // a reference of the warp's rows is so large that its rounding matters in an exponent
       if (active) {
         for (int n = 0; n < tiles; ++n) {
           const int tt = t + n;
@@ -282,7 +282,7 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1) prefill_kernel(con
             }
           }
           if (__any_sync(0xFFFFFFFFu, top > m + kSlack)) {
-            const float m1 = fmaxf(m, top);
+            const float m1 = fmaxf(m, top - kLift);
             const float keep = ex2(m - m1);
             m = m1;
             l *= keep;

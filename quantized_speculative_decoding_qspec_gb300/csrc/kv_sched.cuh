@@ -17,9 +17,12 @@ namespace qspec {
 namespace att {
 
 constexpr long long kWaitLimit = 4000000000LL;   // clock cycles (about 2 s) before a wait gives up
-constexpr float kNoMax = -3.3e38f;               // running maximum of a row that has seen nothing
-// A row's maximum stays until a score exceeds it by this many powers of two: P = 2^(z - m) <= 2^15 fits fp16.
-constexpr float kSlack = 15.0f;
+constexpr float kNoMax = -3.3e38f;               // reference of a row that has seen nothing
+// P = 2^(z - m) is fp16 for the product with the values.  A row's reference m is set kLift below its largest score and
+// stays until a score exceeds it by kSlack: P <= 2^15 fits, and a key keeps a share of the product down to 2^-33 of the
+// largest weight.  (With m at the largest score it ended at 2^-25: behind one dominant key, a million others of 2^-25.5,
+// 2% of the sum, were lost.)
+constexpr float kSlack = 15.0f, kLift = 8.0f;
 
 struct AttArgs {
   qspec_kv_cache c;
