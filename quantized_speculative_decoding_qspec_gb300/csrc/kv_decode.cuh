@@ -204,7 +204,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, RG>::kThreads, DecodeCfg<D, RG>::
           bits[r] = there ? a.tree[it.tok0 + i] : 0ull;
         } else {
           lim[r] = min(max(base + i + 1, 0), it.kv);
-          low[r] = a.window > 0 ? max(base + i + 1 - a.window, 0) : 0;
+          low[r] = window_start(base + i, a.window);
           bits[r] = 0;
         }
       }
@@ -214,7 +214,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, RG>::kThreads, DecodeCfg<D, RG>::
     {
       const int i0 = a.token_of(it.row0), i1 = a.token_of(it.row0 + it.rows - 1);
       all_hi = a.tree ? max(base, 0) : min(max(base + i0 + 1, 0), it.kv);
-      all_lo = a.window > 0 ? max(base + i1 + 1 - a.window, 0) : 0;
+      all_lo = window_start(base + i1, a.window);
     }
     __syncthreads();
     const uint4* q4 = qfrag + rg * D * 2 + lane;

@@ -185,7 +185,7 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1) prefill_kernel(con
       {
         const int i0 = a.token_of(it.row0), i1 = a.token_of(it.row0 + it.rows - 1), base = it.kv - it.n;
         all_hi = a.tree ? max(base, 0) : min(max(base + i0 + 1, 0), it.kv);
-        all_lo = a.window > 0 ? max(base + i1 + 1 - a.window, 0) : 0;
+        all_lo = window_start(base + i1, a.window);
       }
       // What a row sees, taken up anew for each tile with masks (few have any, and registers are short), and which of 16
       // keys from key j0 on that is (bit e: key j0 + e).
@@ -198,7 +198,7 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1) prefill_kernel(con
         const int token = a.token_of(it.row0 + (row < it.rows ? row : 0));
         v.base = it.kv - it.n;
         v.lim = a.tree ? it.kv : min(max(v.base + token + 1, 0), it.kv);
-        v.low = a.window > 0 ? max(v.base + token + 1 - a.window, 0) : 0;
+        v.low = window_start(v.base + token, a.window);
         v.bits = a.tree && row < it.rows ? a.tree[it.tok0 + token] : 0ull;
         return v;
       };

@@ -55,9 +55,13 @@ struct Item {
   long long ub, ue;    // units of the whole item
 };
 
+// The first position that a token at position p (below 2^30, negative before the cache) sees through a window.
+__host__ __device__ __forceinline__ int window_start(int p, int window) {
+  return window > 0 ? max(max(p + 1, 0) - window, 0) : 0;  // (p + 1 - window can leave 32 bits where p is negative)
+}
 __host__ __device__ __forceinline__ void key_range(int i0, int i1, int base, int kv, bool tree, int window, int& lo, int& hi) {
   hi = tree ? kv : min(max(base + i1 + 1, 0), kv);
-  lo = window > 0 ? max(base + i0 + 1 - window, 0) : 0;
+  lo = window_start(base + i0, window);
   if (lo > hi) lo = hi;
 }
 template <int kKeys>
