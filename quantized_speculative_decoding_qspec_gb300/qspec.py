@@ -557,13 +557,13 @@ class KVBatch:
         _need(cu_tok, B + 1, "cu_tok"); _need(kv_len, B, "kv_len")
         self.cu_tok, self.kv_len, self.pages = cu_tok, kv_len, pages
         self.desc = KVBatchDesc(_ptr(cu_tok), _ptr(kv_len), _ptr(pages), B, max_pages, int(max_tok), 0, 0)
-        self._address, self._T = ctypes.addressof(self.desc), 0
 
     def ref(self, T):
-        """Address of the descriptor for a step of T new tokens."""
-        if T != self._T:
-            self.desc.T = self._T = T
-        return self._address
+        """The descriptor for a step of T new tokens, to be passed to a call.  Each is a copy of its own: threads may use
+        one batch for steps of different sizes at once (ctypes lets go of the interpreter's lock while a call runs)."""
+        desc = KVBatchDesc.from_buffer_copy(self.desc)
+        desc.T = T
+        return ctypes.byref(desc)
 
 
 def qspec_kv_append(cache, batch, k, v, rotary=None, pos=None, q=None, q_out=None, stream=None):

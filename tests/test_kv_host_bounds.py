@@ -35,3 +35,18 @@ def test_rotary_refuses_outputs_that_overlap(lib):
     # the far ends of the accepted range
     assert call(2 ** 31 - 1, 65535, 8 * 16, 8) == 2 and call(2 ** 20, 65535, 65535 * 8, 8) == 3
     assert call(2 ** 20, 65535, 8, 2 ** 23) == 3 and call(2 ** 20, 65535, 8, 2 ** 23 - 8) == 2
+
+
+def test_steps_of_one_batch_do_not_share_their_size():
+    batch = q.KVBatch.__new__(q.KVBatch)                       # (its constructor wants tensors on a GPU)
+    batch.desc = q.KVBatchDesc(FAKE, FAKE, FAKE, 2, 4, 3, 0, 0)
+    batch._address, batch._T = ctypes.addressof(batch.desc), 0
+
+    def read(r):
+        d = ctypes.cast(r, ctypes.POINTER(q.KVBatchDesc)).contents
+        return d.T, d.max_tok, d.B
+
+    five, nine = batch.ref(5), batch.ref(9)
+    assert read(five) == (5, 3, 2) and read(nine) == (9, 3, 2)
+    batch.desc.max_tok = 7                                     # what is written into the batch's own descriptor counts
+    assert read(batch.ref(9)) == (9, 7, 2) and read(nine) == (9, 3, 2)
