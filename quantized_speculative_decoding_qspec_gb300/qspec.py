@@ -131,6 +131,14 @@ def _need(t, n, name):
         raise ValueError(f"{name} holds {t.numel()} elements, the call needs {n}")
 
 
+def _arg32(x, name):
+    """x as the 32-bit argument that it becomes (ctypes would cut it down silently)."""
+    x = int(x)
+    if not -2 ** 31 <= x < 2 ** 31:
+        raise ValueError(f"{name} does not fit 32 bits: {x}")
+    return x
+
+
 def qspec_pack_weights(W, Wp, S, stream=None):
     """W bf16 [N, K] -> Wp uint8 [N, K/2], S fp16 [N, K/128] (outputs written in place)."""
     _dt(W, torch.bfloat16, "W"); _dt(Wp, torch.uint8, "Wp"); _dt(S, torch.float16, "S")
@@ -454,7 +462,8 @@ def qspec_rotary_turns(rot, base=10000.0, scaling="none", factor=1.0, original=0
     """Frequencies of a rotary embedding: (int64 CPU tensor [rot/2] of 64-bit turn fractions, mult)."""
     if scaling not in ROTARY_SCALINGS:
         raise ValueError(f"scaling must be one of {sorted(ROTARY_SCALINGS)}")
-    turns = torch.empty(max(int(rot) // 2, 1), dtype=torch.int64)
+    rot = _arg32(rot, "rot")
+    turns = torch.empty(max(min(rot, 1024) // 2, 1), dtype=torch.int64)
     mult = ctypes.c_float()
     _check("qspec_rotary_turns", load().qspec_rotary_turns(rot, base, ROTARY_SCALINGS[scaling], factor, original, low,
                                                            high, turns.data_ptr(), ctypes.addressof(mult)))
@@ -556,7 +565,7 @@ class KVBatch:
         B, max_pages = pages.shape
         _need(cu_tok, B + 1, "cu_tok"); _need(kv_len, B, "kv_len")
         self.cu_tok, self.kv_len, self.pages = cu_tok, kv_len, pages
-        self.desc = KVBatchDesc(_ptr(cu_tok), _ptr(kv_len), _ptr(pages), B, max_pages, int(max_tok), 0, 0)
+        self.desc = KVBatchDesc(_ptr(cu_tok), _ptr(kv_len), _ptr(pages), B, max_pages, _arg32(max_tok, "max_tok"), 0, 0)
 
     def ref(self, T):
         """The descriptor for a step of T new tokens, to be passed to a call.  Each is a copy of its own: threads may use
@@ -611,7 +620,7 @@ def qspec_kv_attention(cache, batch, q, out, ws, scale=None, window=0, tree=None
     op, os_ = _rows(out, hq, cache.dim, "out")
     _check("qspec_kv_attention",
            load().qspec_kv_attention(cache.ref, batch.ref(T), qp, qs, hq,
-                                     cache.dim ** -0.5 if scale is None else float(scale), int(window), _ptr(tree), op,
+                                     cache.dim ** -0.5 if scale is None else float(scale), _arg32(min(int(window), 2 ** 31 - 1), "window"), _ptr(tree), op,
                                      os_, _ptr(lse), _ptr(ws), ws.numel(), _stream(stream)))
 
 

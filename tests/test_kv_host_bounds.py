@@ -3,6 +3,7 @@ import ctypes
 import itertools
 
 import pytest
+import torch
 
 from quantized_speculative_decoding_qspec_gb300 import qspec as q
 
@@ -50,3 +51,34 @@ def test_steps_of_one_batch_do_not_share_their_size():
     assert read(five) == (5, 3, 2) and read(nine) == (9, 3, 2)
     batch.desc.max_tok = 7                                     # what is written into the batch's own descriptor counts
     assert read(batch.ref(9)) == (9, 7, 2) and read(nine) == (9, 3, 2)
+
+
+class Recorder:
+    """Stands for the library: keeps the arguments of a call, as the 32-bit ones arrive."""
+    def __init__(self):
+        self.calls = []
+
+    def __getattr__(self, name):
+        types = q.SIGNATURES[name][1]
+        return lambda *args: self.calls.append([t(x).value if t is ctypes.c_int32 else x for t, x in zip(types, args)]) or 0
+
+
+def test_numbers_beyond_32_bits_are_not_cut_down(monkeypatch):
+    i32 = torch.int32
+    monkeypatch.setattr(q, "_ptr", lambda t: FAKE)
+    monkeypatch.setattr(q, "_rows", lambda t, heads, dim, name: (FAKE, heads * dim))
+    lib = Recorder()
+    monkeypatch.setattr(q, "load", lambda: lib)
+    tables = torch.zeros(2, dtype=i32), torch.zeros(1, dtype=i32), torch.zeros(1, 4, dtype=i32)
+    with pytest.raises(ValueError, match="max_tok does not fit"):
+        q.KVBatch(*tables, 2 ** 32 + 3)
+    with pytest.raises(ValueError, match="rot does not fit"):
+        q.qspec_rotary_turns(2 ** 32 + 64)
+    u = torch.zeros(1, 1, 16, 64, dtype=torch.uint8)
+    cache = q.KVCache(u, u, torch.zeros(1, 1, dtype=torch.int8), torch.zeros(1, 1, dtype=torch.int8))
+    x, ws = torch.zeros(2, 1, 64, dtype=torch.bfloat16), torch.zeros(8, dtype=torch.uint8)
+    for window, arrives in ((0, 0), (5, 5), (2 ** 31 - 1, 2 ** 31 - 1), (2 ** 32 + 5, 2 ** 31 - 1), (-1, -1)):
+        q.qspec_kv_attention(cache, q.KVBatch(*tables, 2), x, x, ws, window=window, stream=0)
+        assert lib.calls[-1][6] == arrives                      # (a window beyond every position hides none)
+    with pytest.raises(ValueError, match="window does not fit"):
+        q.qspec_kv_attention(cache, q.KVBatch(*tables, 2), x, x, ws, window=-2 ** 32, stream=0)
