@@ -20,11 +20,9 @@ template <int D, int RG>
 qspec_status launch_decode(AttArgs& a, int64_t rows, cudaStream_t s) {
   using C = DecodeCfg<D, RG>;
   a.max_tiles = static_cast<int>((rows + C::kRows - 1) / C::kRows);
-  const size_t smem = C::kSmem + sizeof(int2) * (a.b.B + 1);
-  if (cudaFuncSetAttribute(decode_kernel<D, RG>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           C::kSmem + static_cast<int>(sizeof(int2)) * (QSPEC_KV_MAX_B + 1)) != cudaSuccess)
+  if (cudaFuncSetAttribute(decode_kernel<D, RG>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::smem(QSPEC_KV_MAX_B)) != cudaSuccess)
     return QSPEC_ERR_CUDA;
-  return launch_pdl(decode_kernel<D, RG>, dim3(max_grid(C::kCtas)), dim3(C::kThreads), smem, s, a);
+  return launch_pdl(decode_kernel<D, RG>, dim3(max_grid(C::ctas(a.b.B))), dim3(C::kThreads), C::smem(a.b.B), s, a);
 }
 
 template <int D, bool kBigPages>

@@ -32,13 +32,24 @@ struct DecodeCfg {
   static constexpr int kRows = 16 * RG;
   static constexpr int kKeys = 64;
   static constexpr int kThreads = 128 * RG;
-  static constexpr int kCtas = 4 / RG;           // resident per SM
+  static constexpr int kCtas = 4 / RG;           // resident per SM, at most
   static constexpr int kStages = 3;
   static constexpr int kSide = 16 * D;           // bytes of 16 keys or values
   static constexpr int kRing = 4 * kStages * 2 * kSide;
   static constexpr int kRowPad = D + (D / 32) * 4 * (D == 128 ? 1 : 2);  // floats of a merge row: conflict-free
   static constexpr int kMerge = 4 * RG * 16 * kRowPad * 4;               // takes the ring's place between items
-  static constexpr int kSmem = 128 + (kRing > kMerge ? kRing : kMerge) + RG * D * 32 + 2048;
+  // the warps' maxima and sums, the walk, the scan, flags
+  static constexpr int kState = 4 * RG * 16 * 8 + sizeof(Walk<kRows, kKeys>) + sizeof(ScanShared) + 16;
+  static constexpr int kSmem = 128 + (kRing > kMerge ? kRing : kMerge) + RG * D * 32 + kState;
+  static constexpr int smem(int B) { return kSmem + static_cast<int>(sizeof(int2)) * (B + 1); }
+  // CTAs that an SM's shared memory holds beside each other: with the table of many sequences one less.  (Heads of 128,
+  // up to 16 rows: three from 377 sequences on.  A grid of more leaves the rest of its equal runs to a second, mostly
+  // empty wave: single tokens over 460000 positions in all, 64 heads on 8, 512 sequences 242 us against 181; 256, where
+  // exact sizes let four fit, 220 against 157.)
+  static constexpr int ctas(int B) {
+    const int fit = kSmemPerSm / ((smem(B) + 127) / 128 * 128 + kSmemReserved);
+    return fit < kCtas ? fit : kCtas;
+  }
 };
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint4& a, uint32_t b0, uint32_t b1) {

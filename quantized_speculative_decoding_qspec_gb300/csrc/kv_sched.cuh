@@ -24,6 +24,8 @@ constexpr float kNoMax = -3.3e38f;               // reference of a row that has 
 // 2% of the sum, were lost.)
 constexpr float kSlack = 15.0f, kLift = 8.0f;
 
+constexpr int kSmemPerSm = 228 * 1024, kSmemReserved = 1024;  // of sm_103: an SM's shared memory, and what a CTA takes unseen
+
 struct AttArgs {
   qspec_kv_cache c;
   qspec_kv_batch b;

@@ -1,11 +1,12 @@
 // The attention kernels' schedule, run on the host: which CTA arrives at which ticket, when runs are given up half way.
-// Prints one line per seed: units, runs, cut items, arrivals missed without the rest of a run that is given up.
+// Prints one line per seed: units, runs, cut items, arrivals missed without the rest of a run that is given up.  Then
+// "ctas", heads' size, row groups, sequences, CTAs an SM, shared memory of each, for the decode kernels' grids.
 #include <cstdio>
 #include <cstdlib>
 #include <random>
 #include <vector>
 
-#include "kv_sched.cuh"
+#include "kv_decode.cuh"
 
 using namespace qspec::att;
 constexpr int kRows = 256, kKeys = 128;
@@ -32,6 +33,12 @@ struct Tickets {
     return n;
   }
 };
+
+template <int D, int RG>
+void grids() {
+  using C = DecodeCfg<D, RG>;
+  for (int b : {1, 64, 239, 240, 256, 300, 512, 1024}) std::printf("ctas %d %d %d %d %d\n", D, RG, b, C::ctas(b), C::smem(b));
+}
 
 int main() {
   for (int seed = 0; seed < 40; ++seed) {
@@ -112,5 +119,9 @@ int main() {
     }
     std::printf("%lld %d %d %d\n", sh.total, sh.runs, cut, missed);
   }
+  grids<64, 1>();
+  grids<64, 2>();
+  grids<128, 1>();
+  grids<128, 2>();
   return 0;
 }
