@@ -593,7 +593,8 @@ qspec_status qspec_kv_attention(const qspec_kv_cache* cache, const qspec_kv_batc
  *     seen[v] v occurs there or in the prompt, hist[b, 0 .. prompt_len - 1]
  *     z = logit;  if seen: z = z > 0 ? z / repetition : z * repetition
  *     z = z - frequency * c - (c > 0 ? presence : 0) + bias[v];   masked out: z = -inf
- * computed in fp32 and rounded to bf16 once; a logit that nothing touches keeps its bits.
+ * computed in fp32 (the quotient as the product with 1 / repetition) and rounded to bf16 once; a logit that nothing
+ * touches keeps its bits.
  *
  *   logits     [B, rows, V] bf16;  out [B, rows, V] bf16, may be logits itself
  *   draft_tok  [B, rows-1] int32, or NULL: none

@@ -37,15 +37,23 @@ struct LogitsArgs {
   int rows, V, n_bias, range;  // range: tokens per block
 };
 
-// What a token's history and bias do to its logit: z > 0 ? z * up : z * down where it was seen, then - sub.
+// What a token's history and bias do to its logit: z > 0 ? z / rep : z * rep where it was seen, then - sub.  The quotient
+// is the product with the reciprocal, one fp32 rounding more before the one to bf16 ([64, 8, 152064] with divisions: 96
+// us against 80).  Where the reciprocal is no normal number (`divide`) the sequence's blocks walk token by token and
+// divide: a choice for each logit cost 9 us of the 80, too.
 struct Penalty {
   float rep, inv, freq, pres;
+  bool divide;
   __device__ float sub(uint32_t count, float bias) const {
     const uint32_t c = count & ~kSeen;
     return (c ? fmaf(freq, static_cast<float>(c), pres) : 0.0f) - bias;
   }
   __device__ float adjust(float z, bool seen, float sub) const {
     if (seen) z *= z > 0.0f ? inv : rep;
+    return z - sub;
+  }
+  __device__ float adjust_dividing(float z, bool seen, float sub) const {
+    if (seen) z = z > 0.0f ? z / rep : z * rep;
     return z - sub;
   }
 };
@@ -97,14 +105,15 @@ __global__ void __launch_bounds__(kThreads, 4) logits_kernel(const LogitsArgs a)
     bad |= t < 0 || t >= a.V;
     sdraft[threadIdx.x] = t;
   }
-  Penalty p{1.0f, 1.0f, 0.0f, 0.0f};
+  Penalty p{1.0f, 1.0f, 0.0f, 0.0f, false};
   if (a.pen) {
-    p = Penalty{a.pen[3 * b], 1.0f, a.pen[3 * b + 1], a.pen[3 * b + 2]};
+    p = Penalty{a.pen[3 * b], 1.0f, a.pen[3 * b + 1], a.pen[3 * b + 2], false};
     if (!(p.rep > 0.0f)) {
       bad = true;
       p.rep = 1.0f;
     }
     p.inv = 1.0f / p.rep;
+    p.divide = !(p.rep >= 0x1p-126f && p.rep <= 0x1p126f);
   }
   __syncthreads();
   if (a.hist && a.pen) {
@@ -162,7 +171,7 @@ __global__ void __launch_bounds__(kThreads, 4) logits_kernel(const LogitsArgs a)
     for (int r = 1; r <= n_draft; ++r)
       if (static_cast<uint32_t>(sdraft[r - 1]) - static_cast<uint32_t>(v0) < static_cast<uint32_t>(nv)) drafted |= 1u << r;
   const int64_t row0 = static_cast<int64_t>(b) * a.rows;
-  if (kVec == 8) {
+  if (kVec == 8 && !p.divide) {
     for (int i0 = (threadIdx.x & ~31) * 8; i0 < nv; i0 += kThreads * 8) {  // 256 tokens of a warp
       const int lane = threadIdx.x & 31, i = i0 + 8 * lane;
       const bool in = i < nv;
@@ -267,7 +276,10 @@ __global__ void __launch_bounds__(kThreads, 4) logits_kernel(const LogitsArgs a)
           if (r >= a.rows) break;
           if ((drafted >> r & 1u) && sdraft[r - 1] == v0 + i) c = one_more(c);
           uint16_t x = w[q];
-          if (c | bs) x = f32_to_bf16_bits(p.adjust(bf16_lo(x), c != 0, p.sub(c, __uint_as_float(bs))));
+          if (c | bs) {
+            const float sub = p.sub(c, __uint_as_float(bs));
+            x = f32_to_bf16_bits(p.divide ? p.adjust_dividing(bf16_lo(x), c != 0, sub) : p.adjust(bf16_lo(x), c != 0, sub));
+          }
           if (!(allowed[q] & 1u)) x = 0xFF80u;
           a.out[(row0 + r) * a.V + v0 + i] = x;
         }
