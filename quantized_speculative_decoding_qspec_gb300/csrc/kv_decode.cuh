@@ -298,7 +298,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, RG>::kThreads, DecodeCfg<D, RG>::
       }
       const float top0 = fmaxf(fmaxf(z[0][0], z[0][1]), fmaxf(z[1][0], z[1][1]));
       const float top1 = fmaxf(fmaxf(z[0][2], z[0][3]), fmaxf(z[1][2], z[1][3]));
-      if (__any_sync(0xFFFFFFFFu, top0 > m[0] + kSlack || top1 > m[1] + kSlack)) {
+      if (__any_sync(0xFFFFFFFFu, top0 - m[0] > kSlack || top1 - m[1] > kSlack)) {  // (a sum m + kSlack would round)
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
           float top = r == 0 ? top0 : top1;

@@ -281,7 +281,7 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1) prefill_kernel(con
               if (see) top = fmaxf(top, fmaf(x, fminf(mult * gv.x, 3e38f), gv.y));
             }
           }
-          if (__any_sync(0xFFFFFFFFu, top > m + kSlack)) {
+          if (__any_sync(0xFFFFFFFFu, top - m > kSlack)) {  // (a sum m + kSlack would round)
             const float m1 = fmaxf(m, top - kLift);
             const float keep = ex2(m - m1);
             m = m1;

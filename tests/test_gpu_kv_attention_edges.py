@@ -37,3 +37,35 @@ def test_many_sequences(B, heads_q, heads, dim):
     qq = queries(33, bt.T, heads_q, dim)
     check(run(q, bt, qq), bt, qq)
     q.qspec_check_status()
+
+
+@pytest.mark.parametrize("heads_q", [2, 20, 70])               # both decode kernels, the prefill kernel
+@pytest.mark.parametrize("magnitude", [20, 22, 23, 24, 25, 26, 28])
+def test_scores_so_large_that_their_steps_are_coarse(magnitude, heads_q):
+    """A score of about 2^magnitude powers of two, and one 12 to 20 powers of two above it a few tiles later: all
+    values are 1, so the output is 1 whatever the weights round to.  (700 sequences of seven kinds: a CTA walks several tiles.)"""
+    q = lib()
+    P, D, N, B = 128, 64, 300, 700
+    scale = next(s for k in range(-4, 5) for s in [torch.tensor(0.6931472, dtype=torch.float32).view(torch.int32).add(k).view(torch.float32)]
+                 if float(s * torch.tensor(1.44269504088896, dtype=torch.float32)) == 1.0)
+    above = torch.tensor([12, 13, 14, 15, 16, 18, 20], dtype=torch.float64)
+    kinds, n = len(above), -(-N // P)
+    k, v = torch.zeros(kinds * n, 1, P, D, dtype=torch.uint8), torch.full((kinds * n, 1, P, D), 0x38, dtype=torch.uint8)
+    for b in range(kinds):
+        k[b * n, 0, 0, 0] = k[b * n + 1, 0, 0, 0] = 0x78                    # 2^8
+        k[b * n + 1, 0, 0, 1] = ref.e4m3(above[b:b + 1])[0]
+    exps = torch.zeros(kinds * n, 1, dtype=torch.int8)
+    table = torch.arange(kinds * n, dtype=torch.int32, device=DEV).view(kinds, n).repeat(B // kinds, 1)
+    cache = q.KVCache(k.to(DEV), v.to(DEV), exps.to(DEV), exps.clone().to(DEV))
+    batch = q.KVBatch(torch.arange(B + 1, dtype=torch.int32, device=DEV), torch.full((B,), N, dtype=torch.int32, device=DEV),
+                      table, 1)
+    qq = torch.zeros(B, heads_q, D, dtype=torch.bfloat16, device=DEV)
+    qq[..., 0], qq[..., 1] = 2.0 ** (magnitude - 8), 1.0
+    out, lse = torch.empty_like(qq), torch.empty(B, heads_q, device=DEV)
+    q.qspec_kv_attention(cache, batch, qq, out, q.new_kv_attention_workspace(), scale=float(scale), lse=lse)
+    q.qspec_check_status()
+    # the weights' rounding to fp16 (2^-11), the output's to bf16
+    assert float((out.double() - 1).abs().max()) <= 2.0 ** -8 + 2.0 ** -10
+    # the score's own rounding (half a step of fp32 and of its product), and the logarithm of at most two such weights
+    want = (2.0 ** magnitude + above.to(DEV).repeat(B // kinds)[:, None]) * 0.6931471805599453
+    assert float((lse.double() - want).abs().max()) <= 2.0 ** (magnitude - 22) + 1
