@@ -69,3 +69,42 @@ def test_scores_so_large_that_their_steps_are_coarse(magnitude, heads_q):
     # the score's own rounding (half a step of fp32 and of its product), and the logarithm of at most two such weights
     want = (2.0 ** magnitude + above.to(DEV).repeat(B // kinds)[:, None]) * 0.6931471805599453
     assert float((lse.double() - want).abs().max()) <= 2.0 ** (magnitude - 22) + 1
+
+
+@pytest.mark.parametrize("tok,kv,heads_q,heads,dim", [([140], [300], 2, 1, 128), ([200, 70], [512, 129], 4, 2, 128), ([64, 1], [1000, 77], 8, 1, 128)])
+def test_prompt_chunks_over_long_pages(tok, kv, heads_q, heads, dim):
+    """More than 64 rows a key head, heads of 128, pages of 128 slots."""
+    q = lib()
+    bt = ref.Batch(121, tok, kv, heads, 128, dim)
+    qq = queries(35, bt.T, heads_q, dim)
+    check(run(q, bt, qq), bt, qq)
+    q.qspec_check_status()
+
+
+@pytest.mark.parametrize("heads_q", [2, 20, 70])               # both decode kernels, the prefill kernel
+@pytest.mark.parametrize("page,dim", [(16, 64), (64, 128), (128, 64)])
+def test_the_tokens_of_bad_pages_are_left_out(page, dim, heads_q, monkeypatch):
+    """The first, a middle and the last page of a sequence are missing: the others' tokens alone count."""
+    q = lib()
+    tok, kv = [1, 2], [90, 5 * page - 7]
+    bt = ref.Batch(131, tok, kv, 1, page, dim)
+    qq = queries(37, bt.T, heads_q, dim)
+    cache, batch = bt.gpu(q)
+    missing = (0, 2, 4)
+    batch.pages[1, 0], batch.pages[1, 2], batch.pages[1, 4] = -1, bt.n_pages, 2 ** 31 - 1
+    qg = qq.to(DEV)
+    out, lse = torch.full_like(qg, 77.0), torch.empty(qq.shape[:2], device=DEV)
+    q.qspec_kv_attention(cache, batch, qg, out, q.new_kv_attention_workspace(), lse=lse)
+    with pytest.raises(q.QSpecError, match="INVALID_ARG"):
+        q.qspec_check_status()
+    seen = ref.visible
+
+    def visible(i, n, length, *args):
+        see = seen(i, n, length, *args)
+        if length == kv[1]:
+            for p in missing:
+                see[p * page:(p + 1) * page] = False
+        return see
+
+    monkeypatch.setattr(ref, "visible", visible)
+    check((out, lse), bt, qq)
