@@ -438,7 +438,8 @@ qspec_status qspec_copy(void* dst, const void* src, size_t bytes, qspec_stream_t
  * qspec_rotary_turns -- the frequencies of a rotary embedding, for qspec_rotary and qspec_kv_append.
  * A HOST function: writes rot/2 words and one float to host memory; the caller copies the words to the
  * device.  Word i is the rotation of pair i per position as a 64-bit fraction of a full turn, so
- * position * word modulo 2^64 is the angle with no error from range reduction, at any position.
+ * position * word modulo 2^64 is the angle with no error from range reduction, at any position.  (A word has the few
+ * fp64 roundings of its frequency, 2^-53 each, which the position multiplies.)
  *     w_i = base^(-2 i / rot) radians per position, scaled for long contexts:
  *     QSPEC_ROTARY_PLAIN   w_i
  *     QSPEC_ROTARY_LINEAR  w_i / factor
@@ -447,7 +448,8 @@ qspec_status qspec_copy(void* dst, const void* src, size_t bytes, qspec_stream_t
  *                          w_i / factor below `low` turns, w_i above `high`, linear in t_i between
  *     QSPEC_ROTARY_YARN    pairs that turn more than `high` times over the trained context keep w_i, those
  *                          that turn less than `low` times take w_i / factor, with a linear ramp over
- *                          the pair index between (edges rounded outwards to whole indices);
+ *                          the pair index between (edges rounded outwards to whole indices; the ramp
+ *                          begins at pair 0 at the earliest, which keeps w_0 therefore);
  *                          *mult = 0.1 ln(factor) + 1
  *   rot even, 2 <= rot <= 1024 (rot >= 4 for QSPEC_ROTARY_BASE); base > 1; factor >= 1; original > 0;
  *   0 < low < high (BANDS and YARN; ignored otherwise)
@@ -536,13 +538,17 @@ typedef struct {
  *       otherwise:  exp = max(exp, e(amax)); where that raises it, the codes of the page's other slots are
  *                   quantised again: code = e4m3(code * 2^(old - new))
  *     code = e4m3(x * 2^-exp), round to nearest even, saturating
- * Dropping rejected tokens needs no call: use a smaller kv_len next time.  A page's scale does not shrink
- * until the page is begun again.  A non-finite key or value is stored as 0 and makes the next
+ * Dropping rejected tokens of a chain needs no call: use a smaller kv_len next time.  The accepted path of a tree is no
+ * prefix of what was appended: append its tokens' keys and values again, at the kv_len of the path.  A page's scale does
+ * not shrink until the page is begun again, so tokens that were dropped leave a mark: where they raised the scale, the
+ * codes of the page's other tokens have been rounded again (those alone that fell below e4m3's normal range change).
+ * A non-finite key or value is stored as 0 and makes the next
  * qspec_check_status return QSPEC_ERR_INVALID_ARG.
  *
  *   k, v   bf16, value d of head h of token t at k[t * k_token + h * dim + d]
  *   plan   rotary embedding of the keys and queries (keys are rounded to bf16 before they are
- *          quantised), or NULL: none
+ *          quantised), or NULL: none.  Its rot is a multiple of 16 unless pairs are interleaved
+ *          (QSPEC_ERR_UNSUPPORTED_SHAPE otherwise)
  *   pos    [T] int32 device: each token's rotary position, or NULL: its cache position
  *   q      bf16 [T] tokens of heads_q * dim values, stride q_token, rotated into q_out (stride
  *          q_out_token; q_out may be q itself with the same stride), or NULL: no queries
@@ -565,8 +571,8 @@ qspec_status qspec_kv_append(const qspec_kv_cache* cache, const qspec_kv_batch* 
  *     with a tree:  j < kv_len - n, or bit (j - (kv_len - n)) of the token's tree word is set (j < kv_len)
  * A token that sees nothing gets out = 0 and lse = -inf; a query with a NaN or an infinity that sees
  * anything gets out = lse = NaN.  Scores and softmax statistics are fp32; the
- * probabilities are rounded to fp16 for the product with the (exactly converted) codes, out is rounded
- * to bf16 once.
+ * probabilities are rounded to fp16 for the product with the (exactly converted) codes, where a weight p_j 2^exp counts
+ * down to 2^-33 of the largest that came with it; out is rounded to bf16 once.
  *
  *   q      bf16, value d of head h of token t at q[t * q_token + h * dim + d]
  *   window 0: none
@@ -575,7 +581,8 @@ qspec_status qspec_kv_append(const qspec_kv_cache* cache, const qspec_kv_batch* 
  *   lse    [T, heads_q] fp32 or NULL
  *   ws, ws_bytes  device workspace of >= qspec_kv_attention_workspace_size() bytes, zero-filled before
  *          its first use; it serves every shape and is left ready for the next call (after a wait that
- *          ran out, QSPEC_ERR_TIMEOUT, too: only the outputs are void then)
+ *          ran out, QSPEC_ERR_TIMEOUT, too: only the outputs are void then).  Calls that can overlap, on two
+ *          streams, need one each
  *   heads_q a multiple of the cache's heads, at most 128 times them; scale finite; token strides multiples of
  *   8 and at least heads_q * dim
  */
@@ -593,6 +600,8 @@ qspec_status qspec_kv_attention(const qspec_kv_cache* cache, const qspec_kv_batc
  *     seen[v] v occurs there or in the prompt, hist[b, 0 .. prompt_len - 1]
  *     z = logit;  if seen: z = z > 0 ? z / repetition : z * repetition
  *     z = z - frequency * c - (c > 0 ? presence : 0) + bias[v];   masked out: z = -inf
+ * (The bias comes last.  Where it is added before the penalties, as many servers do, a token that is both seen and biased
+ * comes out differently, as the repetition penalty goes by the logit's sign.)
  * computed in fp32 (the quotient as the product with 1 / repetition) and rounded to bf16 once; a logit that nothing
  * touches keeps its bits.
  *

@@ -11,6 +11,11 @@ greedy verification, put together as a serving loop uses them:
   adjusted logits of all positions go to the verify call, position i counting the drafts before it;
 * what was rejected is dropped by a smaller length.
 
+Every emitted token is the greedy choice of the W4A16 pass that verified it.  The cache that this pass attends to is not
+quite the one that decoding token by token would have left: drafted and rejected tokens may have raised a page's scale, and
+the codes of accepted ones below e4m3's normal range were rounded again.  Where two logits are as near as that, the text can
+differ from plain W4A16 decoding.
+
 ``python -m quantized_speculative_decoding_qspec_gb300.attention_lm`` runs it on one GPU.
 """
 from __future__ import annotations

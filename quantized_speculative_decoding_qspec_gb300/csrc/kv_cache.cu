@@ -2,7 +2,8 @@
 //
 // value = code * 2^exp with one exponent per (page, head) for the keys and one for the values: the
 // smallest e with amax <= 448 * 2^e.  Power-of-two scales make both directions exact but for the one
-// rounding to e4m3, and a page that has to grow is quantised again by an exact shift.  Each value is read
+// rounding to e4m3.  A page that has to grow is quantised again by a shift: codes that stay in e4m3's normal range keep
+// their values, those that fall below it are rounded once more.  Each value is read
 // once (2 bytes) and its code written once (1 byte); memory bounds long appends, launch latency short
 // ones.  A block owns one side (keys or values) of one (sequence, touched page) and up to four heads: it holds the page's new
 // values in registers (at most 8 items of 16 a thread), so the maximum, the rounding and the writes need one
