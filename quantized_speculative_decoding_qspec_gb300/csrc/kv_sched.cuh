@@ -21,7 +21,7 @@ constexpr float kNoMax = -3.3e38f;               // reference of a row that has 
 // P = 2^(z - m) is fp16 for the product with the values.  A row's reference m is set kLift below its largest score and
 // stays until a score exceeds it by kSlack: P <= 2^15 fits, and a key keeps a share of the product down to 2^-33 of the
 // largest weight.  (With m at the largest score it ended at 2^-25: behind one dominant key, a million others of 2^-25.5,
-// 2% of the sum, were lost.)
+// 2% of the sum, were lost.  It costs some more moves of m: 4096 tokens over 8192 positions 375 -> 380 us.)
 constexpr float kSlack = 15.0f, kLift = 8.0f;
 
 constexpr int kSmemPerSm = 228 * 1024, kSmemReserved = 1024;  // of sm_103: an SM's shared memory, and what a CTA takes unseen
