@@ -304,7 +304,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, RG>::kThreads, DecodeCfg<D, RG>::
           float top = r == 0 ? top0 : top1;
           top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
           top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-          const float m1 = fmaxf(m[r], top - kLift);
+          const float m1 = fmaxf(m[r], reference_of(top));
           const float keep = ex2(m[r] - m1);
           m[r] = m1;
           l[r] *= keep;

@@ -282,11 +282,11 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1) prefill_kernel(con
             }
           }
           if (__any_sync(0xFFFFFFFFu, top - m > kSlack)) {  // (a sum m + kSlack would round)
-            const float m1 = fmaxf(m, top - kLift);
+            const float m1 = fmaxf(m, reference_of(top));
             const float keep = ex2(m - m1);
             m = m1;
             l *= keep;
-            far = __any_sync(0xFFFFFFFFu, fabsf(m) > 4194304.0f);
+            far = __any_sync(0xFFFFFFFFu, fabsf(m) > kFar);
             if (n > 0) {
 #pragma unroll 1
               for (int c = 0; c < D; c += 16) {

@@ -23,6 +23,10 @@ constexpr float kNoMax = -3.3e38f;               // reference of a row that has 
 // largest weight.  (With m at the largest score it ended at 2^-25: behind one dominant key, a million others of 2^-25.5,
 // 2% of the sum, were lost.  It costs some more moves of m: 4096 tokens over 8192 positions 375 -> 380 us.)
 constexpr float kSlack = 15.0f, kLift = 8.0f;
+// The reference for a largest score `top`.  Scores beyond kFar are so coarse that a sum with kLift could round to another
+// 8 below: the reference is the score itself there.
+constexpr float kFar = 4194304.0f;
+__device__ __forceinline__ float reference_of(float top) { return fabsf(top) < kFar ? top - kLift : top; }
 
 constexpr int kSmemPerSm = 228 * 1024, kSmemReserved = 1024;  // of sm_103: an SM's shared memory, and what a CTA takes unseen
 

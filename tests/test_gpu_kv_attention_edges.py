@@ -40,7 +40,7 @@ def test_many_sequences(B, heads_q, heads, dim):
 
 
 @pytest.mark.parametrize("heads_q", [2, 20, 70])               # both decode kernels, the prefill kernel
-@pytest.mark.parametrize("magnitude", [20, 22, 23, 24, 25, 26, 28])
+@pytest.mark.parametrize("magnitude", [20, 21, 22, 23, 24, 25, 26, 27, 28, 29, 31])
 def test_scores_so_large_that_their_steps_are_coarse(magnitude, heads_q):
     """A score of about 2^magnitude powers of two, and one 12 to 20 powers of two above it a few tiles later: all
     values are 1, so the output is 1 whatever the weights round to.  (700 sequences of seven kinds: a CTA walks several tiles.)"""
