@@ -583,7 +583,7 @@ qspec_status qspec_kv_append(const qspec_kv_cache* cache, const qspec_kv_batch* 
  *          its first use; it serves every shape and is left ready for the next call (after a wait that
  *          ran out, QSPEC_ERR_TIMEOUT, too: only the outputs are void then).  Calls that can overlap, on two
  *          streams, need one each
- *   heads_q a multiple of the cache's heads, at most 128 times them; scale finite; token strides multiples of
+ *   heads_q a multiple of the cache's heads, at most 128 times them; |scale| <= 2^127; token strides multiples of
  *   8 and at least heads_q * dim
  */
 size_t qspec_kv_attention_workspace_size(void);

@@ -52,7 +52,8 @@ extern "C" qspec_status qspec_kv_attention(const qspec_kv_cache* cache, const qs
                                            int64_t q_token, int32_t heads_q, float scale, int32_t window,
                                            const uint64_t* tree, uint16_t* out, int64_t out_token, float* lse, void* ws,
                                            size_t ws_bytes, qspec_stream_t stream) {
-  if (!q || !out || heads_q <= 0 || !isfinite(scale) || window < 0) return QSPEC_ERR_INVALID_ARG;
+  const float scale_log2 = scale * 1.44269504088896f;
+  if (!q || !out || heads_q <= 0 || !isfinite(scale_log2) || window < 0) return QSPEC_ERR_INVALID_ARG;
   qspec_status st = check_kv(cache, batch);
   if (st != QSPEC_OK) return st;
   if (heads_q % cache->heads != 0 || heads_q / cache->heads > 128) return QSPEC_ERR_UNSUPPORTED_SHAPE;
@@ -77,7 +78,7 @@ extern "C" qspec_status qspec_kv_attention(const qspec_kv_cache* cache, const qs
   while ((1 << shift) < a.group) ++shift;
   a.group_shift = 31 + shift;
   a.group_mul = static_cast<uint32_t>(((uint64_t(1) << a.group_shift) + a.group - 1) / a.group);
-  a.scale_log2 = scale * 1.44269504088896f;
+  a.scale_log2 = scale_log2;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   // Up to 64 rows a key head the decode kernel reads a sequence's keys twice at most and wins everywhere (16
   // sequences of 4096, 64 rows: 71 against 77 us; one of 32768: 51 against 94); with 96 rows and more it reads them three

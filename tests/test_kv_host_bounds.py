@@ -82,3 +82,12 @@ def test_numbers_beyond_32_bits_are_not_cut_down(monkeypatch):
         assert lib.calls[-1][6] == arrives                      # (a window beyond every position hides none)
     with pytest.raises(ValueError, match="window does not fit"):
         q.qspec_kv_attention(cache, q.KVBatch(*tables, 2), x, x, ws, window=-2 ** 32, stream=0)
+
+
+def test_attention_refuses_scales_that_leave_fp32_in_powers_of_two(lib):
+    """Scores are taken in powers of two: scale * log2(e) has to be finite.  (A misaligned q is looked at afterwards.)"""
+    W = lib.qspec_kv_attention_workspace_size()
+    cache = ctypes.byref(q.KVCacheDesc(FAKE, FAKE, FAKE, FAKE, 10, 8, 64, 128, 0))
+    batch = ctypes.byref(q.KVBatchDesc(FAKE, FAKE, FAKE, 2, 4, 3, 0, 6))
+    for scale, code in ((2.0 ** 127, 3), (-2.0 ** 127, 3), (0.0, 3), (3e38, 1), (-3e38, 1)):
+        assert lib.qspec_kv_attention(cache, batch, FAKE + 2, 4096, 32, scale, 0, None, FAKE, 4096, None, FAKE, W, None) == code, scale
