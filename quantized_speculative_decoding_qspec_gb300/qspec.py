@@ -519,6 +519,11 @@ class KVBatchDesc(ctypes.Structure):
     _fields_ = [("cu_tok", ctypes.c_void_p), ("kv_len", ctypes.c_void_p), ("pages", ctypes.c_void_p),
                 ("B", ctypes.c_int32), ("max_pages", ctypes.c_int32), ("max_tok", ctypes.c_int32),
                 ("reserved", ctypes.c_int32), ("T", ctypes.c_int64)]
+    refs = None   # copies given to calls, by their T
+
+    def __setattr__(self, name, value):
+        super().__setattr__(name, value)
+        self.__dict__["refs"] = {}   # what is written counts from the next call on
 
 
 class KVCache:
@@ -568,11 +573,18 @@ class KVBatch:
         self.desc = KVBatchDesc(_ptr(cu_tok), _ptr(kv_len), _ptr(pages), B, max_pages, _arg32(max_tok, "max_tok"), 0, 0)
 
     def ref(self, T):
-        """The descriptor for a step of T new tokens, to be passed to a call.  Each is a copy of its own: threads may use
-        one batch for steps of different sizes at once (ctypes lets go of the interpreter's lock while a call runs)."""
-        desc = KVBatchDesc.from_buffer_copy(self.desc)
-        desc.T = T
-        return ctypes.byref(desc)
+        """The descriptor for a step of T new tokens, to be passed to a call.  Each T has a copy of its own that stays as it
+        is: threads may use one batch for steps of different sizes at once (ctypes lets go of the interpreter's lock
+        while a call runs)."""
+        refs = self.desc.refs
+        ref = refs.get(T)
+        if ref is None:
+            desc = KVBatchDesc.from_buffer_copy(self.desc)
+            desc.T = T
+            if len(refs) >= 64:
+                refs.clear()
+            ref = refs[T] = ctypes.byref(desc)
+        return ref
 
 
 def qspec_kv_append(cache, batch, k, v, rotary=None, pos=None, q=None, q_out=None, stream=None):
@@ -618,10 +630,13 @@ def qspec_kv_attention(cache, batch, q, out, ws, scale=None, window=0, tree=None
     _need(tree, T, "tree"); _need(lse, T * hq, "lse")
     qp, qs = _rows(q, hq, cache.dim, "q")
     op, os_ = _rows(out, hq, cache.dim, "out")
+    window = int(window)
+    if not 0 <= window < 2 ** 31:  # (one beyond every position hides none)
+        window = _arg32(min(window, 2 ** 31 - 1), "window")
     _check("qspec_kv_attention",
            load().qspec_kv_attention(cache.ref, batch.ref(T), qp, qs, hq,
-                                     cache.dim ** -0.5 if scale is None else float(scale), _arg32(min(int(window), 2 ** 31 - 1), "window"), _ptr(tree), op,
-                                     os_, _ptr(lse), _ptr(ws), ws.numel(), _stream(stream)))
+                                     cache.dim ** -0.5 if scale is None else float(scale), window, _ptr(tree), op, os_,
+                                     _ptr(lse), _ptr(ws), ws.numel(), _stream(stream)))
 
 
 def qspec_logits_adjust(logits, out, draft_tok=None, hist=None, hist_len=None, prompt_len=None, penalties=None,

@@ -41,7 +41,6 @@ def test_rotary_refuses_outputs_that_overlap(lib):
 def test_steps_of_one_batch_do_not_share_their_size():
     batch = q.KVBatch.__new__(q.KVBatch)                       # (its constructor wants tensors on a GPU)
     batch.desc = q.KVBatchDesc(FAKE, FAKE, FAKE, 2, 4, 3, 0, 0)
-    batch._address, batch._T = ctypes.addressof(batch.desc), 0
 
     def read(r):
         d = ctypes.cast(r, ctypes.POINTER(q.KVBatchDesc)).contents
@@ -51,6 +50,9 @@ def test_steps_of_one_batch_do_not_share_their_size():
     assert read(five) == (5, 3, 2) and read(nine) == (9, 3, 2)
     batch.desc.max_tok = 7                                     # what is written into the batch's own descriptor counts
     assert read(batch.ref(9)) == (9, 7, 2) and read(nine) == (9, 3, 2)
+    refs = [batch.ref(t) for t in range(1, 300)]               # (the ones kept are few, but all stay good)
+    assert [read(r) for r in refs] == [(t, 7, 2) for t in range(1, 300)]
+    assert batch.ref(299) is refs[-1] and len(batch.desc.refs) <= 64
 
 
 class Recorder:
