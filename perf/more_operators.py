@@ -399,9 +399,10 @@ def _compact(s):
         x = torch.gather(x, 3, source[None, :, None, :, None].expand(L, -1, H, -1, D)).view(L, -1, H, W, P, D).permute(0, 1, 3, 2, 4, 5)
         put = moved.view(-1, W, P)
         amax = (x.abs().amax(5) * put[None, :, :, None, :]).amax(4)
-        e_new = torch.where(put[:, :, 0][None, :, :, None], _block_exp(amax), torch.maximum(e_old, _block_exp(amax)))
+        begun = put[:, :, 0][None, :, :, None]                      # what else lies in such a page means nothing any more
+        e_new = torch.where(begun, _block_exp(amax), torch.maximum(e_old, _block_exp(amax)))
         e_new = torch.where(put.any(2)[None, :, :, None], e_new, e_old)
-        keep = (~put)[None, :, :, None, :, None] & (e_new == e_old)[..., None, None]
+        keep = (~put)[None, :, :, None, :, None] & (begun | (e_new == e_old))[..., None, None]
         codes[:, page] = torch.where(keep, old, _codes(x, e_new))
         exps[:, page] = e_new.to(torch.int8)
 
