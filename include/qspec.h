@@ -593,6 +593,69 @@ qspec_status qspec_kv_attention(const qspec_kv_cache* cache, const qspec_kv_batc
                                 qspec_stream_t stream);
 
 /*
+ * ---------------------------------------------------------------------------------------------------
+ * Several continuations of one prompt: beams, samples, candidate trees.  The pages name tree-style candidates alone; these
+ * calls choose continuations, let their sequences share pages of the cache, and read what they share once.
+ */
+
+/*
+ * qspec_kv_pages -- the page tables of the next step: rows fork, move, shorten, grow, end or begin, in one call.
+ * Row b of the old table holds ceil(room[b] / page) pages, pages[b, 0 ...].  Row r of the new one keeps the first keep[r]
+ * positions of row parent[r] and has room for need[r] positions.  refs[p] counts who holds page p: each row that has it
+ * in its table, and anyone else for whom the caller raised the count (kept prefixes).  A page of count 0 is free.
+ *   - Kept pages are shared: their counts rise by one for each new row that has them; then all old rows are released.
+ *   - Where keep[r] ends inside a page and need[r] > keep[r], row r will write in that page.  If all that hold it are such rows,
+ *     the lowest of them keeps it; every other row gets a page of its own in its place, and (copy_src[r], copy_dst[r],
+ *     copy_len[r]) = (page, its own page, keep[r] mod page) for qspec_kv_copy_pages.  Rows without a copy get (-1, -1, 0).
+ *   - Fresh pages (copies first, then those up to need[r]) go to the rows in order, the free page of the lowest id first; pages
+ *     that this call released count as free.
+ *   - left = free pages that remain.  If they do not suffice, left is minus the number that lacks, the counts stay as they were,
+ *     no copies are asked for and new_pages is of no use.
+ *
+ *   pages [rows, max_pages], room [rows]: rows may be 0 (both NULL then);  parent [new_rows], or NULL: row r comes from row r
+ *   (negative: from none, with keep[r] = 0);  keep, need [new_rows]: 0 <= keep[r] <= room[parent[r]], keep[r] <= need[r];
+ *   new_pages [new_rows, new_max_pages] (not the old table: entries beyond need[r] are left as they are);  refs, new_refs
+ *   [n_pages], which may be the same array;  copy_src, copy_dst, copy_len [new_rows];  left [1].  new_rows may be 0 (its arrays
+ *   NULL then: all rows end).  All int32, DEVICE, 4-byte aligned (refs and new_refs 16).
+ *   page is 16, 32, 64 or 128; rows and new_rows at most QSPEC_KV_MAX_B; max_pages * page <= 2^30
+ * A row whose numbers are out of range gets no pages (an old one: releases none), an id outside [0, n_pages) is passed on without
+ * being counted, and either of them or a count below zero makes the next qspec_check_status return QSPEC_ERR_INVALID_ARG.
+ * Bit-exact.
+ */
+qspec_status qspec_kv_pages(const int32_t* pages, const int32_t* room, int32_t rows, int32_t max_pages, const int32_t* parent,
+                            const int32_t* keep, const int32_t* need, int32_t new_rows, int32_t new_max_pages,
+                            const int32_t* refs, int64_t n_pages, int32_t page, int32_t* new_pages, int32_t* new_refs,
+                            int32_t* copy_src, int32_t* copy_dst, int32_t* copy_len, int32_t* left, qspec_stream_t stream);
+
+/*
+ * qspec_kv_copy_pages -- page src[i] -> page dst[i] in each of n_caches caches (the layers of a model, which share page tables):
+ * the scales, and the codes of the first len[i] slots of every head (len NULL: of all).
+ *   caches HOST array of n_caches descriptors of one shape, 1 <= n_caches <= QSPEC_KV_MAX_LAYERS (read during the call)
+ *   src, dst, len [n] int32 DEVICE, 4-byte aligned; pairs with src[i] < 0 are skipped.  No dst[i] may be any other pair's src or dst
+ * A pair with an id outside [0, n_pages) or a len[i] outside [0, page] copies nothing and makes the next qspec_check_status return
+ * QSPEC_ERR_INVALID_ARG.
+ */
+#define QSPEC_KV_MAX_LAYERS 64
+qspec_status qspec_kv_copy_pages(const qspec_kv_cache* caches, int32_t n_caches, const int32_t* src, const int32_t* dst,
+                                 const int32_t* len, int32_t n, qspec_stream_t stream);
+
+/*
+ * qspec_kv_compact -- the accepted path of a tree becomes a prefix of what was appended, without its keys and values at hand.
+ * The last n new tokens of sequence b (n = cu_tok[b+1] - cu_tok[b]) were appended as a tree: node j lies at position
+ * kv_len - n + first + j (first = 1 where the token before the tree was appended with it).  For t < count[b] the cached keys and
+ * values of node nodes[b, t] move to position kv_len - n + first + t, as if qspec_kv_append wrote their (dequantised) values there:
+ * a page whose slot 0 is written takes the smallest scale that holds what it receives, another page's scale grows where it
+ * must.  The sequence's length after it is kv_len - n + first + count[b].
+ *   caches, n_caches  as for qspec_kv_copy_pages;  batch: as it was for the append
+ *   nodes [B, T] int32, count [B] int32 DEVICE, 4-byte aligned: what qspec_verify_tree_greedy returns.  1 <= T <=
+ *   QSPEC_MAX_TREE;  first >= 0;  nodes in [0, n - first), n - first <= QSPEC_MAX_TREE, count[b] <= min(T, n - first)
+ * A sequence whose numbers, nodes or pages are out of range is left as it is and makes the next qspec_check_status return
+ * QSPEC_ERR_INVALID_ARG.  The pages of the tree must belong to one sequence only.  Bit-exact.
+ */
+qspec_status qspec_kv_compact(const qspec_kv_cache* caches, int32_t n_caches, const qspec_kv_batch* batch, const int32_t* nodes,
+                              const int32_t* count, int32_t T, int32_t first, qspec_stream_t stream);
+
+/*
  * qspec_logits_adjust -- penalties for repeated tokens, biases and a grammar mask on the logits of a verify
  * call (or of plain decoding: rows = 1).  Row i of sequence b scores the token after its history and its
  * first i draft tokens, so those count as history there:

@@ -61,6 +61,9 @@ SIGNATURES = {
     "qspec_kv_attention": (ctypes.c_int, [_P, _P, _P, _I64, _I32, ctypes.c_float, _I32, _P, _P, _I64, _P, _P,
                                           ctypes.c_size_t, _P]),
     "qspec_logits_adjust": (ctypes.c_int, [_P, _I32, _I32, _I32, _P, _P, _I64, _P, _P, _P, _P, _P, _I32, _P, _P, _P]),
+    "qspec_kv_pages": (ctypes.c_int, [_P, _P, _I32, _I32, _P, _P, _P, _I32, _I32, _P, _I64, _I32, _P, _P, _P, _P, _P, _P, _P]),
+    "qspec_kv_copy_pages": (ctypes.c_int, [_P, _I32, _P, _P, _P, _I32, _P]),
+    "qspec_kv_compact": (ctypes.c_int, [_P, _I32, _P, _P, _P, _I32, _I32, _P]),
     "qspec_check_status": (ctypes.c_int, [_P, _P]),
     "qspec_copy": (ctypes.c_int, [_P, _P, ctypes.c_size_t, _P]),
     "qspec_status_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -637,6 +640,66 @@ def qspec_kv_attention(cache, batch, q, out, ws, scale=None, window=0, tree=None
            load().qspec_kv_attention(cache.ref, batch.ref(T), qp, qs, hq,
                                      cache.dim ** -0.5 if scale is None else float(scale), window, _ptr(tree), op, os_,
                                      _ptr(lse), _ptr(ws), ws.numel(), _stream(stream)))
+
+
+class KVLayers:
+    """The caches of a model's layers, which share page tables: KVCaches of one shape."""
+
+    def __init__(self, caches):
+        self.caches = list(caches)
+        if not self.caches:
+            raise ValueError("at least one cache")
+        self.arr = (KVCacheDesc * len(self.caches))(*[c.desc for c in self.caches])
+        self.n, self.page, self.ref = len(self.caches), self.caches[0].page, ctypes.addressof(self.arr)
+
+
+def _layers(caches):
+    """(address, number, page) of the descriptors of a KVCache or KVLayers."""
+    return (caches.ref, caches.n if isinstance(caches, KVLayers) else 1, caches.page)
+
+
+def qspec_kv_pages(pages, room, keep, need, refs, page, new_pages, new_refs, copy_src, copy_dst, copy_len, left, parent=None,
+                   stream=None):
+    """The next step's page tables: new row r (of new_pages [R, W]) keeps keep[r] positions of row parent[r] (r when omitted) of
+    pages and has room for need[r]; refs / new_refs [n_pages] count each page's holders (may be one tensor), and
+    (copy_src, copy_dst, copy_len) [R] say what qspec_kv_copy_pages has to copy.  left [1]: free pages, or minus those that lack."""
+    for name, t in (("pages", pages), ("room", room), ("keep", keep), ("need", need), ("refs", refs), ("new_pages", new_pages),
+                    ("new_refs", new_refs), ("copy_src", copy_src), ("copy_dst", copy_dst), ("copy_len", copy_len),
+                    ("left", left), ("parent", parent)):
+        _dt(t, _int32, name)
+    if pages.dim() != 2 or new_pages.dim() != 2:
+        raise ValueError("pages and new_pages must be [rows, max_pages]")
+    (B, W), (R, NW), n_pages = pages.shape, new_pages.shape, refs.numel()
+    _need(room, B, "room"); _need(keep, R, "keep"); _need(need, R, "need"); _need(new_refs, n_pages, "new_refs"); _need(left, 1, "left")
+    _need(copy_src, R, "copy_src"); _need(copy_dst, R, "copy_dst"); _need(copy_len, R, "copy_len"); _need(parent, R, "parent")
+    _check("qspec_kv_pages",
+           load().qspec_kv_pages(_ptr(pages) or None, _ptr(room) or None, B, W, _ptr(parent) or None, _ptr(keep) or None,
+                                 _ptr(need) or None, R, NW, _ptr(refs), n_pages, _arg32(page, "page"), _ptr(new_pages) or None,
+                                 _ptr(new_refs), _ptr(copy_src) or None, _ptr(copy_dst) or None, _ptr(copy_len) or None,
+                                 _ptr(left), _stream(stream)))
+
+
+def qspec_kv_copy_pages(caches, src, dst, lengths=None, stream=None):
+    """Page src[i] -> dst[i] (int32; src < 0: none) in a KVCache or all of a KVLayers: scales and the first lengths[i] slots (all)."""
+    _dt(src, _int32, "src"); _dt(dst, _int32, "dst"); _dt(lengths, _int32, "lengths")
+    n = src.numel()
+    _need(dst, n, "dst"); _need(lengths, n, "lengths")
+    ref, layers, _ = _layers(caches)
+    _check("qspec_kv_copy_pages", load().qspec_kv_copy_pages(ref, layers, _ptr(src), _ptr(dst), _ptr(lengths), n, _stream(stream)))
+
+
+def qspec_kv_compact(caches, batch, nodes, count, first=1, stream=None):
+    """The accepted nodes (int32 [B, T], count [B] of them) of the tree that the batch's append wrote, `first` tokens behind each
+    sequence's first new one, move behind it: in a KVCache or all of a KVLayers."""
+    _dt(nodes, _int32, "nodes"); _dt(count, _int32, "count")
+    B, T = nodes.shape
+    if B < batch.desc.B:
+        raise ValueError(f"nodes must be [{batch.desc.B}, T]")
+    _need(count, batch.desc.B, "count")
+    ref, layers, _ = _layers(caches)
+    tokens = batch.desc.max_tok * batch.desc.B  # (the call reads no tokens: an upper bound of their number)
+    _check("qspec_kv_compact", load().qspec_kv_compact(ref, layers, batch.ref(tokens), _ptr(nodes), _ptr(count), T,
+                                                       _arg32(first, "first"), _stream(stream)))
 
 
 def qspec_logits_adjust(logits, out, draft_tok=None, hist=None, hist_len=None, prompt_len=None, penalties=None,
