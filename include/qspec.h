@@ -599,6 +599,34 @@ qspec_status qspec_kv_attention(const qspec_kv_cache* cache, const qspec_kv_batc
  */
 
 /*
+ * qspec_beam_select -- the n best continuations of each sequence's beams, by summed log probability:
+ *     S(k, v) = scores[b,k] + (logit[b,k,v] - ln sum_v exp(logit[b,k,v]))     for every beam k and token v
+ *     done[b,k] != 0: the beam offers itself alone, S = scores[b,k] with token end_tok
+ * The n largest S(k, v) * weights[b,k], largest first; equal ones in the order of the beams, a beam's own offers in the order of
+ * its logits, equal logits in the order of the tokens.  (weights: 1 / length penalty, for beams of different lengths.)
+ *     parent = b * beams + k (a row of logits, and of what qspec_kv_pages and qspec_gather_rows reorder),  tok = v,  score = S
+ * Where fewer than n are possible the rest are parent = tok = -1, score = -inf.  Logits of -inf and beams whose score is -inf
+ * offer nothing (the logits of such a beam and of a finished one are not read).
+ *
+ *   logits [B, beams, V] bf16 (16-byte aligned);  scores [B, beams] fp32;  done [B, beams] int32 or NULL: none;
+ *   weights [B, beams] fp32 or NULL: 1;  parent, tok [B, n] int32, score [B, n] fp32 (outputs)
+ *   ws, ws_bytes  device workspace, >= qspec_beam_workspace_size(B, beams, V, n), zero-filled before its first use and left ready for
+ *          the next call of the same shape; calls that can overlap need one each
+ *   1 <= beams <= QSPEC_BEAM_MAX_BEAMS, 1 <= n <= min(QSPEC_BEAM_MAX_N, beams * V), 2 <= V <= 2^24, B <= 65535,
+ *   B*beams*V < 2^40; the other arrays 4-byte aligned
+ * Sums of exponentials are fp32 by trees of at most 2^15 terms and fp64 beyond, log probabilities and comparisons fp64, score is
+ * rounded to fp32 once; so two candidates of different beams can change places only where S is equal to about 1e-7.
+ * A beam with a NaN or +inf among its logits, a score that is NaN or +inf, or a weight that is not positive and finite offers
+ * nothing and makes the next qspec_check_status return QSPEC_ERR_INVALID_ARG.
+ */
+#define QSPEC_BEAM_MAX_BEAMS 32
+#define QSPEC_BEAM_MAX_N 64
+size_t qspec_beam_workspace_size(int32_t B, int32_t beams, int32_t V, int32_t n);
+qspec_status qspec_beam_select(const uint16_t* logits, const float* scores, const int32_t* done, int32_t end_tok,
+                               const float* weights, int32_t B, int32_t beams, int32_t V, int32_t n, int32_t* parent,
+                               int32_t* tok, float* score, void* ws, size_t ws_bytes, qspec_stream_t stream);
+
+/*
  * qspec_kv_pages -- the page tables of the next step: rows fork, move, shorten, grow, end or begin, in one call.
  * Row b of the old table holds ceil(room[b] / page) pages, pages[b, 0 ...].  Row r of the new one keeps the first keep[r]
  * positions of row parent[r] and has room for need[r] positions.  refs[p] counts who holds page p: each row that has it

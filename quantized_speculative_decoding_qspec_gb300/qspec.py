@@ -61,6 +61,8 @@ SIGNATURES = {
     "qspec_kv_attention": (ctypes.c_int, [_P, _P, _P, _I64, _I32, ctypes.c_float, _I32, _P, _P, _I64, _P, _P,
                                           ctypes.c_size_t, _P]),
     "qspec_logits_adjust": (ctypes.c_int, [_P, _I32, _I32, _I32, _P, _P, _I64, _P, _P, _P, _P, _P, _I32, _P, _P, _P]),
+    "qspec_beam_workspace_size": (ctypes.c_size_t, [_I32, _I32, _I32, _I32]),
+    "qspec_beam_select": (ctypes.c_int, [_P, _P, _P, _I32, _P, _I32, _I32, _I32, _I32, _P, _P, _P, _P, ctypes.c_size_t, _P]),
     "qspec_kv_pages": (ctypes.c_int, [_P, _P, _I32, _I32, _P, _P, _P, _I32, _I32, _P, _I64, _I32, _P, _P, _P, _P, _P, _P, _P]),
     "qspec_kv_copy_pages": (ctypes.c_int, [_P, _I32, _P, _P, _P, _I32, _P]),
     "qspec_kv_compact": (ctypes.c_int, [_P, _I32, _P, _P, _P, _I32, _I32, _P]),
@@ -640,6 +642,35 @@ def qspec_kv_attention(cache, batch, q, out, ws, scale=None, window=0, tree=None
            load().qspec_kv_attention(cache.ref, batch.ref(T), qp, qs, hq,
                                      cache.dim ** -0.5 if scale is None else float(scale), window, _ptr(tree), op, os_,
                                      _ptr(lse), _ptr(ws), ws.numel(), _stream(stream)))
+
+
+def qspec_beam_workspace_size(B, beams, V, n):
+    return int(load().qspec_beam_workspace_size(B, beams, V, n))
+
+
+def new_beam_workspace(B, beams, V, n, device="cuda"):
+    """A zero-filled beam-selection workspace (zero once; calls of this shape keep it ready)."""
+    size = qspec_beam_workspace_size(B, beams, V, n)
+    if size == 0:
+        raise ValueError("invalid beam shape")
+    return torch.zeros(size, dtype=torch.uint8, device=device)
+
+
+def qspec_beam_select(logits, scores, parent, tok, score, ws, done=None, end_tok=0, weights=None, stream=None):
+    """The n best of each sequence's beams times tokens: logits bf16 [B, beams, V], scores fp32 [B, beams] (summed log probabilities)
+    -> parent (row of logits), tok int32 [B, n], score fp32 [B, n].  done int32 [B, beams]: finished beams, which offer end_tok at
+    their own score; weights fp32 [B, beams]: candidates compare by score times weight."""
+    _dt(logits, _bf16, "logits"); _dt(scores, _f32, "scores"); _dt(parent, _int32, "parent"); _dt(tok, _int32, "tok")
+    _dt(score, _f32, "score"); _dt(done, _int32, "done"); _dt(weights, _f32, "weights"); _dt(ws, torch.uint8, "ws")
+    B, K, V = logits.shape
+    if parent.dim() != 2 or parent.shape[0] != B:
+        raise ValueError(f"parent must be [{B}, n]")
+    n = parent.shape[1]
+    _need(scores, B * K, "scores"); _need(done, B * K, "done"); _need(weights, B * K, "weights")
+    _need(tok, B * n, "tok"); _need(score, B * n, "score")
+    _check("qspec_beam_select",
+           load().qspec_beam_select(_ptr(logits), _ptr(scores), _ptr(done), _arg32(end_tok, "end_tok"), _ptr(weights), B, K, V, n,
+                                    _ptr(parent), _ptr(tok), _ptr(score), _ptr(ws), ws.numel(), _stream(stream)))
 
 
 class KVLayers:
