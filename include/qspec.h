@@ -684,6 +684,30 @@ qspec_status qspec_kv_compact(const qspec_kv_cache* caches, int32_t n_caches, co
                               const int32_t* count, int32_t T, int32_t first, qspec_stream_t stream);
 
 /*
+ * qspec_kv_attention_shared -- qspec_kv_attention for sequences that share a prefix, which is read and multiplied once for all of
+ * them.  Group g is the sequences cu_seq[g] .. cu_seq[g+1] - 1; the first len[g] cache positions of all of them hold the same
+ * tokens, and are read through the page table of the group's first sequence that has new tokens.  (A group of one sequence, or
+ * of any sequences with len = 0, is plain attention.)  len[g] may exceed what its sequences have in common with their new tokens
+ * taken off: the prefix ends where the new tokens of one of them begin, at the latest.
+ *   cu_seq [n_groups+1] int32, non-decreasing within [0, B];  len [n_groups] int32 (both DEVICE, 4-byte aligned)
+ *   max_tok: at least the largest number of new tokens of one group, at most T.  1 <= n_groups <= QSPEC_KV_MAX_GROUPS
+ * Arguments, masks, outputs and limits otherwise as for qspec_kv_attention, whose workspace serves both calls.  Sequences of
+ * no group are not computed, their outputs not written.  A group with a sequence whose numbers are out of range (or more than max_tok
+ * new tokens, or a len outside [0, max_pages * page]) is left out, all groups if cu_seq is out of order, and the next
+ * qspec_check_status returns QSPEC_ERR_INVALID_ARG.
+ */
+#define QSPEC_KV_MAX_GROUPS 512
+typedef struct {
+  const int32_t* cu_seq;
+  const int32_t* len;
+  int32_t n_groups, max_tok;
+} qspec_kv_prefixes;
+qspec_status qspec_kv_attention_shared(const qspec_kv_cache* cache, const qspec_kv_batch* batch, const qspec_kv_prefixes* prefixes,
+                                       const uint16_t* q, int64_t q_token, int32_t heads_q, float scale, int32_t window,
+                                       const uint64_t* tree, uint16_t* out, int64_t out_token, float* lse, void* ws,
+                                       size_t ws_bytes, qspec_stream_t stream);
+
+/*
  * qspec_logits_adjust -- penalties for repeated tokens, biases and a grammar mask on the logits of a verify
  * call (or of plain decoding: rows = 1).  Row i of sequence b scores the token after its history and its
  * first i draft tokens, so those count as history there:

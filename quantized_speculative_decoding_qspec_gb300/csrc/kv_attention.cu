@@ -16,24 +16,41 @@ int max_grid(int ctas_per_sm) {
   return n < kMaxGrid ? n : kMaxGrid;
 }
 
-template <int D, int RG>
+// kShared: `a` has groups of sequences, otherwise their items are the sequences'.
+template <int D, int RG, bool kShared>
 qspec_status launch_decode(AttArgs& a, int64_t rows, cudaStream_t s) {
-  using C = DecodeCfg<D, RG>;
+  using C = DecodeCfg<D, RG, kShared>;
   a.max_tiles = static_cast<int>((rows + C::kRows - 1) / C::kRows);
-  if (cudaFuncSetAttribute(decode_kernel<D, RG>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::smem(QSPEC_KV_MAX_B)) != cudaSuccess)
+  const int owners = kShared ? a.groups : a.b.B, most = kShared ? QSPEC_KV_MAX_GROUPS : QSPEC_KV_MAX_B;
+  if (cudaFuncSetAttribute(decode_kernel<D, RG, kShared>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::smem(most)) != cudaSuccess)
     return QSPEC_ERR_CUDA;
-  return launch_pdl(decode_kernel<D, RG>, dim3(max_grid(C::ctas(a.b.B))), dim3(C::kThreads), C::smem(a.b.B), s, a);
+  return launch_pdl(decode_kernel<D, RG, kShared>, dim3(max_grid(C::ctas(owners))), dim3(C::kThreads), C::smem(owners), s, a);
 }
 
-template <int D, bool kBigPages>
+template <int D, bool kBigPages, bool kShared>
 qspec_status launch_prefill(AttArgs& a, int64_t rows, cudaStream_t s) {
   using C = PrefillCfg<D>;
   a.max_tiles = static_cast<int>((rows + C::kRows - 1) / C::kRows);
-  const size_t smem = C::kSmem + sizeof(int2) * (a.b.B + 1);
-  if (cudaFuncSetAttribute(prefill_kernel<D, kBigPages>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           C::kSmem + static_cast<int>(sizeof(int2)) * (QSPEC_KV_MAX_B + 1)) != cudaSuccess)
+  const int owners = kShared ? a.groups : a.b.B, most = kShared ? QSPEC_KV_MAX_GROUPS : QSPEC_KV_MAX_B;
+  const int fixed = kShared ? C::kSmemShared : C::kSmem, each = sizeof(int2);
+  if (cudaFuncSetAttribute(prefill_kernel<D, kBigPages, kShared>, cudaFuncAttributeMaxDynamicSharedMemorySize, fixed + each * (most + 1)) !=
+      cudaSuccess)
     return QSPEC_ERR_CUDA;
-  return launch_pdl(prefill_kernel<D, kBigPages>, dim3(max_grid(1)), dim3(C::kThreads), smem, s, a);
+  return launch_pdl(prefill_kernel<D, kBigPages, kShared>, dim3(max_grid(1)), dim3(C::kThreads), fixed + each * (owners + 1), s, a);
+}
+
+template <bool kShared>
+qspec_status launch(AttArgs& a, int64_t rows, cudaStream_t s) {
+  const bool d128 = a.c.dim == 128;
+  // Up to 64 rows a key head the decode kernel reads a sequence's keys twice at most and wins everywhere (16
+  // sequences of 4096, 64 rows: 71 against 77 us; one of 32768: 51 against 94); with 96 rows and more it reads them three
+  // times and computes on the legacy tensor path (128 rows: 119 against 78 us).
+  if (rows > 64) {
+    if (a.c.page >= 64) return d128 ? launch_prefill<128, true, kShared>(a, rows, s) : launch_prefill<64, true, kShared>(a, rows, s);
+    return d128 ? launch_prefill<128, false, kShared>(a, rows, s) : launch_prefill<64, false, kShared>(a, rows, s);
+  }
+  if (d128) return rows <= 16 ? launch_decode<128, 1, kShared>(a, rows, s) : launch_decode<128, 2, kShared>(a, rows, s);
+  return rows <= 16 ? launch_decode<64, 1, kShared>(a, rows, s) : launch_decode<64, 2, kShared>(a, rows, s);
 }
 
 }  // namespace
@@ -48,10 +65,12 @@ extern "C" size_t qspec_kv_attention_workspace_size(void) {
   return kTicketBytes + (few > many ? few : many);
 }
 
-extern "C" qspec_status qspec_kv_attention(const qspec_kv_cache* cache, const qspec_kv_batch* batch, const uint16_t* q,
-                                           int64_t q_token, int32_t heads_q, float scale, int32_t window,
-                                           const uint64_t* tree, uint16_t* out, int64_t out_token, float* lse, void* ws,
-                                           size_t ws_bytes, qspec_stream_t stream) {
+namespace {
+
+// Checks that both calls share; fills `a`.  rows: query rows a key head of `owners` sequences or groups of most_tok tokens at most.
+qspec_status prepare(const qspec_kv_cache* cache, const qspec_kv_batch* batch, const uint16_t* q, int64_t q_token, int32_t heads_q,
+                     float scale, int32_t window, const uint64_t* tree, uint16_t* out, int64_t out_token, float* lse, void* ws,
+                     size_t ws_bytes, int64_t owners, int64_t most_tok, AttArgs& a, int64_t& rows) {
   const float scale_log2 = scale * 1.44269504088896f;
   if (!q || !out || heads_q <= 0 || !isfinite(scale_log2) || window < 0) return QSPEC_ERR_INVALID_ARG;
   qspec_status st = check_kv(cache, batch);
@@ -63,9 +82,9 @@ extern "C" qspec_status qspec_kv_attention(const qspec_kv_cache* cache, const qs
   if ((st = check_rows(out, batch->T, row, out_token)) != QSPEC_OK) return st;
   if ((tree && (reinterpret_cast<uintptr_t>(tree) & 7u)) || !aligned4(lse) || !aligned16(ws)) return QSPEC_ERR_MISALIGNED;
   if (!ws || ws_bytes < qspec_kv_attention_workspace_size()) return QSPEC_ERR_WORKSPACE;
-  const int64_t rows = static_cast<int64_t>(batch->max_tok) * (heads_q / cache->heads);
-  if (rows > 0x7FFFFF00 || batch->B * ((rows + 15) / 16) >= (int64_t(1) << 30)) return QSPEC_ERR_UNSUPPORTED_SHAPE;
-  AttArgs a{*cache, *batch, q, out, lse, reinterpret_cast<const unsigned long long*>(tree), linear_error_word()};
+  rows = most_tok * (heads_q / cache->heads);
+  if (rows > 0x7FFFFF00 || owners * ((rows + 15) / 16) >= (int64_t(1) << 30)) return QSPEC_ERR_UNSUPPORTED_SHAPE;
+  a = AttArgs{*cache, *batch, q, out, lse, reinterpret_cast<const unsigned long long*>(tree), linear_error_word()};
   if (!a.err) return QSPEC_ERR_CUDA;
   a.tickets = static_cast<unsigned int*>(ws);
   a.partial = reinterpret_cast<float*>(static_cast<char*>(ws) + kTicketBytes);
@@ -79,14 +98,38 @@ extern "C" qspec_status qspec_kv_attention(const qspec_kv_cache* cache, const qs
   a.group_shift = 31 + shift;
   a.group_mul = static_cast<uint32_t>(((uint64_t(1) << a.group_shift) + a.group - 1) / a.group);
   a.scale_log2 = scale_log2;
-  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  // Up to 64 rows a key head the decode kernel reads a sequence's keys twice at most and wins everywhere (16
-  // sequences of 4096, 64 rows: 71 against 77 us; one of 32768: 51 against 94); with 96 rows and more it reads them three
-  // times and computes on the legacy tensor path (128 rows: 119 against 78 us).
-  if (rows > 64) {
-    if (cache->page >= 64) return cache->dim == 128 ? launch_prefill<128, true>(a, rows, s) : launch_prefill<64, true>(a, rows, s);
-    return cache->dim == 128 ? launch_prefill<128, false>(a, rows, s) : launch_prefill<64, false>(a, rows, s);
-  }
-  if (cache->dim == 128) return rows <= 16 ? launch_decode<128, 1>(a, rows, s) : launch_decode<128, 2>(a, rows, s);
-  return rows <= 16 ? launch_decode<64, 1>(a, rows, s) : launch_decode<64, 2>(a, rows, s);
+  return QSPEC_OK;
+}
+
+}  // namespace
+
+extern "C" qspec_status qspec_kv_attention(const qspec_kv_cache* cache, const qspec_kv_batch* batch, const uint16_t* q,
+                                           int64_t q_token, int32_t heads_q, float scale, int32_t window,
+                                           const uint64_t* tree, uint16_t* out, int64_t out_token, float* lse, void* ws,
+                                           size_t ws_bytes, qspec_stream_t stream) {
+  AttArgs a;
+  int64_t rows;
+  const qspec_status st = prepare(cache, batch, q, q_token, heads_q, scale, window, tree, out, out_token, lse, ws, ws_bytes,
+                                  batch ? batch->B : 0, batch ? batch->max_tok : 0, a, rows);
+  if (st != QSPEC_OK) return st;
+  return launch<false>(a, rows, reinterpret_cast<cudaStream_t>(stream));
+}
+
+extern "C" qspec_status qspec_kv_attention_shared(const qspec_kv_cache* cache, const qspec_kv_batch* batch,
+                                                  const qspec_kv_prefixes* prefixes, const uint16_t* q, int64_t q_token,
+                                                  int32_t heads_q, float scale, int32_t window, const uint64_t* tree, uint16_t* out,
+                                                  int64_t out_token, float* lse, void* ws, size_t ws_bytes, qspec_stream_t stream) {
+  if (!prefixes || !prefixes->cu_seq || !prefixes->len || prefixes->n_groups <= 0 || prefixes->max_tok <= 0) return QSPEC_ERR_INVALID_ARG;
+  AttArgs a;
+  int64_t rows;
+  const qspec_status st = prepare(cache, batch, q, q_token, heads_q, scale, window, tree, out, out_token, lse, ws, ws_bytes,
+                                  prefixes->n_groups, prefixes->max_tok, a, rows);
+  if (st != QSPEC_OK) return st;
+  if (prefixes->n_groups > QSPEC_KV_MAX_GROUPS || prefixes->max_tok > batch->T) return QSPEC_ERR_UNSUPPORTED_SHAPE;
+  if (!aligned4(prefixes->cu_seq) || !aligned4(prefixes->len)) return QSPEC_ERR_MISALIGNED;
+  a.cu_seq = prefixes->cu_seq;
+  a.prefix = prefixes->len;
+  a.groups = prefixes->n_groups;
+  a.group_tok = prefixes->max_tok;
+  return launch<true>(a, rows, reinterpret_cast<cudaStream_t>(stream));
 }

@@ -20,14 +20,16 @@
 //    the fragment loads are free of bank conflicts (see copy_step).
 // With more than 16 rows a second set of four warps takes the next 16 and the two warps of a key group share
 // their stages.  Each warp sums its own keys; the sums meet in shared memory once per item.
+// kShared: items of groups that share a prefix (kv_shared.cuh).  A key tile's segment decides whose page table it lies in
+// and which rows see it.
 #pragma once
 
-#include "kv_sched.cuh"
+#include "kv_shared.cuh"
 
 namespace qspec {
 namespace att {
 
-template <int D, int RG>
+template <int D, int RG, bool kShared = false>
 struct DecodeCfg {
   static constexpr int kRows = 16 * RG;
   static constexpr int kKeys = 64;
@@ -39,8 +41,11 @@ struct DecodeCfg {
   static constexpr int kRowPad = D + (D / 32) * 4 * (D == 128 ? 1 : 2);  // floats of a merge row: conflict-free
   static constexpr int kMerge = 4 * RG * 16 * kRowPad * 4;               // takes the ring's place between items
   // the warps' maxima and sums, the walk, the scan, flags
-  static constexpr int kState = 4 * RG * 16 * 8 + sizeof(Walk<kRows, kKeys>) + sizeof(ScanShared) + 16;
+  using W = typename WalkOf<kShared, kRows, kKeys>::type;
+  static constexpr int kPlan = kShared ? static_cast<int>(sizeof(Plan) + 8 + sizeof(int4) * (kRows + 1)) : 0;
+  static constexpr int kState = 4 * RG * 16 * 8 + sizeof(W) + sizeof(ScanShared) + 16 + kPlan;
   static constexpr int kSmem = 128 + (kRing > kMerge ? kRing : kMerge) + RG * D * 32 + kState;
+  // B: sequences, or groups of them
   static constexpr int smem(int B) { return kSmem + static_cast<int>(sizeof(int2)) * (B + 1); }
   // CTAs that an SM's shared memory holds beside each other: with the table of many sequences one less.  (Heads of 128,
   // up to 16 rows: three from 377 sequences on.  A grid of more leaves the rest of its equal runs to a second, mostly
@@ -59,9 +64,10 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], const uint4& a, uint32_t 
       : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
 }
 
-template <int D, int RG>
+template <int D, int RG, bool kShared = false>
 __global__ void __launch_bounds__(DecodeCfg<D, RG>::kThreads, DecodeCfg<D, RG>::kCtas) decode_kernel(const AttArgs a) {
-  using C = DecodeCfg<D, RG>;
+  using C = DecodeCfg<D, RG, kShared>;
+  using W = typename C::W;
   using namespace ptx;
   constexpr int kRows = C::kRows, kKeys = C::kKeys, kS = C::kStages, kSide = C::kSide, kPad = C::kRowPad;
   constexpr int kTiles = D / 8;    // n8 tiles of the output
@@ -71,17 +77,19 @@ __global__ void __launch_bounds__(DecodeCfg<D, RG>::kThreads, DecodeCfg<D, RG>::
   float* merge = reinterpret_cast<float*>(ring);  // [4 RG warps][16][kPad], between items
   uint4* qfrag = reinterpret_cast<uint4*>(ring + (C::kRing > C::kMerge ? C::kRing : C::kMerge));  // [RG][D / 16][32]
   float2* ml = reinterpret_cast<float2*>(qfrag + RG * D * 2);  // [4 RG][16] running maximum and sum of each warp's rows
-  Walk<kRows, kKeys>* walk = reinterpret_cast<Walk<kRows, kKeys>*>(ml + 4 * RG * 16);
+  W* walk = reinterpret_cast<W*>(ml + 4 * RG * 16);
   ScanShared* scan = reinterpret_cast<ScanShared*>(walk + 1);
   int* flags = reinterpret_cast<int*>(scan + 1);  // more items; last to arrive
-  int2* seq = reinterpret_cast<int2*>(flags + 4);
+  Plan* plan = reinterpret_cast<Plan*>(flags + 4);                    // of the item's stream (kShared), and its segments
+  int4* seg = reinterpret_cast<int4*>((reinterpret_cast<uintptr_t>(plan + 1) + 15) & ~uintptr_t(15));
+  int2* seq = kShared ? reinterpret_cast<int2*>(seg + kRows + 1) : reinterpret_cast<int2*>(flags + 4);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   grid_launch_dependents();
   grid_dependency_wait();
   long long run0, run1;
   {
-    Walk<kRows, kKeys> w;
+    W w;
     share_out<C::kThreads>(a, seq, scan, w);
     run0 = w.u;
     run1 = w.u1;
@@ -92,7 +100,15 @@ __global__ void __launch_bounds__(DecodeCfg<D, RG>::kThreads, DecodeCfg<D, RG>::
   uint8_t* const my_ring = ring + kw * kS * 2 * kSide;
 
   while (true) {
-    if (threadIdx.x == 0) flags[0] = walk->next();
+    if constexpr (kShared) {
+      if (warp == 0) {
+        const bool more = walk_next(walk);
+        if (lane == 0) flags[0] = more;
+        if (more) make_plan<kKeys>(walk, plan, seg);
+      }
+    } else {
+      if (threadIdx.x == 0) flags[0] = walk->next();
+    }
     __syncthreads();
     if (!flags[0]) break;
     const Item& it = walk->it;
@@ -101,9 +117,44 @@ __global__ void __launch_bounds__(DecodeCfg<D, RG>::kThreads, DecodeCfg<D, RG>::
     // ---- the warp's stream of key groups
     // Lane l holds page and exponents of tile batch0 + l (this warp's 16 keys of it).
     int batch0 = kt0, b_page = -1, b_exps = 0, b_before = 0;  // b_before: the exponents of the batch before
+    // kShared: the tile's segment | place of the keys in their page / 16 << 8 | all rows see all keys << 16 | slots behind the
+    // end << 17
+    int b_where = 0, b_where_before = 0;
     auto load_batch = [&]() {
       b_page = -1;
       b_before = b_exps;
+      if constexpr (kShared) {
+        b_where_before = b_where;
+        int key0 = 0;
+        const int at = batch0 + lane < kt1 ? seg_of<kKeys>(seg, plan->count, batch0 + lane, key0) : -1;
+        if (at < 0) return;
+        const int4 sg = seg[at];
+        const int key = key0 + 16 * kw, table = at == 0 ? it.kv : sg.z;
+        const int all_lo = at == 0 ? plan->pre_lo : plan->one_lo, all_hi = at == 0 ? it.hi : plan->one_hi;
+        int own_lo = 0;  // positions before a window may have no page any more
+        if (a.window > 0) {
+          if (at == 0) {
+            own_lo = it.lo;
+          } else {
+            int own_hi;
+            walk->own_range(sg.z, it.tok0 + a.token_of(it.row0), it.tok0 + a.token_of(it.row0 + it.rows - 1), it.hi, own_lo, own_hi);
+          }
+        }
+        if (key < sg.w && key + 16 > own_lo) {
+          const int page = a.b.pages[static_cast<int64_t>(table) * a.b.max_pages + key / a.c.page];
+          if (page >= 0 && page < a.c.n_pages) {
+            b_page = page;
+            b_where = at | (key & (a.c.page - 1)) << 4 | (key >= all_lo && key + 16 <= all_hi) << 16 | (key + 16 > sg.w) << 17;
+            const int64_t ph = static_cast<int64_t>(page) * a.c.heads + it.head;
+            const int ek = min(max(static_cast<int>(a.c.k_exp[ph]), kKvMinExp), kKvMaxExp);
+            const int ev = min(max(static_cast<int>(a.c.v_exp[ph]), kKvMinExp), kKvMaxExp);
+            b_exps = (ek + 64) | (ev + 64) << 8;
+          } else {
+            atomicOr(a.err, kErrInvalid);
+          }
+        }
+        return;
+      }
       const long long key = (static_cast<long long>(batch0) + lane) * kKeys + 16 * kw;
       if (batch0 + lane < kt1 && key < hi && key + 16 > lo) {
         const int page = a.b.pages[static_cast<int64_t>(it.b) * a.b.max_pages + key / a.c.page];
@@ -134,7 +185,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, RG>::kThreads, DecodeCfg<D, RG>::
           any = true;
           constexpr int kPerRow = D / 16, kRowsAt = 32 / kPerRow;  // lanes to a row, rows at a time
           const int row0 = lane / kPerRow, chunk = lane % kPerRow;
-          const int slot = (kt * kKeys + 16 * kw) & (a.c.page - 1);
+          const int slot = kShared ? __shfl_sync(0xFFFFFFFFu, b_where, kt - batch0) >> 4 & 0x70 : (kt * kKeys + 16 * kw) & (a.c.page - 1);
           const int64_t at = ((static_cast<int64_t>(page) * a.c.heads + it.head) * a.c.page + slot + row0) * D + chunk * 16;
           const uint32_t dst = smem_u32(my_ring + stage * 2 * kSide);
 #pragma unroll
@@ -175,7 +226,8 @@ __global__ void __launch_bounds__(DecodeCfg<D, RG>::kThreads, DecodeCfg<D, RG>::
     int lim[2], low[2];
     unsigned long long bits[2];
     bool odd[2];  // rows with a NaN or an infinity
-    const int base = it.kv - it.n;
+    int of[2], row_base[2];  // kShared: each row's sequence, and where its new tokens begin
+    const int base = kShared ? 0 : it.kv - it.n;
     {
       uint32_t* qf = reinterpret_cast<uint32_t*>(qfrag + rg * D * 2);
 #pragma unroll
@@ -209,6 +261,14 @@ __global__ void __launch_bounds__(DecodeCfg<D, RG>::kThreads, DecodeCfg<D, RG>::
             if ((4 * h + e / 2) % 4 == kw)
               qf[((4 * h + e / 2) * 32 + lane) * 4 + r + 2 * (e & 1)] =
                   odd[r] ? 0u : pack_f16(bf16_lo(w[h][e]) * shrink, bf16_hi(w[h][e]) * shrink);
+        if constexpr (kShared) {
+          const RowSight v = row_sight(walk, it.tok0 + i, plan->seq0, plan->seq1);
+          of[r] = v.seq;
+          low[r] = v.low;
+          lim[r] = v.lim;
+          row_base[r] = v.base;
+          bits[r] = a.tree && there ? a.tree[it.tok0 + i] : 0ull;
+        } else
         if (a.tree) {
           lim[r] = it.kv;
           low[r] = 0;
@@ -221,8 +281,8 @@ __global__ void __launch_bounds__(DecodeCfg<D, RG>::kThreads, DecodeCfg<D, RG>::
       }
     }
     // positions that every row of the item sees: no masks there
-    int all_lo, all_hi;
-    {
+    int all_lo = 0, all_hi = 0;
+    if (!kShared) {
       const int i0 = a.token_of(it.row0), i1 = a.token_of(it.row0 + it.rows - 1);
       all_hi = a.tree ? max(base, 0) : min(max(base + i0 + 1, 0), it.kv);
       all_lo = window_start(base + i1, a.window);
@@ -254,7 +314,8 @@ __global__ void __launch_bounds__(DecodeCfg<D, RG>::kThreads, DecodeCfg<D, RG>::
       }
       const int exps = __shfl_sync(0xFFFFFFFFu, kt >= batch0 ? b_exps : b_before, (kt - batch0) & 31);
       const int ek = (exps & 255) - 64, ev = (exps >> 8) - 64;
-      const int key0 = kt * kKeys + 16 * kw;
+      const int where = kShared ? __shfl_sync(0xFFFFFFFFu, kt >= batch0 ? b_where : b_where_before, (kt - batch0) & 31) : 0;
+      int key0 = kt * kKeys + 16 * kw;
 
       float sc[2][2][4];  // [n tile][chain]
 #pragma unroll
@@ -285,14 +346,21 @@ __global__ void __launch_bounds__(DecodeCfg<D, RG>::kThreads, DecodeCfg<D, RG>::
       for (int t = 0; t < 2; ++t)
 #pragma unroll
         for (int e = 0; e < 4; ++e) z[t][e] = fmaf(sc[t][0][e] + sc[t][1][e], mk[e >> 1], static_cast<float>(ev));
-      if (key0 + 16 > all_hi || key0 < all_lo) {
+      if (kShared ? (where >> 16 & 1) == 0 : key0 + 16 > all_hi || key0 < all_lo) {
+        const int at = where & 255;
+        if (kShared) key0 = (seg[at].y + kt - (at > 0 ? seg[at - 1].x : 0)) * kKeys + 16 * kw;
 #pragma unroll
         for (int t = 0; t < 2; ++t)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int j = key0 + 8 * t + 2 * c + (e & 1), r = e >> 1;
             bool see = j < lim[r] && j >= low[r];
-            if (a.tree && j >= base) see = see && j - base < 64 && (bits[r] >> (j - base) & 1ull);
+            if (kShared) {
+              see = see && (at == 0 ? j < it.hi : j >= it.hi && of[r] == seg[at].z);
+              if (a.tree && j >= row_base[r]) see = see && j - row_base[r] < 64 && (bits[r] >> (j - row_base[r]) & 1ull);
+            } else if (a.tree && j >= base) {
+              see = see && j - base < 64 && (bits[r] >> (j - base) & 1ull);
+            }
             if (!see) z[t][e] = -INFINITY;
           }
       }
@@ -345,10 +413,16 @@ __global__ void __launch_bounds__(DecodeCfg<D, RG>::kThreads, DecodeCfg<D, RG>::
           v[k][1] = x.y;
         }
       }
-      if (key0 + 16 > it.kv) {  // slots behind the end hold anything, NaN codes included
+      if (kShared ? where >> 17 & 1 : key0 + 16 > it.kv) {  // slots behind the end hold anything, NaN codes included
+        int end = it.kv;
+        if (kShared) {
+          const int at = where & 255;
+          end = seg[at].w;
+          key0 = (seg[at].y + kt - (at > 0 ? seg[at - 1].x : 0)) * kKeys + 16 * kw;
+        }
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          if (key0 + 2 * c + (k & 1) + 8 * (k >> 1) >= it.kv)
+          if (key0 + 2 * c + (k & 1) + 8 * (k >> 1) >= end)
 #pragma unroll
             for (int w = 0; w < kTiles / 4; ++w) v[k][w] = 0;
       }

@@ -23,10 +23,16 @@
 // bounded and ends the CTA in order (kErrTimeout) when it runs out.
 #pragma once
 
-#include "kv_sched.cuh"
+#include "kv_shared.cuh"
 
 namespace qspec {
 namespace att {
+
+// Per 16 keys of a tile: the keys' scale, the values' exponent, its inverse scale, whether there are keys at all.
+struct TileMeta {
+  float4 group[8];
+  int whole[4];  // [0]: all eight groups have keys; kShared: and, 2, all rows see all keys; first key, end, sequence or -1
+};
 
 template <int D>
 struct PrefillCfg {
@@ -40,19 +46,24 @@ struct PrefillCfg {
   static constexpr int kHalves = D / 64;          // 128-byte wide sub-tiles
   static constexpr int kQ = 128 * D * 2;          // one tile of queries
   static constexpr int kNR = 3 * (128 / D), kNC = 3, kMeta = 8;
-  static constexpr int kSmem = 1024 + 2 * kQ + kNC * kConv + kNR * kRaw + 6144;
-};
-
-// Per 16 keys of a tile: the keys' scale, the values' exponent, its inverse scale, whether there are keys at all.
-struct TileMeta {
-  float4 group[8];
-  int whole[4];  // [0]: all eight groups have keys
+  static constexpr int kTiles = 1024 + 2 * kQ + kNC * kConv + kNR * kRaw, kState = 6144;
+  static constexpr int kSmem = kTiles + kState;
+  // kShared: a plan of the item's stream, its segments, and what each row sees.  The state as it is, as 512 groups just fit.
+  using SW = SharedWalk<kRows, kKeys>;
+  static constexpr int kBars = 2 * kNR + 2 * kNC + kMeta + 7;
+  static constexpr int kSharedState = static_cast<int>(sizeof(TileMeta) * kMeta + 8 * kBars + sizeof(ScanShared) + 16 + 16 * sizeof(SW));
+  static constexpr int kPlan = static_cast<int>(sizeof(Plan) + 8 + sizeof(int4) * (kRows + 1) + sizeof(RowSight) * kRows);
+  static constexpr int kSmemShared = kTiles + kSharedState + kPlan;
+  static_assert(kSharedState <= kState && kSmemShared + sizeof(int2) * (QSPEC_KV_MAX_GROUPS + 1) <= 227 * 1024, "shared memory");
 };
 
 // kBigPages: pages of 64 slots or more, so 64 keys lie in one page and share its scales.
-template <int D, bool kBigPages>
+// kShared: items of groups that share a prefix (kv_shared.cuh).  The copy warp alone knows the stream; what the others need of
+// a tile stands in its TileMeta.
+template <int D, bool kBigPages, bool kShared = false>
 __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1) prefill_kernel(const AttArgs a) {
   using C = PrefillCfg<D>;
+  using W = typename WalkOf<kShared, C::kRows, C::kKeys>::type;
   using namespace ptx;
   constexpr int kRows = C::kRows, kKeys = C::kKeys, kNR = C::kNR, kNC = C::kNC, kMeta = C::kMeta;
   constexpr int kSub = kKeys * 128;  // bytes of a sub-tile: 128 rows of 128 bytes
@@ -75,8 +86,11 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1) prefill_kernel(con
   ScanShared* scan = reinterpret_cast<ScanShared*>(ofree + 1);
   volatile int* flags = reinterpret_cast<volatile int*>(scan + 1);  // abort, last to arrive, abort as the item ended
   uint32_t* tmem_base = reinterpret_cast<uint32_t*>(scan + 1) + 3;
-  Walk<kRows, kKeys>* walks = reinterpret_cast<Walk<kRows, kKeys>*>(reinterpret_cast<int2*>(scan + 1) + 2);  // [16]
-  int2* seq = reinterpret_cast<int2*>(walks + 16);
+  W* walks = reinterpret_cast<W*>(reinterpret_cast<int2*>(scan + 1) + 2);  // [16]
+  Plan* plan = reinterpret_cast<Plan*>(walks + 16);  // (the copy warp's)
+  int4* seg = reinterpret_cast<int4*>((reinterpret_cast<uintptr_t>(plan + 1) + 15) & ~uintptr_t(15));
+  RowSight* row_sees = reinterpret_cast<RowSight*>(seg + kRows + 1);
+  int2* seq = kShared ? reinterpret_cast<int2*>(row_sees + kRows) : reinterpret_cast<int2*>(walks + 16);
   volatile int* abort_flag = flags;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -107,10 +121,10 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1) prefill_kernel(con
   grid_launch_dependents();
   grid_dependency_wait();
   tc_fence_before();
-  Walk<kRows, kKeys>* walk = walks + warp;  // (in shared memory: its state would cost every role 40 registers)
+  W* walk = walks + warp;  // (in shared memory: its state would cost every role 40 registers)
   long long run0, run1;
   {
-    Walk<kRows, kKeys> w;
+    W w;
     share_out<C::kThreads>(a, seq, scan, w);  // (barriers inside)
     run0 = w.u;
     run1 = w.u1;
@@ -181,8 +195,11 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1) prefill_kernel(con
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(qfull);
-      int all_lo, all_hi;  // positions that every row of the item sees
-      {
+      int all_lo = 0, all_hi = 0;  // positions that every row of the item sees
+      if constexpr (kShared) {
+        const int token = a.token_of(it.row0 + (there ? row : 0));
+        row_sees[row] = row_sight(walk, it.tok0 + token, walk->grp[it.b].x, walk->grp[it.b + 1].x);  // (its own thread reads it)
+      } else {
         const int i0 = a.token_of(it.row0), i1 = a.token_of(it.row0 + it.rows - 1), base = it.kv - it.n;
         all_hi = a.tree ? max(base, 0) : min(max(base + i0 + 1, 0), it.kv);
         all_lo = window_start(base + i1, a.window);
@@ -193,8 +210,17 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1) prefill_kernel(con
         int base, lim, low;
         unsigned long long bits;
       };
-      auto sight = [&]() {
+      auto sight = [&](const TileMeta& md) {
         Sight v;
+        if (kShared) {
+          const RowSight r = row_sees[row];
+          const int s = md.whole[3];
+          v.base = r.base;
+          v.lim = s < 0 ? md.whole[2] : s == r.seq ? r.lim : 0;
+          v.low = s < 0 ? r.low : max(r.low, it.hi);
+          v.bits = a.tree && there ? a.tree[it.tok0 + a.token_of(it.row0 + row)] : 0ull;
+          return v;
+        }
         const int token = a.token_of(it.row0 + (row < it.rows ? row : 0));
         v.base = it.kv - it.n;
         v.lim = a.tree ? it.kv : min(max(v.base + token + 1, 0), it.kv);
@@ -229,14 +255,14 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1) prefill_kernel(con
             ge[g] = v.y;
             gu[g] = v.z;
           }
-          const bool whole_tile = md.whole[0] != 0;
+          const bool whole_tile = (md.whole[0] & 1) != 0;
           ok = ok && wait_bar(sfull + X, ns & 1, abort_flag, a.err);
           ok = __all_sync(0xFFFFFFFFu, ok);
           if (!ok) break;
           ++ns;
           tc_fence_after();
-          const int key0 = (kt0 + n) * kKeys;
-          const bool plain = key0 + kKeys <= all_hi && key0 >= all_lo && whole_tile;
+          const int key0 = kShared ? md.whole[1] : (kt0 + n) * kKeys;
+          const bool plain = kShared ? md.whole[0] == 3 : key0 + kKeys <= all_hi && key0 >= all_lo && whole_tile;
           float top = -INFINITY;
           float s[4][32];
           if (plain) {
@@ -265,7 +291,7 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1) prefill_kernel(con
               }
             }
           } else {
-            const Sight v = sight();
+            const Sight v = sight(md);
 #pragma unroll 1
             for (int g = 0; g < 8; ++g) {
               float sg[16];
@@ -324,7 +350,7 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1) prefill_kernel(con
               if (f >= 0 && f % 16 == 15) tmem_st16(ts + f / 16 * 16, p);
             }
           } else {
-            const Sight v = sight();
+            const Sight v = sight(md);
 #pragma unroll 1
             for (int g = 0; g < 8; ++g) {
               float sg[16];
@@ -487,7 +513,7 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1) prefill_kernel(con
       while (ok && walk_next(walk)) {
         const Item& it = walk->it;
         for (int kt = it.kt0; ok && kt < it.kt1; ++kt) {
-          const int kv_in = it.kv - kt * kKeys;  // slots from here on hold anything
+          int kv_in = it.kv - kt * kKeys;  // slots from here on hold anything
           for (int side = 0; side < 2; ++side, ++i) {
             const int st = i % kNR, sc = i % kNC;
             ok = ok && wait_bar(rawfull + st, (i / kNR) & 1, abort_flag, a.err);
@@ -497,9 +523,10 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1) prefill_kernel(con
             const uint8_t* src = raw + st * C::kRaw;
             uint8_t* dst = conv + sc * C::kConv;
             const TileMeta& md = meta[(i >> 1) % kMeta];
+            if (kShared) kv_in = md.whole[2] - md.whole[1];
             // a quarter warp takes two keys; D = 128: the first key's chunks of one half, the second's of the other
             const int quad = lane & 3, sub = (lane >> 2) & 1;
-            const bool all = md.whole[0] != 0 && kv_in >= kKeys;
+            const bool all = (md.whole[0] & 1) != 0 && kv_in >= kKeys;
             // 16 steps of 8 keys, two or three to a warp; all loads first
             constexpr int kMine = (kKeys / 8 + C::kConvs - 1) / C::kConvs;
             uint4 w[kMine][C::kHalves];
@@ -548,10 +575,17 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1) prefill_kernel(con
       while (walk_next(walk)) {
         const Item& it = walk->it;
         SegBatch sb;
+        SharedSegs ss;
+        if constexpr (kShared) make_plan<kKeys>(walk, plan, seg);
         for (int kt = it.kt0; kt < it.kt1; ++kt, ++t) {
-          const int seg = kt * per_tile;
-          if (sb.seg0 < 0 || seg >= sb.seg0 + 32) sb = load_segs(a, it, seg, P);
-          const int l0 = seg - sb.seg0;
+          const int seg0 = kt * per_tile;
+          if (sb.seg0 < 0 || seg0 >= sb.seg0 + 32) {
+            if constexpr (kShared)
+              sb = load_shared_segs<kKeys>(a, *walk, plan, seg, seg0, per_tile, ss);
+            else
+              sb = load_segs(a, it, seg0, P);
+          }
+          const int l0 = seg0 - sb.seg0;
           const bool mine = lane >= l0 && lane < l0 + per_tile && sb.page >= 0;
           const uint32_t who = __ballot_sync(0xFFFFFFFFu, mine);
           const int64_t at = mine ? (static_cast<int64_t>(sb.page) * a.c.heads + it.head) * seg_bytes : 0;
@@ -567,7 +601,16 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1) prefill_kernel(con
               // converted slot before that was used up by an MMA that followed their PVs
               TileMeta& md = meta[t % kMeta];
               if (lane < 8) md.group[lane] = make_float4(0.0f, 0.0f, 1.0f, 0.0f);
-              if (lane == 0) md.whole[0] = __popc(who) == per_tile;
+              if (kShared) {
+                if (lane == l0) {
+                  md.whole[0] = __popc(who) != per_tile ? 0 : ss.key0 >= ss.all_lo && ss.key0 + kKeys <= ss.all_hi ? 3 : 1;
+                  md.whole[1] = ss.key0;
+                  md.whole[2] = ss.end;
+                  md.whole[3] = ss.seq;
+                }
+              } else if (lane == 0) {
+                md.whole[0] = __popc(who) == per_tile;
+              }
               __syncwarp();
               if (mine) {
                 const int g0 = (lane - l0) * (P / 16);

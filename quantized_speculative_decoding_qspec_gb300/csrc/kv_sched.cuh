@@ -43,8 +43,12 @@ struct AttArgs {
   int64_t q_token, out_token;
   int heads_q, group, window;
   uint32_t group_mul, group_shift;  // row / group = row * group_mul >> group_shift, rows below 2^31
-  int max_tiles;          // row tiles of a sequence of max_tok tokens
+  int max_tiles;          // row tiles of a sequence (a group) of max_tok tokens
   float scale_log2;       // scale * log2(e)
+  // attention over shared prefixes alone (kv_shared.cuh)
+  const int32_t* cu_seq;  // [groups + 1]
+  const int32_t* prefix;  // [groups]
+  int groups, group_tok;  // group_tok: new tokens of a group at most
 
   __device__ int token_of(int packed) const {
     return static_cast<int>(static_cast<uint64_t>(static_cast<uint32_t>(packed)) * group_mul >> group_shift);
@@ -158,8 +162,8 @@ struct Walk {
 };
 
 // A walk in shared memory, one per warp: a lane advances it, all read its item.
-template <int kRows, int kKeys>
-__device__ __forceinline__ bool walk_next(Walk<kRows, kKeys>* w) {
+template <class W>
+__device__ __forceinline__ bool walk_next(W* w) {
   __syncwarp();
   bool more = false;
   if ((threadIdx.x & 31) == 0) more = w->next();
@@ -182,30 +186,12 @@ __host__ __device__ __forceinline__ int owner_of(long long u, const ScanShared* 
   return static_cast<int>(quotient((u + 1) * sh->runs - 1, sh->total));
 }
 
-// Fills seq (all threads), shares the units out and positions the walk for this CTA.  Ends with a barrier.
-template <int kThreads, int kRows, int kKeys>
-__device__ __forceinline__ void share_out(const AttArgs& a, int2* seq, ScanShared* sh, Walk<kRows, kKeys>& w) {
-  const int B = a.b.B;
-  for (int b = threadIdx.x; b <= B; b += kThreads) {
-    if (b == B) {
-      seq[b] = make_int2(a.b.cu_tok[B], -1);
-    } else {
-      const SeqSpan s = seq_span(a.b, a.c.page, b);
-      if (!s.ok && blockIdx.x == 0) atomicOr(a.err, kErrInvalid);
-      seq[b] = make_int2(s.tok0, s.ok ? s.kv : -1);
-    }
-  }
-  __syncthreads();
-  w.seq = seq;
-  w.B = B;
-  w.heads = a.c.heads;
-  w.group = a.group;
-  w.group_mul = a.group_mul;
-  w.group_shift = a.group_shift;
-  w.window = a.window;
-  w.tree = a.tree != nullptr;
+// Shares out the units of `owners` sequences (or groups) of a.max_tiles row tiles at most, and positions the walk for this
+// CTA.  Ends with a barrier.
+template <int kThreads, class W>
+__device__ __forceinline__ void deal(const AttArgs& a, int owners, ScanShared* sh, W& w) {
   // (sequence, row tile) pairs, a run of them per thread; sequences of fewer tiles leave gaps
-  const uint32_t pairs = static_cast<uint32_t>(B) * a.max_tiles;  // (below 2^30)
+  const uint32_t pairs = static_cast<uint32_t>(owners) * a.max_tiles;  // (below 2^30)
   const uint32_t per = (pairs + kThreads - 1) / kThreads;
   const uint32_t e0 = threadIdx.x * per, e1 = min(e0 + per, pairs);
   int b = e0 < pairs ? e0 / static_cast<uint32_t>(a.max_tiles) : 0, tile = e0 - b * a.max_tiles;
@@ -255,6 +241,31 @@ __device__ __forceinline__ void share_out(const AttArgs& a, int2* seq, ScanShare
   }
   __syncthreads();
   if (w.u < w.u1) w.start(sh->b, sh->tile, sh->before);
+}
+
+// Fills seq (all threads), shares the units out and positions the walk for this CTA.  Ends with a barrier.
+template <int kThreads, int kRows, int kKeys>
+__device__ __forceinline__ void share_out(const AttArgs& a, int2* seq, ScanShared* sh, Walk<kRows, kKeys>& w) {
+  const int B = a.b.B;
+  for (int b = threadIdx.x; b <= B; b += kThreads) {
+    if (b == B) {
+      seq[b] = make_int2(a.b.cu_tok[B], -1);
+    } else {
+      const SeqSpan s = seq_span(a.b, a.c.page, b);
+      if (!s.ok && blockIdx.x == 0) atomicOr(a.err, kErrInvalid);
+      seq[b] = make_int2(s.tok0, s.ok ? s.kv : -1);
+    }
+  }
+  __syncthreads();
+  w.seq = seq;
+  w.B = B;
+  w.heads = a.c.heads;
+  w.group = a.group;
+  w.group_mul = a.group_mul;
+  w.group_shift = a.group_shift;
+  w.window = a.window;
+  w.tree = a.tree != nullptr;
+  deal<kThreads>(a, B, sh, w);
 }
 
 

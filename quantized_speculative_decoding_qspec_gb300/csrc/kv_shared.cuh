@@ -1,0 +1,325 @@
+// Attention for groups of sequences that share a prefix: what the kernels walk.
+//
+// The rows of a group and key head are the new tokens of all its sequences times the G query heads, packed as ever; an item
+// is one (group, row tile, key head).  Its keys come as one stream of tiles: first the prefix, which all its rows see and
+// which is read once for them, then what each sequence of the tile has alone, which is masked for the others' rows.  A
+// sequence's own keys are read once as well (by the row tiles that its tokens lie in); the products with the other rows cost
+// nothing where memory bounds a tile, and tiles of the tensor cores have 16 rows or 128 in any case.  So one launch does both
+// parts, the softmax of a row runs over both, and the equal runs, tickets and sums of kv_sched.cuh serve unchanged.
+#pragma once
+
+#include "kv_sched.cuh"
+
+namespace qspec {
+namespace att {
+
+// Key tiles of [lo, hi).
+template <int kKeys>
+__host__ __device__ __forceinline__ int tiles_between(int lo, int hi) {
+  return lo < hi ? (hi + kKeys - 1) / kKeys - lo / kKeys : 0;
+}
+
+// As Walk, over groups.  grp[g] = {first sequence, prefix length or -1 for a group that is left out}, g <= groups; cu and kv are
+// the batch's arrays (sequences of a group that is not left out are in order).  Of an item, b is the group, tok0 its first token,
+// n its tokens, [lo, hi) what the tile's rows see of the prefix, kv the sequence through whose pages the prefix is read; kt0 and
+// kt1 count the tiles of the item's own stream.
+template <int kRows, int kKeys>
+struct SharedWalk {
+  const int2* grp;
+  const int32_t* cu;
+  const int32_t* kv;
+  int groups, heads, group, window;
+  uint32_t group_mul, group_shift;
+  bool tree;
+  long long u, u1;
+  Item it;
+  long long first;  // units before the current (group, tile)
+  int nk;
+
+  __host__ __device__ int token_of(int packed) const {
+    return static_cast<int>(static_cast<uint64_t>(static_cast<uint32_t>(packed)) * group_mul >> group_shift);
+  }
+  // The sequence among [s0, s1) that has the token; the group has it.
+  __host__ __device__ int seq_of(int token, int s0, int s1) const {
+    while (s1 - s0 > 1) {
+      const int mid = (s0 + s1) >> 1;
+      if (cu[mid] <= token)
+        s0 = mid;
+      else
+        s1 = mid;
+    }
+    return s0;
+  }
+  // What the tokens t0 .. t1 of the step see of sequence s behind the first p positions.
+  __host__ __device__ void own_range(int s, int t0, int t1, int p, int& lo, int& hi) const {
+    const int c0 = cu[s], n = cu[s + 1] - c0;
+    key_range(max(t0 - c0, 0), min(t1 - c0, n - 1), kv[s] - n, kv[s], tree, window, lo, hi);
+    lo = min(max(lo, p), hi);
+  }
+  __host__ __device__ int tiles(int g, int& n) const {
+    n = grp[g].y < 0 ? 0 : cu[grp[g + 1].x] - cu[grp[g].x];
+    return (n * group + kRows - 1) / kRows;
+  }
+  // Key tiles of row tile t of group g with n tokens, and the first position of the prefix that one of its rows sees.
+  __host__ __device__ int key_tiles_of(int g, int t, int n, int& lo) const {
+    const int s0 = grp[g].x, s1 = grp[g + 1].x, p = grp[g].y, tok0 = cu[s0];
+    const int t0 = tok0 + token_of(t * kRows), t1 = tok0 + token_of(min((t + 1) * kRows, n * group) - 1);
+    int total = 0;
+    lo = window > 0 ? p : 0;
+    for (int s = seq_of(t0, s0, s1); s < s1 && cu[s] <= t1; ++s) {
+      if (cu[s + 1] == cu[s]) continue;
+      int a, b;
+      own_range(s, t0, t1, p, a, b);
+      total += tiles_between<kKeys>(a, b);
+      if (window > 0) lo = min(lo, window_start(kv[s] - cu[s + 1] + max(t0, cu[s]), window));
+    }
+    total += tiles_between<kKeys>(lo, p);
+    return max(total, 1);  // (rows that see nothing are written as well)
+  }
+  __host__ __device__ long long units(int g, int t) const {
+    int n, lo;
+    if (t >= tiles(g, n)) return 0;
+    return static_cast<long long>(key_tiles_of(g, t, n, lo)) * heads;
+  }
+  __host__ __device__ void enter(int g) {
+    left_ = tiles(g, it.n);
+    if (left_ > 0) {
+      it.kv = grp[g].x;
+      while (cu[it.kv + 1] == cu[it.kv]) ++it.kv;
+    }
+  }
+  __host__ __device__ void start(int g, int tile, long long before) {
+    it.b = g;
+    it.tile = tile - 1;
+    first = before;
+    nk = 0;
+    enter(g);
+  }
+  __host__ __device__ bool next() {
+    if (u >= u1) return false;
+    while (nk == 0 || u >= first + static_cast<long long>(nk) * heads) {
+      first += static_cast<long long>(nk) * heads;
+      ++it.tile;
+      while (it.tile >= left_) {
+        if (++it.b >= groups) return false;
+        it.tile = 0;
+        enter(it.b);
+      }
+      it.tok0 = cu[grp[it.b].x];
+      it.row0 = it.tile * kRows;
+      it.rows = min(it.n * group - it.row0, kRows);
+      it.hi = grp[it.b].y;
+      nk = key_tiles_of(it.b, it.tile, it.n, it.lo);
+    }
+    const long long r = u - first;
+    it.head = static_cast<int>(quotient(r, nk));
+    it.ub = first + static_cast<long long>(it.head) * nk;
+    it.ue = it.ub + nk;
+    it.kt0 = static_cast<int>(u - it.ub);
+    const long long end = it.ue < u1 ? it.ue : u1;
+    it.kt1 = static_cast<int>(end - it.ub);
+    u = end;
+    return true;
+  }
+  __host__ __device__ bool next_cut(long long run0, long long run1) {
+    while (next())
+      if (it.ub < run0 || it.ue > run1) return true;
+    return false;
+  }
+  int left_;  // row tiles of the current group
+};
+
+template <bool kShared, int kRows, int kKeys>
+struct WalkOf {
+  using type = Walk<kRows, kKeys>;
+};
+template <int kRows, int kKeys>
+struct WalkOf<true, kRows, kKeys> {
+  using type = SharedWalk<kRows, kKeys>;
+};
+
+// Fills grp (all threads), shares the units out and positions the walk for this CTA.  Ends with a barrier.
+// A prefix ends where the new tokens of one of its sequences begin, at the latest.  A group with a sequence whose numbers are
+// out of range is left out; so are all if the groups' bounds are not in order.
+template <int kThreads, int kRows, int kKeys>
+__device__ __forceinline__ void share_out(const AttArgs& a, int2* grp, ScanShared* sh, SharedWalk<kRows, kKeys>& w) {
+  const int G = a.groups, B = a.b.B;
+  bool bad = false;
+  for (int g = threadIdx.x; g <= G; g += kThreads) {
+    const int s = a.cu_seq[g];
+    if (s < 0 || s > B || (g > 0 && a.cu_seq[g - 1] > s)) bad = true;
+    int p = -1;
+    if (g < G) {
+      p = a.prefix[g];
+      if (p < 0 || p > static_cast<int64_t>(a.b.max_pages) * a.c.page) p = -1;
+      if (p < 0 && blockIdx.x == 0) atomicOr(a.err, kErrInvalid);
+    }
+    grp[g] = make_int2(s, p);
+  }
+  const bool disorder = __syncthreads_or(bad);
+  if (disorder) {
+    for (int g = threadIdx.x; g <= G; g += kThreads) grp[g] = make_int2(0, -1);
+    if (blockIdx.x == 0 && threadIdx.x == 0) atomicOr(a.err, kErrInvalid);
+  } else {
+    for (int b = grp[0].x + threadIdx.x; b < grp[G].x; b += kThreads) {
+      int lo = 0, hi = G;
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (grp[mid].x <= b)
+          lo = mid;
+        else
+          hi = mid;
+      }
+      const SeqSpan s = seq_span(a.b, a.c.page, b);
+      if (!s.ok && blockIdx.x == 0) atomicOr(a.err, kErrInvalid);
+      if (!s.ok)
+        atomicMin(&grp[lo].y, -1);
+      else if (s.n > 0)
+        atomicMin(&grp[lo].y, max(s.kv - s.n, 0));
+    }
+  }
+  __syncthreads();
+  for (int g = threadIdx.x; g < G; g += kThreads) {  // (their sequences' numbers are in order, or they are out already)
+    if (grp[g].y >= 0 && a.b.cu_tok[grp[g + 1].x] - a.b.cu_tok[grp[g].x] > a.group_tok) {
+      grp[g].y = -1;
+      if (blockIdx.x == 0) atomicOr(a.err, kErrInvalid);
+    }
+  }
+  __syncthreads();
+  w.grp = grp;
+  w.cu = a.b.cu_tok;
+  w.kv = a.b.kv_len;
+  w.groups = G;
+  w.heads = a.c.heads;
+  w.group = a.group;
+  w.group_mul = a.group_mul;
+  w.group_shift = a.group_shift;
+  w.window = a.window;
+  w.tree = a.tree != nullptr;
+  deal<kThreads>(a, G, sh, w);
+}
+
+// An item's stream: its segments in order, [0] the prefix.  seg = {tiles up to its end, first key tile, sequence or -1, end of
+// what is seen}.
+struct Plan {
+  int count;
+  int seq0, seq1;        // the group's sequences
+  int pre_lo;            // from here on every row sees the prefix
+  int one_lo, one_hi;    // where all rows are of one sequence: what they all see of its own
+};
+
+// One warp makes the plan of the walk's item.
+template <int kKeys, class W>
+__device__ __forceinline__ void make_plan(const W* w, Plan* plan, int4* seg) {
+  const Item& it = w->it;
+  const int lane = threadIdx.x & 31, s0 = w->grp[it.b].x, s1 = w->grp[it.b + 1].x, p = it.hi;
+  const int t0 = it.tok0 + w->token_of(it.row0), t1 = it.tok0 + w->token_of(it.row0 + it.rows - 1);
+  const int first = w->seq_of(t0, s0, s1);
+  int end = tiles_between<kKeys>(it.lo, p), count = 1, pre_lo = 0, one_lo = 0, one_hi = 0;
+  if (lane == 0) seg[0] = make_int4(end, it.lo / kKeys, -1, p);
+  for (int s_at = first;; s_at += 32) {
+    const int s = s_at + lane;
+    const bool in = s < s1 && w->cu[s] <= t1, real = in && w->cu[s + 1] > w->cu[s];
+    int lo = 0, hi = 0;
+    if (real) {
+      w->own_range(s, t0, t1, p, lo, hi);
+      const int c0 = w->cu[s], c1 = w->cu[s + 1], kv = w->kv[s], base = kv - (c1 - c0);
+      pre_lo = max(pre_lo, window_start(base + min(t1, c1 - 1) - c0, w->window));
+      if (c0 <= t0 && c1 > t1) {
+        one_lo = max(window_start(base + t1 - c0, w->window), p);
+        one_hi = w->tree ? max(base, 0) : min(max(base + t0 - c0 + 1, 0), kv);
+      }
+    }
+    const int mine = tiles_between<kKeys>(lo, hi);
+    int incl = mine;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int o = __shfl_up_sync(0xFFFFFFFFu, incl, off);
+      if (lane >= off) incl += o;
+    }
+    const uint32_t has = __ballot_sync(0xFFFFFFFFu, mine > 0);
+    if (mine > 0) seg[count + __popc(has & ((1u << lane) - 1u))] = make_int4(end + incl, lo / kKeys, s, hi);
+    count += __popc(has);
+    end += __shfl_sync(0xFFFFFFFFu, incl, 31);
+    if (!__all_sync(0xFFFFFFFFu, in)) break;
+  }
+  pre_lo = __reduce_max_sync(0xFFFFFFFFu, pre_lo);
+  one_lo = __reduce_max_sync(0xFFFFFFFFu, one_lo);
+  one_hi = __reduce_max_sync(0xFFFFFFFFu, one_hi);
+  if (lane == 0) *plan = Plan{count, s0, s1, pre_lo, one_lo, one_hi};
+  __syncwarp();
+}
+
+// Key tile v of the stream: its segment (or -1), the position of its first key.
+template <int kKeys>
+__device__ __forceinline__ int seg_of(const int4* seg, int count, int v, int& key0) {
+  int lo = 0, hi = count;  // the first segment that ends behind v
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (seg[mid].x <= v)
+      lo = mid + 1;
+    else
+      hi = mid;
+  }
+  if (lo == count) return -1;
+  const int4 s = seg[lo];
+  key0 = (s.y + v - (lo > 0 ? seg[lo - 1].x : 0)) * kKeys;
+  return lo;
+}
+
+// Stage bookkeeping of the prefill kernel's copy warp over such a stream, as load_segs: lane l holds page (page0 + l) of the
+// stream, per_tile to a tile.  Of the lane's tile: its first key, the end of what is seen, the sequence or -1, and what all rows see.
+struct SharedSegs {
+  int key0 = 0, end = 0, seq = -1, all_lo = 0, all_hi = 0;
+};
+template <int kKeys, class W>
+__device__ __forceinline__ SegBatch load_shared_segs(const AttArgs& a, const W& w, const Plan* plan, const int4* seg, int page0,
+                                                     int per_tile, SharedSegs& x) {
+  const Item& it = w.it;
+  SegBatch s;
+  s.seg0 = page0;
+  const int at_page = page0 + (threadIdx.x & 31), v = at_page / per_tile;
+  x = SharedSegs{};
+  const int at = v < it.kt1 ? seg_of<kKeys>(seg, plan->count, v, x.key0) : -1;
+  if (at < 0) return s;
+  const int4 sg = seg[at];
+  x.end = sg.w;
+  x.seq = sg.z;
+  x.all_lo = at == 0 ? plan->pre_lo : plan->one_lo;
+  x.all_hi = at == 0 ? it.hi : plan->one_hi;
+  int own_lo = 0;  // positions before a window may have no page any more
+  if (a.window > 0) {
+    if (at == 0) {
+      own_lo = it.lo;
+    } else {
+      int own_hi;
+      w.own_range(sg.z, it.tok0 + a.token_of(it.row0), it.tok0 + a.token_of(it.row0 + it.rows - 1), it.hi, own_lo, own_hi);
+    }
+  }
+  const int key = x.key0 + (at_page - v * per_tile) * a.c.page;
+  if (key < sg.w && key + a.c.page > own_lo) {
+    const int page = a.b.pages[static_cast<int64_t>(at == 0 ? it.kv : sg.z) * a.b.max_pages + key / a.c.page];
+    if (page >= 0 && page < a.c.n_pages) {
+      s.page = page;
+      const int64_t ph = static_cast<int64_t>(page) * a.c.heads + it.head;
+      s.ek = min(max(static_cast<int>(a.c.k_exp[ph]), kKvMinExp), kKvMaxExp);
+      s.ev = min(max(static_cast<int>(a.c.v_exp[ph]), kKvMinExp), kKvMaxExp);
+    } else {
+      atomicOr(a.err, kErrInvalid);
+    }
+  }
+  return s;
+}
+
+// What a query row sees: its own sequence, positions [low, lim), and from base on what its tree word says.
+struct RowSight {
+  int seq, low, lim, base;
+};
+template <class W>
+__device__ __forceinline__ RowSight row_sight(const W* w, int token, int s0, int s1) {
+  const int s = w->seq_of(token, s0, s1), n = w->cu[s + 1] - w->cu[s], i = token - w->cu[s], kv = w->kv[s], base = kv - n;
+  return RowSight{s, window_start(base + i, w->window), w->tree ? kv : min(max(base + i + 1, 0), kv), base};
+}
+
+}  // namespace att
+}  // namespace qspec

@@ -61,6 +61,8 @@ SIGNATURES = {
     "qspec_kv_attention": (ctypes.c_int, [_P, _P, _P, _I64, _I32, ctypes.c_float, _I32, _P, _P, _I64, _P, _P,
                                           ctypes.c_size_t, _P]),
     "qspec_logits_adjust": (ctypes.c_int, [_P, _I32, _I32, _I32, _P, _P, _I64, _P, _P, _P, _P, _P, _I32, _P, _P, _P]),
+    "qspec_kv_attention_shared": (ctypes.c_int, [_P, _P, _P, _P, _I64, _I32, ctypes.c_float, _I32, _P, _P, _I64, _P, _P,
+                                                 ctypes.c_size_t, _P]),
     "qspec_beam_workspace_size": (ctypes.c_size_t, [_I32, _I32, _I32, _I32]),
     "qspec_beam_select": (ctypes.c_int, [_P, _P, _P, _I32, _P, _I32, _I32, _I32, _I32, _P, _P, _P, _P, ctypes.c_size_t, _P]),
     "qspec_kv_pages": (ctypes.c_int, [_P, _P, _I32, _I32, _P, _P, _P, _I32, _I32, _P, _I64, _I32, _P, _P, _P, _P, _P, _P, _P]),
@@ -642,6 +644,43 @@ def qspec_kv_attention(cache, batch, q, out, ws, scale=None, window=0, tree=None
            load().qspec_kv_attention(cache.ref, batch.ref(T), qp, qs, hq,
                                      cache.dim ** -0.5 if scale is None else float(scale), window, _ptr(tree), op, os_,
                                      _ptr(lse), _ptr(ws), ws.numel(), _stream(stream)))
+
+
+class KVPrefixesDesc(ctypes.Structure):
+    """The C struct qspec_kv_prefixes."""
+    _fields_ = [("cu_seq", ctypes.c_void_p), ("len", ctypes.c_void_p), ("n_groups", ctypes.c_int32), ("max_tok", ctypes.c_int32)]
+
+
+class KVPrefixes:
+    """Groups of a batch's sequences that share a prefix: cu_seq int32 [groups + 1], lengths int32 [groups], max_tok new tokens
+    of a group at most.  The tensors are read by the kernels, as a KVBatch's are."""
+
+    def __init__(self, cu_seq, lengths, max_tok):
+        _dt(cu_seq, _int32, "cu_seq"); _dt(lengths, _int32, "lengths")
+        n = lengths.numel()
+        _need(cu_seq, n + 1, "cu_seq")
+        self.cu_seq, self.lengths = cu_seq, lengths
+        self.desc = KVPrefixesDesc(_ptr(cu_seq), _ptr(lengths), n, _arg32(max_tok, "max_tok"))
+        self.ref = ctypes.addressof(self.desc)
+
+
+def qspec_kv_attention_shared(cache, batch, prefixes, q, out, ws, scale=None, window=0, tree=None, lse=None, stream=None):
+    """qspec_kv_attention where the sequences of each group of a KVPrefixes share their first positions, read once for all."""
+    _dt(q, _bf16, "q"); _dt(out, _bf16, "out"); _dt(tree, torch.int64, "tree"); _dt(lse, _f32, "lse")
+    _dt(ws, torch.uint8, "ws")
+    T, hq = q.shape[:2]
+    if out.shape != q.shape:
+        raise ValueError("out must have the shape of q")
+    _need(tree, T, "tree"); _need(lse, T * hq, "lse")
+    qp, qs = _rows(q, hq, cache.dim, "q")
+    op, os_ = _rows(out, hq, cache.dim, "out")
+    window = int(window)
+    if not 0 <= window < 2 ** 31:  # (one beyond every position hides none)
+        window = _arg32(min(window, 2 ** 31 - 1), "window")
+    _check("qspec_kv_attention_shared",
+           load().qspec_kv_attention_shared(cache.ref, batch.ref(T), prefixes.ref, qp, qs, hq,
+                                            cache.dim ** -0.5 if scale is None else float(scale), window, _ptr(tree), op, os_,
+                                            _ptr(lse), _ptr(ws), ws.numel(), _stream(stream)))
 
 
 def qspec_beam_workspace_size(B, beams, V, n):
