@@ -90,7 +90,10 @@ __global__ void __launch_bounds__(DecodeCfg<D, RG>::kThreads, DecodeCfg<D, RG>::
   long long run0, run1;
   {
     W w;
-    share_out<C::kThreads>(a, seq, scan, w);
+    if constexpr (kShared)
+      share_out<C::kThreads>(a, seq, scan, w, reinterpret_cast<long long*>(ring));
+    else
+      share_out<C::kThreads>(a, seq, scan, w);
     run0 = w.u;
     run1 = w.u1;
     if (threadIdx.x == 0) *walk = w;

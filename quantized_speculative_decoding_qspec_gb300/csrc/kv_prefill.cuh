@@ -31,7 +31,9 @@ namespace att {
 // Per 16 keys of a tile: the keys' scale, the values' exponent, its inverse scale, whether there are keys at all.
 struct TileMeta {
   float4 group[8];
-  int whole[4];  // [0]: all eight groups have keys; kShared: and, 2, all rows see all keys; first key, end, sequence or -1
+  // [0]: all eight groups have keys; kShared: and, 2, all rows see all keys, 4 and 8, the query tiles that take part, 16, a page is
+  // missing among those that are seen; first key, end, sequence or -1
+  int whole[4];
 };
 
 template <int D>
@@ -50,16 +52,31 @@ struct PrefillCfg {
   static constexpr int kSmem = kTiles + kState;
   // kShared: a plan of the item's stream, its segments, and what each row sees.  The state as it is, as 512 groups just fit.
   using SW = SharedWalk<kRows, kKeys>;
-  static constexpr int kBars = 2 * kNR + 2 * kNC + kMeta + 7;
+  static constexpr int kBars = 2 * kNR + 2 * kNC + 2 * kMeta + 7;
   static constexpr int kSharedState = static_cast<int>(sizeof(TileMeta) * kMeta + 8 * kBars + sizeof(ScanShared) + 16 + 16 * sizeof(SW));
   static constexpr int kPlan = static_cast<int>(sizeof(Plan) + 8 + sizeof(int4) * (kRows + 1) + sizeof(RowSight) * kRows);
   static constexpr int kSmemShared = kTiles + kSharedState + kPlan;
   static_assert(kSharedState <= kState && kSmemShared + sizeof(int2) * (QSPEC_KV_MAX_GROUPS + 1) <= 227 * 1024, "shared memory");
 };
 
+// Side i of an item of T tiles in that order: its tile, and whether it is the values.
+struct SideAt {
+  int tile, v;
+};
+__device__ __forceinline__ SideAt side_at(int i, int T) {
+  const bool last = i == 2 * T - 1, keys = i == 0 || ((i & 1) && !last);
+  return SideAt{last ? T - 1 : keys ? (i + 1) / 2 : i / 2 - 1, keys ? 0 : 1};
+}
+__device__ __forceinline__ int side_of_keys(int tile) { return tile == 0 ? 0 : 2 * tile - 1; }
+__device__ __forceinline__ int side_of_values(int tile, int T) { return tile == T - 1 ? 2 * T - 1 : 2 * tile + 2; }
+
 // kBigPages: pages of 64 slots or more, so 64 keys lie in one page and share its scales.
 // kShared: items of groups that share a prefix (kv_shared.cuh).  The copy warp alone knows the stream; what the others need of
-// a tile stands in its TileMeta.
+// a tile stands in its TileMeta.  A key tile need not concern both query tiles: one of a sequence's own keys goes to the query tile that
+// has its rows, and items of up to 128 rows have their rows in both and take key tiles in turn, so that here as well the
+// softmax of one runs under the products of the other (the two sums meet in shared memory at the end).  The converted sides come in
+// the order K0 K1 V0 K2 V1 ...: with the values of a tile right behind its keys they held one of the three places for as long as its
+// softmax took, and the next keys' conversion stood open (16 groups of 32 single tokens over 6001 + 300 positions: 337 us).
 template <int D, bool kBigPages, bool kShared = false>
 __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1) prefill_kernel(const AttArgs a) {
   using C = PrefillCfg<D>;
@@ -83,7 +100,8 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1) prefill_kernel(con
   uint64_t* qfull = pfull + 2;
   uint64_t* odone = qfull + 1;
   uint64_t* ofree = odone + 1;
-  ScanShared* scan = reinterpret_cast<ScanShared*>(ofree + 1);
+  uint64_t* metaempty = ofree + 1;     // [kMeta], kShared alone
+  ScanShared* scan = reinterpret_cast<ScanShared*>(metaempty + (kShared ? kMeta : 0));
   volatile int* flags = reinterpret_cast<volatile int*>(scan + 1);  // abort, last to arrive, abort as the item ended
   uint32_t* tmem_base = reinterpret_cast<uint32_t*>(scan + 1) + 3;
   W* walks = reinterpret_cast<W*>(reinterpret_cast<int2*>(scan + 1) + 2);  // [16]
@@ -104,6 +122,8 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1) prefill_kernel(con
       mbar_init(convempty + i, 1);
     }
     for (int i = 0; i < kMeta; ++i) mbar_init(metafull + i, 1);
+    if (kShared)
+      for (int i = 0; i < kMeta; ++i) mbar_init(metaempty + i, C::kSoftmax);
     for (int i = 0; i < 2; ++i) {
       mbar_init(sfull + i, 1);
       mbar_init(pfull + i, 4);
@@ -125,7 +145,10 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1) prefill_kernel(con
   long long run0, run1;
   {
     W w;
-    share_out<C::kThreads>(a, seq, scan, w);  // (barriers inside)
+    if constexpr (kShared)
+      share_out<C::kThreads>(a, seq, scan, w, reinterpret_cast<long long*>(qs));
+    else
+      share_out<C::kThreads>(a, seq, scan, w);  // (barriers inside)
     run0 = w.u;
     run1 = w.u1;
     if (lane == 0) *walk = w;
@@ -138,7 +161,8 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1) prefill_kernel(con
   if (warp < C::kSoftmax) {
     reg_take<C::kRegsSoftmax>();
     // ------------------------------------------------------------------ softmax: thread = row
-    const int X = warp >> 2, row = threadIdx.x;  // of the item
+    const int X = warp >> 2;
+    int row = threadIdx.x;  // of the item
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + lane_base + X * 128, to = tmem + lane_base + kOCol + X * D;
     // The warp's 32 rows of the queries' shared memory, reached row by row (lane = row) or with D / 8 lanes to a
@@ -153,18 +177,21 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1) prefill_kernel(con
     while (walk_next(walk)) {
       const Item& it = walk->it;
       const int kt0 = it.kt0, tiles = it.kt1 - it.kt0;
-      const bool active = X * 128 < it.rows, there = row < it.rows;
+      const bool narrow = kShared && it.rows <= 128;  // the rows are in both query tiles
+      const int warp_row = narrow ? (warp & 3) * 32 : warp * 32;
+      if (kShared) row = warp_row + lane;
+      const bool active = narrow || X * 128 < it.rows, there = row < it.rows;
       // ---- queries: coalesced, largest value of each row to 2^14; fp16 then holds all bits of bf16
       uint32_t amax = 0;  // of the thread's row
       if (active) {
         const uint16_t* qp = a.q + static_cast<int64_t>(it.tok0) * a.q_token + static_cast<int64_t>(it.head) * a.group * D + 8 * my_chunk;
-        int tk = a.token_of(it.row0 + warp * 32 + my_row), in_group = it.row0 + warp * 32 + my_row - tk * a.group;
+        int tk = a.token_of(it.row0 + warp_row + my_row), in_group = it.row0 + warp_row + my_row - tk * a.group;
 #pragma unroll 1
         for (int i0 = 0; i0 < kSteps; i0 += 8) {  // (8 loads in flight; rolled, as cold code costs its fetch)
           uint4 w[8];
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            const bool real = warp * 32 + (i0 + i) * kPer + my_row < it.rows;
+            const bool real = warp_row + (i0 + i) * kPer + my_row < it.rows;
             w[i] = real ? *reinterpret_cast<const uint4*>(qp + tk * a.q_token + in_group * D) : make_uint4(0, 0, 0, 0);
             in_group += kPer;
             while (in_group >= a.group) {
@@ -198,7 +225,7 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1) prefill_kernel(con
       int all_lo = 0, all_hi = 0;  // positions that every row of the item sees
       if constexpr (kShared) {
         const int token = a.token_of(it.row0 + (there ? row : 0));
-        row_sees[row] = row_sight(walk, it.tok0 + token, walk->grp[it.b].x, walk->grp[it.b + 1].x);  // (its own thread reads it)
+        row_sees[threadIdx.x] = row_sight(walk, it.tok0 + token, walk->grp[it.b].x, walk->grp[it.b + 1].x);  // (its own thread reads it)
       } else {
         const int i0 = a.token_of(it.row0), i1 = a.token_of(it.row0 + it.rows - 1), base = it.kv - it.n;
         all_hi = a.tree ? max(base, 0) : min(max(base + i0 + 1, 0), it.kv);
@@ -213,7 +240,7 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1) prefill_kernel(con
       auto sight = [&](const TileMeta& md) {
         Sight v;
         if (kShared) {
-          const RowSight r = row_sees[row];
+          const RowSight r = row_sees[threadIdx.x];
           const int s = md.whole[3];
           v.base = r.base;
           v.lim = s < 0 ? md.whole[2] : s == r.seq ? r.lim : 0;
@@ -238,13 +265,20 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1) prefill_kernel(con
         }
         return keys != 0.0f ? see : 0u;
       };
+      constexpr int kBlockGroups = kBigPages ? 1 : 4;  // kShared: of 64 keys, groups with scales of their own
       float m = kNoMax, l = 0.0f;
       bool far = false;  // a reference of the warp's rows is so large that its rounding matters in an exponent
+      bool begun = false;  // kShared: a key tile concerned this query tile
       if (active) {
         for (int n = 0; n < tiles; ++n) {
           const int tt = t + n;
           ok = ok && wait_bar(metafull + tt % kMeta, (tt / kMeta) & 1, abort_flag, a.err);
           const TileMeta& md = meta[tt % kMeta];
+          if (kShared && ok && (md.whole[0] >> 2 >> X & 1) == 0) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(metaempty + tt % kMeta);
+            continue;
+          }
           // what the groups of keys bring, read ahead of the scores: factor, exponent, inverse scale
           constexpr int kGroups = kBigPages ? 2 : 8, kPairs = 64 / kGroups;  // groups with scales of their own, pairs of keys in each
           float gm[kGroups], ge[kGroups], gu[kGroups];
@@ -262,10 +296,76 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1) prefill_kernel(con
           ++ns;
           tc_fence_after();
           const int key0 = kShared ? md.whole[1] : (kt0 + n) * kKeys;
-          const bool plain = kShared ? md.whole[0] == 3 : key0 + kKeys <= all_hi && key0 >= all_lo && whole_tile;
+          const bool plain = kShared ? (md.whole[0] & 3) == 3 : key0 + kKeys <= all_hi && key0 >= all_lo && whole_tile;
           float top = -INFINITY;
           float s[4][32];
-          if (plain) {
+          // kShared: the warp's rows see none of the tile; masks that are more than a row's range of positions; that range
+          bool nothing = false, general = false;
+          int low = 0, lim = 0x7FFFFFFF;
+          if (kShared && !plain) {
+            const int own = md.whole[3];
+            const RowSight r = row_sees[threadIdx.x];
+            nothing = !__any_sync(0xFFFFFFFFu, own < 0 || own == r.seq);
+            general = (md.whole[0] & 16) != 0 || (a.tree && own >= 0);
+            lim = own < 0 ? md.whole[2] : own == r.seq ? r.lim : 0;
+            low = own < 0 ? r.low : max(r.low, it.hi);
+          }
+          if constexpr (kShared) {
+            // Two rolled steps of 64 keys, once for the maximum and once for the exponentials: a score is read from TMEM twice, but
+            // the code is a fifth as long.  Here the warps do not run in step (a tile concerns one query tile, or a warp of it), and
+            // the code of 128 scores in registers came from memory for each: 2000 cycles a tile where all warps run it
+            // together, 3700 to 4800 where four or one do.  Rows see all of 64 keys or none of them but where their range begins or
+            // ends; scores that are hidden there go back to TMEM as -inf.  (By integer operations on words of 32 keys; by a general
+            // mask for each score a tile took 6000 cycles.)
+            if (nothing) {
+            } else if (!general) {
+#pragma unroll 1
+              for (int b = 0; b < 2; ++b) {
+                float sb[2][32];
+                tmem_ld32(ts + 64 * b, sb[0]);
+                tmem_ld32(ts + 64 * b + 32, sb[1]);
+                tmem_wait_ld();
+                const int first = low - (key0 + 64 * b), end = lim - (key0 + 64 * b);
+                const bool seen = end > 0 && first < 64;
+                if (!__all_sync(0xFFFFFFFFu, !seen || (first <= 0 && end >= 64))) {
+#pragma unroll
+                  for (int w = 0; w < 2; ++w) {
+                    const int f = first - 32 * w, n = end - 32 * w;
+                    uint32_t see = n >= 32 ? 0xFFFFFFFFu : n <= 0 ? 0u : (1u << n) - 1u;
+                    if (f > 0) see &= f >= 32 ? 0u : ~((1u << f) - 1u);
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) {
+                      const int keep = static_cast<int>(see << (31 - e)) >> 31;
+                      sb[w][e] = __int_as_float((__float_as_int(sb[w][e]) & keep) | (static_cast<int>(0xFF800000u) & ~keep));
+                    }
+#pragma unroll
+                    for (int e = 0; e < 32; e += 16) {
+                      uint32_t back[16];
+#pragma unroll
+                      for (int k = 0; k < 16; ++k) back[k] = __float_as_uint(sb[w][e + k]);
+                      tmem_st16(ts + 64 * b + 32 * w + e, back);
+                    }
+                  }
+                  tmem_wait_st();
+                }
+#pragma unroll
+                for (int g = 0; g < kBlockGroups; ++g) {
+                  const float4 gv = md.group[4 * b + g];
+                  constexpr int kEach = 64 / kBlockGroups;
+                  auto at = [&](int e) { return sb[(kEach * g + e) / 32][(kEach * g + e) % 32]; };
+                  float x = at(0), y = at(1);
+#pragma unroll
+                  for (int e = 2; e < kEach - 2; e += 4) {
+                    x = max3(x, at(e), at(e + 1));
+                    y = max3(y, at(e + 2), at(e + 3));
+                  }
+                  x = max3(x, at(kEach - 2), at(kEach - 1));
+                  if (seen) top = fmaxf(top, fmaf(fmaxf(x, y), fminf(mult * gv.x, 3e38f), gv.y));  // (-inf times 0 is no maximum)
+                }
+              }
+            }
+          }
+          if (kShared ? false : plain) {
             tmem_ld32(ts, s[0]);
             tmem_ld32(ts + 32, s[1]);
             tmem_wait_ld();
@@ -290,7 +390,7 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1) prefill_kernel(con
                 x = -INFINITY;
               }
             }
-          } else {
+          } else if (!kShared || (general && !nothing)) {
             const Sight v = sight(md);
 #pragma unroll 1
             for (int g = 0; g < 8; ++g) {
@@ -312,8 +412,9 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1) prefill_kernel(con
             const float keep = ex2(m - m1);
             m = m1;
             l *= keep;
-            far = __any_sync(0xFFFFFFFFu, fabsf(m) > kFar);
-            if (n > 0) {
+            // (kShared: rows that have seen nothing yet are no such rows, and their sequences' neighbours need not go the long way)
+            far = __any_sync(0xFFFFFFFFu, fabsf(m) > kFar && !(kShared && m == kNoMax));
+            if (kShared ? begun : n > 0) {
 #pragma unroll 1
               for (int c = 0; c < D; c += 16) {
                 uint32_t o[16];
@@ -325,7 +426,43 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1) prefill_kernel(con
               }
             }
           }
-          if (plain && !far) {
+          if (nothing) {
+            const uint32_t zero[16] = {};
+#pragma unroll
+            for (int f = 0; f < 4; ++f) tmem_st16(ts + f * 16, zero);
+          } else if (kShared && !far && !general) {
+#pragma unroll 1
+            for (int b = 0; b < 2; ++b) {
+              float sb[2][32];
+              tmem_ld32(ts + 64 * b, sb[0]);
+              tmem_ld32(ts + 64 * b + 32, sb[1]);
+              tmem_wait_ld();
+              const bool seen = lim > key0 + 64 * b && low < key0 + 64 * b + 64;
+              constexpr int kLag0 = 2, kLag1 = 8, kBlockPairs = 32 / kBlockGroups;
+              uint64_t mm = 0, bb = 0, sum = 0;
+              uint32_t p[16];
+#pragma unroll
+              for (int e = 0; e < 32 + kLag1; ++e) {  // as below
+                const int x = e - kLag0, f = e - kLag1;
+                if (e < 32 && e % kBlockPairs == 0) {
+                  const float4 gv = md.group[4 * b + e / kBlockPairs];
+                  mm = twice(fmaxf(fminf(mult * gv.x, 3e38f), 1e-37f));  // (-inf times 0 would be NaN)
+                  bb = twice(seen ? gv.y - m : -INFINITY);
+                }
+                if (e < 32) exponents(sb[e / 16][2 * e % 32], sb[e / 16][2 * e % 32 + 1], mm, bb);
+                if (x >= 0 && x < 32) ex2_in_order(sb[x / 16][2 * x % 32]);
+                if (f >= 0) {
+                  p[f % 16] = pack_and_add(sb[f / 16][2 * f % 32], sb[f / 16][2 * f % 32 + 1], sum);
+                  if (f % kBlockPairs == kBlockPairs - 1) {
+                    l = fmaf(both(sum), md.group[4 * b + f / kBlockPairs].z, l);
+                    sum = 0;
+                  }
+                }
+                if (x >= 0 && x < 32) ex2_in_order(sb[x / 16][2 * x % 32 + 1]);
+                if (f >= 0 && f % 16 == 15) tmem_st16(ts + 32 * b + f / 16 * 16, p);
+              }
+            }
+          } else if (plain && !far) {
             // pair e of the row: exponents at step e, exponentials kLag0 pairs later, packed and summed kLag1 pairs later
             constexpr int kLag0 = 2, kLag1 = 8;
             uint64_t mm = 0, bb = 0, sum = 0;
@@ -375,7 +512,11 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1) prefill_kernel(con
           tmem_wait_st();
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(pfull + X);
+          if (lane == 0) {
+            mbar_arrive(pfull + X);
+            if (kShared) mbar_arrive(metaempty + tt % kMeta);
+          }
+          begun = true;
         }
       }
       t += tiles;
@@ -400,7 +541,36 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1) prefill_kernel(con
         }
         __syncwarp();
       };
-      if (ok && active) {
+      // kShared: what the second query tile has of a narrow item's rows, by way of the queries' shared memory
+      float* const o_second = reinterpret_cast<float*>(qs);  // [channel / 4][row] of four
+      float f_first = 1.0f, f_second = 0.0f;
+      if (kShared && narrow) {
+        float2* const ml_second = reinterpret_cast<float2*>(row_sees + 128);
+        if (X == 1) {
+#pragma unroll 1
+          for (int c = 0; c < D; c += 32) {
+            float o[32];
+            __syncwarp();
+            tmem_ld32(to + c, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              *reinterpret_cast<float4*>(o_second + ((c / 4 + e) * 128 + row) * 4) =
+                  begun ? make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          }
+          ml_second[2 * row] = make_float2(m, l);  // (in the thread's own place)
+        }
+        named_bar_sync(1, 256);
+        if (X == 0) {
+          const float2 v = ml_second[2 * row];
+          const float mm = fmaxf(m, v.x);
+          f_first = begun ? ex2(m - mm) : 0.0f;
+          f_second = ex2(v.x - mm);
+          l = fmaf(l, f_first, v.y * f_second);
+          m = mm;
+        }
+      }
+      if (ok && active && !(kShared && narrow && X == 1)) {
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;
 #pragma unroll 1
         for (int c = 0; c < D; c += 32) {
@@ -408,7 +578,32 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1) prefill_kernel(con
           __syncwarp();
           tmem_ld32(to + c, o);
           tmem_wait_ld();
-          if (whole) {
+          if (kShared && !begun) {  // (no product was written there)
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = 0.0f;
+          }
+          if (kShared && narrow) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const float4 v = *reinterpret_cast<const float4*>(o_second + ((c / 4 + e) * 128 + row) * 4);
+              o[4 * e] = fmaf(o[4 * e], f_first, v.x * f_second);
+              o[4 * e + 1] = fmaf(o[4 * e + 1], f_first, v.y * f_second);
+              o[4 * e + 2] = fmaf(o[4 * e + 2], f_first, v.z * f_second);
+              o[4 * e + 3] = fmaf(o[4 * e + 3], f_first, v.w * f_second);
+            }
+          }
+          if (kShared && narrow && whole) {  // (straight out: the staging place holds the second tile's rows)
+            if (there) {
+              const int tk = a.token_of(it.row0 + row);
+              uint16_t* op = a.out + static_cast<int64_t>(it.tok0 + tk) * a.out_token +
+                             static_cast<int64_t>(it.head * a.group + it.row0 + row - tk * a.group) * D + c;
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                *reinterpret_cast<uint4*>(op + 8 * k) =
+                    make_uint4(pack_bf16(o[8 * k] * inv, o[8 * k + 1] * inv), pack_bf16(o[8 * k + 2] * inv, o[8 * k + 3] * inv),
+                               pack_bf16(o[8 * k + 4] * inv, o[8 * k + 5] * inv), pack_bf16(o[8 * k + 6] * inv, o[8 * k + 7] * inv));
+            }
+          } else if (whole) {
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               uint32_t w[4];
@@ -423,7 +618,7 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1) prefill_kernel(con
           }
         }
         if (whole) {
-          store_rows();
+          if (!(kShared && narrow)) store_rows();
           if (a.lse && there) {
             const int token = a.token_of(it.row0 + row), hq = it.head * a.group + it.row0 + row - token * a.group;
             a.lse[static_cast<int64_t>(it.tok0 + token) * a.heads_q + hq] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.693147180559945f;
@@ -508,10 +703,11 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1) prefill_kernel(con
     if (warp >= C::kConv0) {
       // ------------------------------------------------------------------ converters
       const int cw = warp - C::kConv0;
-      int i = 0;
+      int i = 0, tile0 = 0;  // sides, and tiles of the items before
       bool ok = true;
       while (ok && walk_next(walk)) {
         const Item& it = walk->it;
+        if (kShared && i > 0) tile0 = i / 2;
         for (int kt = it.kt0; ok && kt < it.kt1; ++kt) {
           int kv_in = it.kv - kt * kKeys;  // slots from here on hold anything
           for (int side = 0; side < 2; ++side, ++i) {
@@ -522,7 +718,8 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1) prefill_kernel(con
             if (!ok) break;
             const uint8_t* src = raw + st * C::kRaw;
             uint8_t* dst = conv + sc * C::kConv;
-            const TileMeta& md = meta[(i >> 1) % kMeta];
+            const TileMeta& md =
+                meta[(kShared ? tile0 + side_at(2 * (kt - it.kt0) + side, it.kt1 - it.kt0).tile : i >> 1) % kMeta];
             if (kShared) kv_in = md.whole[2] - md.whole[1];
             // a quarter warp takes two keys; D = 128: the first key's chunks of one half, the second's of the other
             const int quad = lane & 3, sub = (lane >> 2) & 1;
@@ -575,16 +772,63 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1) prefill_kernel(con
       while (walk_next(walk)) {
         const Item& it = walk->it;
         SegBatch sb;
-        SharedSegs ss;
-        if constexpr (kShared) make_plan<kKeys>(walk, plan, seg);
-        for (int kt = it.kt0; kt < it.kt1; ++kt, ++t) {
-          const int seg0 = kt * per_tile;
-          if (sb.seg0 < 0 || seg0 >= sb.seg0 + 32) {
-            if constexpr (kShared)
-              sb = load_shared_segs<kKeys>(a, *walk, plan, seg, seg0, per_tile, ss);
-            else
-              sb = load_segs(a, it, seg0, P);
+        if constexpr (kShared) {
+          SharedSegs ss;
+          make_plan<kKeys>(walk, plan, seg);
+          const int T = it.kt1 - it.kt0;
+          // of the tile whose keys were last copied and of the one before: the lane's page or none, the pages there are
+          int64_t at = 0, at_before = 0;
+          uint32_t who = 0, who_before = 0;
+          int l0 = 0, l0_before = 0;
+          bool ok = true;
+          for (int i = 0; i < 2 * T; ++i, ++issued) {
+            const SideAt side = side_at(i, T);
+            const int st = issued % kNR, tt = t + side.tile;
+            if (issued >= kNR) ok = wait_bar(rawempty + st, ((issued / kNR) - 1) & 1, abort_flag, a.err);
+            if (side.v == 0 && tt >= kMeta) ok = ok && wait_bar(metaempty + tt % kMeta, ((tt / kMeta) - 1) & 1, abort_flag, a.err);
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            if (!ok) break;
+            if (side.v == 0) {
+              const int seg0 = (it.kt0 + side.tile) * per_tile;
+              if (sb.seg0 < 0 || seg0 >= sb.seg0 + 32) sb = load_shared_segs<kKeys>(a, *walk, plan, seg, seg0, per_tile, ss);
+              at_before = at;
+              who_before = who;
+              l0_before = l0;
+              l0 = seg0 - sb.seg0;
+              const bool mine = lane >= l0 && lane < l0 + per_tile && sb.page >= 0;
+              who = __ballot_sync(0xFFFFFFFFu, mine);
+              const int missing = __any_sync(0xFFFFFFFFu, lane >= l0 && lane < l0 + per_tile && ss.missing) ? 16 : 0;
+              at = mine ? (static_cast<int64_t>(sb.page) * a.c.heads + it.head) * seg_bytes : -1;
+              TileMeta& md = meta[tt % kMeta];
+              if (lane < 8) md.group[lane] = make_float4(0.0f, 0.0f, 1.0f, 0.0f);
+              if (lane == l0) {
+                md.whole[0] = (__popc(who) != per_tile ? 0 : ss.key0 >= ss.all_lo && ss.key0 + kKeys <= ss.all_hi ? 3 : 1) | ss.parts << 2 | missing;
+                md.whole[1] = ss.key0;
+                md.whole[2] = ss.end;
+                md.whole[3] = ss.seq;
+              }
+              __syncwarp();
+              if (mine) {
+                const int g0 = (lane - l0) * (P / 16);
+                const float4 v = make_float4(exp2_int(sb.ek), static_cast<float>(sb.ev), exp2_int(-sb.ev), 1.0f);
+                for (int g = g0; g < g0 + P / 16; ++g) md.group[g] = v;
+              }
+              __syncwarp();
+              if (lane == 0) mbar_arrive(metafull + tt % kMeta);
+            }
+            // (values of the tile before the one whose keys came last, but for the item's last)
+            const bool old = side.v != 0 && i < 2 * T - 1;
+            const int64_t from = old ? at_before : at;
+            const uint32_t pages = old ? who_before : who;
+            if (lane == 0) mbar_arrive_expect_tx(rawfull + st, __popc(pages) * seg_bytes);
+            __syncwarp();
+            if (pages >> lane & 1u)
+              bulk_load(raw + st * C::kRaw + (lane - (old ? l0_before : l0)) * seg_bytes, (side.v ? a.c.v : a.c.k) + from, seg_bytes, rawfull + st);
           }
+          t += T;
+        } else for (int kt = it.kt0; kt < it.kt1; ++kt, ++t) {
+          const int seg0 = kt * per_tile;
+          if (sb.seg0 < 0 || seg0 >= sb.seg0 + 32) sb = load_segs(a, it, seg0, P);
           const int l0 = seg0 - sb.seg0;
           const bool mine = lane >= l0 && lane < l0 + per_tile && sb.page >= 0;
           const uint32_t who = __ballot_sync(0xFFFFFFFFu, mine);
@@ -601,16 +845,7 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1) prefill_kernel(con
               // converted slot before that was used up by an MMA that followed their PVs
               TileMeta& md = meta[t % kMeta];
               if (lane < 8) md.group[lane] = make_float4(0.0f, 0.0f, 1.0f, 0.0f);
-              if (kShared) {
-                if (lane == l0) {
-                  md.whole[0] = __popc(who) != per_tile ? 0 : ss.key0 >= ss.all_lo && ss.key0 + kKeys <= ss.all_hi ? 3 : 1;
-                  md.whole[1] = ss.key0;
-                  md.whole[2] = ss.end;
-                  md.whole[3] = ss.seq;
-                }
-              } else if (lane == 0) {
-                md.whole[0] = __popc(who) == per_tile;
-              }
+              if (lane == 0) md.whole[0] = __popc(who) == per_tile;
               __syncwarp();
               if (mine) {
                 const int g0 = (lane - l0) * (P / 16);
@@ -684,7 +919,68 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1) prefill_kernel(con
         }
         __syncwarp();
       };
-      while (ok && walk_next(walk)) {
+      // kShared: each query tile has its own turn.  pend: the key tile whose scores it was given last, whose product with the
+      // values waits for the softmax, or -1.  Keys of tile n take the place of the values of tile n - 3 in the ring of three converted
+      // sides, so those are multiplied first (steps 0 and 1).  Rolled, so that each kind of product stands in the code once:
+      // sixteen warps in five roles share the instruction cache.
+      uint32_t tile = 0, np[2] = {0, 0}, side0 = 0;
+      while (kShared && ok && walk_next(walk)) {
+        const int tiles = __shfl_sync(0xFFFFFFFFu, walk->it.kt1 - walk->it.kt0, 0);
+        bool begun[2] = {false, false};
+        int pend[2] = {-1, -1};
+        wait_all(qfull, item & 1);
+#pragma unroll 1
+        for (int n = 0; ok && n <= tiles + 1; ++n) {
+          const int must = n <= tiles ? n - 3 : tiles;  // (at the end nothing is left pending; the last values, too, take such a place)
+          uint32_t ks = 0;
+          int parts = 0;
+#pragma unroll 1
+          for (int step = 0; step < (n < tiles ? 4 : 2); ++step) {
+            const bool one = step & 1;
+            if (step == 2) {
+              const uint32_t i = side0 + side_of_keys(n);
+              ks = i % kNC;
+              wait_all(convfull + ks, (i / kNC) & 1);
+              if (!ok) break;
+              parts = __shfl_sync(0xFFFFFFFFu, meta[tile % kMeta].whole[0] >> 2, 0);
+              ++tile;
+            }
+            const uint32_t X = one ? 1 : 0;
+            const bool mine = step >= 2 && (parts >> X & 1);
+            const int j = one ? pend[1] : pend[0];
+            if (j >= 0 && (mine || (step < 2 && j <= must))) {
+              const uint32_t i = side0 + side_of_values(j, tiles), v = i % kNC, turn = one ? np[1]++ : np[0]++;
+              wait_all(convfull + v, (i / kNC) & 1);
+              wait_all(pfull + X, turn & 1);
+              if (item > 0 && !begun[0] && !begun[1]) wait_all(ofree, (item - 1) & 1);
+              if (!ok) break;
+              values(X, v, !(one ? begun[1] : begun[0]));
+              if (one) {
+                begun[1] = true;
+                pend[1] = -1;
+              } else {
+                begun[0] = true;
+                pend[0] = -1;
+              }
+              if ((one ? pend[0] : pend[1]) != j) commit(convempty + v);
+            }
+            if (mine) {
+              scores(X, ks);
+              if (one)
+                pend[1] = n;
+              else
+                pend[0] = n;
+            }
+          }
+          if (n < tiles && ok) commit(convempty + ks);
+        }
+        side0 += 2 * tiles;
+        if (ok) {
+          commit(odone);
+          ++item;
+        }
+      }
+      while (!kShared && ok && walk_next(walk)) {
         const bool both = __shfl_sync(0xFFFFFFFFu, walk->it.rows, 0) > 128;
         const int tiles = __shfl_sync(0xFFFFFFFFu, walk->it.kt1 - walk->it.kt0, 0);
         wait_all(qfull, item & 1);

@@ -187,9 +187,9 @@ __host__ __device__ __forceinline__ int owner_of(long long u, const ScanShared* 
 }
 
 // Shares out the units of `owners` sequences (or groups) of a.max_tiles row tiles at most, and positions the walk for this
-// CTA.  Ends with a barrier.
-template <int kThreads, class W>
-__device__ __forceinline__ void deal(const AttArgs& a, int owners, ScanShared* sh, W& w) {
+// CTA.  count.units(owner, row tile).  Ends with a barrier.
+template <int kThreads, class W, class Count>
+__device__ __forceinline__ void deal(const AttArgs& a, int owners, ScanShared* sh, W& w, const Count& count) {
   // (sequence, row tile) pairs, a run of them per thread; sequences of fewer tiles leave gaps
   const uint32_t pairs = static_cast<uint32_t>(owners) * a.max_tiles;  // (below 2^30)
   const uint32_t per = (pairs + kThreads - 1) / kThreads;
@@ -198,7 +198,7 @@ __device__ __forceinline__ void deal(const AttArgs& a, int owners, ScanShared* s
   const int b_first = b, tile_first = tile;
   long long mine = 0;
   for (uint32_t e = e0; e < e1; ++e) {
-    mine += w.units(b, tile);
+    mine += count.units(b, tile);
     if (++tile == a.max_tiles) {
       tile = 0;
       ++b;
@@ -226,7 +226,7 @@ __device__ __forceinline__ void deal(const AttArgs& a, int owners, ScanShared* s
   if (w.u < w.u1 && w.u >= before && w.u < before + mine) {  // (one thread)
     b = b_first;
     tile = tile_first;
-    for (long long n; w.u >= before + (n = w.units(b, tile)); before += n)
+    for (long long n; w.u >= before + (n = count.units(b, tile)); before += n)
       if (++tile == a.max_tiles) {
         tile = 0;
         ++b;
@@ -265,7 +265,7 @@ __device__ __forceinline__ void share_out(const AttArgs& a, int2* seq, ScanShare
   w.group_shift = a.group_shift;
   w.window = a.window;
   w.tree = a.tree != nullptr;
-  deal<kThreads>(a, B, sh, w);
+  deal<kThreads>(a, B, sh, w, w);
 }
 
 

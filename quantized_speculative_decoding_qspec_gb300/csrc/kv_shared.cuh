@@ -25,6 +25,7 @@ __host__ __device__ __forceinline__ int tiles_between(int lo, int hi) {
 // kt1 count the tiles of the item's own stream.
 template <int kRows, int kKeys>
 struct SharedWalk {
+  static constexpr int kRowsOf = kRows;
   const int2* grp;
   const int32_t* cu;
   const int32_t* kv;
@@ -60,26 +61,30 @@ struct SharedWalk {
     n = grp[g].y < 0 ? 0 : cu[grp[g + 1].x] - cu[grp[g].x];
     return (n * group + kRows - 1) / kRows;
   }
-  // Key tiles of row tile t of group g with n tokens, and the first position of the prefix that one of its rows sees.
-  __host__ __device__ int key_tiles_of(int g, int t, int n, int& lo) const {
+  // Key tiles of row tile t of group g with n tokens: what one of `lanes` lanes that share the sequences has to add (the first of
+  // them the prefix, given the first position of it that a row sees).
+  __host__ __device__ int own_tiles(int g, int t, int n, int lane, int lanes, int& lo) const {
     const int s0 = grp[g].x, s1 = grp[g + 1].x, p = grp[g].y, tok0 = cu[s0];
     const int t0 = tok0 + token_of(t * kRows), t1 = tok0 + token_of(min((t + 1) * kRows, n * group) - 1);
     int total = 0;
     lo = window > 0 ? p : 0;
-    for (int s = seq_of(t0, s0, s1); s < s1 && cu[s] <= t1; ++s) {
+    for (int s = seq_of(t0, s0, s1) + lane; s < s1 && cu[s] <= t1; s += lanes) {
       if (cu[s + 1] == cu[s]) continue;
       int a, b;
       own_range(s, t0, t1, p, a, b);
       total += tiles_between<kKeys>(a, b);
       if (window > 0) lo = min(lo, window_start(kv[s] - cu[s + 1] + max(t0, cu[s]), window));
     }
-    total += tiles_between<kKeys>(lo, p);
-    return max(total, 1);  // (rows that see nothing are written as well)
+    return total;
+  }
+  __host__ __device__ int all_tiles(int g, int own, int lo) const {
+    return max(own + tiles_between<kKeys>(lo, grp[g].y), 1);  // (rows that see nothing are written as well)
   }
   __host__ __device__ long long units(int g, int t) const {
     int n, lo;
     if (t >= tiles(g, n)) return 0;
-    return static_cast<long long>(key_tiles_of(g, t, n, lo)) * heads;
+    const int own = own_tiles(g, t, n, 0, 1, lo);
+    return static_cast<long long>(all_tiles(g, own, lo)) * heads;
   }
   __host__ __device__ void enter(int g) {
     left_ = tiles(g, it.n);
@@ -95,13 +100,16 @@ struct SharedWalk {
     nk = 0;
     enter(g);
   }
-  __host__ __device__ bool next() {
-    if (u >= u1) return false;
-    while (nk == 0 || u >= first + static_cast<long long>(nk) * heads) {
+  // One step of a walk: -1 at the end of the run, 0 for a row tile whose key tiles are to be counted into nk and it.lo, 1 for
+  // the next part of the run in `it`.
+  __host__ __device__ int step() {
+    if (u >= u1) return -1;
+    if (nk == 0 || u >= first + static_cast<long long>(nk) * heads) {
       first += static_cast<long long>(nk) * heads;
+      nk = 0;
       ++it.tile;
       while (it.tile >= left_) {
-        if (++it.b >= groups) return false;
+        if (++it.b >= groups) return -1;
         it.tile = 0;
         enter(it.b);
       }
@@ -109,7 +117,7 @@ struct SharedWalk {
       it.row0 = it.tile * kRows;
       it.rows = min(it.n * group - it.row0, kRows);
       it.hi = grp[it.b].y;
-      nk = key_tiles_of(it.b, it.tile, it.n, it.lo);
+      return 0;
     }
     const long long r = u - first;
     it.head = static_cast<int>(quotient(r, nk));
@@ -119,6 +127,14 @@ struct SharedWalk {
     const long long end = it.ue < u1 ? it.ue : u1;
     it.kt1 = static_cast<int>(end - it.ub);
     u = end;
+    return 1;
+  }
+  __host__ __device__ bool next() {
+    for (int s; (s = step()) <= 0;) {
+      if (s < 0) return false;
+      const int own = own_tiles(it.b, it.tile, it.n, 0, 1, it.lo);
+      nk = all_tiles(it.b, own, it.lo);
+    }
     return true;
   }
   __host__ __device__ bool next_cut(long long run0, long long run1) {
@@ -129,6 +145,28 @@ struct SharedWalk {
   int left_;  // row tiles of the current group
 };
 
+// The whole warp advances a walk in shared memory: a lane steps, all count.
+template <int kRows, int kKeys>
+__device__ __forceinline__ bool walk_next(SharedWalk<kRows, kKeys>* w) {
+  const int lane = threadIdx.x & 31;
+  while (true) {
+    __syncwarp();
+    int s = 0;
+    if (lane == 0) s = w->step();
+    s = __shfl_sync(0xFFFFFFFFu, s, 0);
+    __syncwarp();
+    if (s != 0) return s > 0;
+    int lo;
+    const int own = __reduce_add_sync(0xFFFFFFFFu, w->own_tiles(w->it.b, w->it.tile, w->it.n, lane, 32, lo));
+    lo = __reduce_min_sync(0xFFFFFFFFu, lo);
+    __syncwarp();
+    if (lane == 0) {
+      w->it.lo = lo;
+      w->nk = w->all_tiles(w->it.b, own, lo);
+    }
+  }
+}
+
 template <bool kShared, int kRows, int kKeys>
 struct WalkOf {
   using type = Walk<kRows, kKeys>;
@@ -138,11 +176,23 @@ struct WalkOf<true, kRows, kKeys> {
   using type = SharedWalk<kRows, kKeys>;
 };
 
+// Units of (group, row tile) pairs, worked out by several lanes each where the pairs are few, in shared memory.
+constexpr int kCounted = 512;
+template <class W>
+struct Counted {
+  const W& w;
+  const long long* sum;  // null: not counted ahead
+  int max_tiles;
+  __device__ long long units(int g, int t) const { return sum ? sum[g * max_tiles + t] : w.units(g, t); }
+};
+
 // Fills grp (all threads), shares the units out and positions the walk for this CTA.  Ends with a barrier.
 // A prefix ends where the new tokens of one of its sequences begin, at the latest.  A group with a sequence whose numbers are
-// out of range is left out; so are all if the groups' bounds are not in order.
+// out of range is left out; so are all if the groups' bounds are not in order.  scratch: kCounted numbers of shared memory that is
+// not in use yet.
 template <int kThreads, int kRows, int kKeys>
-__device__ __forceinline__ void share_out(const AttArgs& a, int2* grp, ScanShared* sh, SharedWalk<kRows, kKeys>& w) {
+__device__ __forceinline__ void share_out(const AttArgs& a, int2* grp, ScanShared* sh, SharedWalk<kRows, kKeys>& w,
+                                          long long* scratch) {
   const int G = a.groups, B = a.b.B;
   bool bad = false;
   for (int g = threadIdx.x; g <= G; g += kThreads) {
@@ -196,7 +246,29 @@ __device__ __forceinline__ void share_out(const AttArgs& a, int2* grp, ScanShare
   w.group_shift = a.group_shift;
   w.window = a.window;
   w.tree = a.tree != nullptr;
-  deal<kThreads>(a, G, sh, w);
+  const uint32_t pairs = static_cast<uint32_t>(G) * a.max_tiles;
+  const bool counted = pairs <= kCounted;
+  if (counted) {
+    // (One thread that goes through 64 sequences takes 5 us, and the walk begins with three such counts: a group of 128 single tokens over
+    // 65536 positions spent 19 us here.)
+    int lanes = 32;
+    while (lanes > 1 && pairs * lanes > 2 * kThreads) lanes /= 2;
+    const int lane = threadIdx.x % lanes;
+    for (uint32_t e = threadIdx.x / lanes; e < (pairs + 31) / 32 * 32; e += kThreads / lanes) {  // (whole warps)
+      int n = 0, own = 0, lo = 0x7FFFFFFF;
+      const int g = e < pairs ? e / static_cast<uint32_t>(a.max_tiles) : 0, t = e - g * a.max_tiles;
+      const bool real = e < pairs && t < w.tiles(g, n);
+      if (real) own = w.own_tiles(g, t, n, lane, lanes, lo);
+      for (int off = lanes / 2; off >= 1; off >>= 1) {
+        own += __shfl_xor_sync(0xFFFFFFFFu, own, off);
+        lo = min(lo, __shfl_xor_sync(0xFFFFFFFFu, lo, off));
+      }
+      if (e < pairs && lane == 0) scratch[e] = real ? static_cast<long long>(w.all_tiles(g, own, lo)) * w.heads : 0;
+    }
+    __syncthreads();
+  }
+  const Counted<SharedWalk<kRows, kKeys>> c{w, counted ? scratch : nullptr, a.max_tiles};
+  deal<kThreads>(a, G, sh, w, c);
 }
 
 // An item's stream: its segments in order, [0] the prefix.  seg = {tiles up to its end, first key tile, sequence or -1, end of
@@ -269,8 +341,10 @@ __device__ __forceinline__ int seg_of(const int4* seg, int count, int v, int& ke
 
 // Stage bookkeeping of the prefill kernel's copy warp over such a stream, as load_segs: lane l holds page (page0 + l) of the
 // stream, per_tile to a tile.  Of the lane's tile: its first key, the end of what is seen, the sequence or -1, and what all rows see.
+// Which query tiles it concerns (bits 0 and 1): see the kernel.
 struct SharedSegs {
-  int key0 = 0, end = 0, seq = -1, all_lo = 0, all_hi = 0;
+  int key0 = 0, end = 0, seq = -1, all_lo = 0, all_hi = 0, parts = 1;
+  bool missing = false;  // the lane's page has no place in the cache
 };
 template <int kKeys, class W>
 __device__ __forceinline__ SegBatch load_shared_segs(const AttArgs& a, const W& w, const Plan* plan, const int4* seg, int page0,
@@ -280,6 +354,8 @@ __device__ __forceinline__ SegBatch load_shared_segs(const AttArgs& a, const W& 
   s.seg0 = page0;
   const int at_page = page0 + (threadIdx.x & 31), v = at_page / per_tile;
   x = SharedSegs{};
+  const bool narrow = it.rows <= W::kRowsOf / 2;
+  if (narrow) x.parts = 1 << (v & 1);
   const int at = v < it.kt1 ? seg_of<kKeys>(seg, plan->count, v, x.key0) : -1;
   if (at < 0) return s;
   const int4 sg = seg[at];
@@ -287,6 +363,14 @@ __device__ __forceinline__ SegBatch load_shared_segs(const AttArgs& a, const W& 
   x.seq = sg.z;
   x.all_lo = at == 0 ? plan->pre_lo : plan->one_lo;
   x.all_hi = at == 0 ? it.hi : plan->one_hi;
+  if (!narrow) {
+    x.parts = 3;
+    if (at > 0) {  // the rows of the sequence's tokens
+      const int64_t half = it.row0 + W::kRowsOf / 2;
+      x.parts = (static_cast<int64_t>(w.cu[sg.z] - it.tok0) * a.group < half ? 1 : 0) |
+                (static_cast<int64_t>(w.cu[sg.z + 1] - it.tok0) * a.group > half ? 2 : 0);
+    }
+  }
   int own_lo = 0;  // positions before a window may have no page any more
   if (a.window > 0) {
     if (at == 0) {
@@ -305,6 +389,7 @@ __device__ __forceinline__ SegBatch load_shared_segs(const AttArgs& a, const W& 
       s.ek = min(max(static_cast<int>(a.c.k_exp[ph]), kKvMinExp), kKvMaxExp);
       s.ev = min(max(static_cast<int>(a.c.v_exp[ph]), kKvMinExp), kKvMaxExp);
     } else {
+      x.missing = true;
       atomicOr(a.err, kErrInvalid);
     }
   }
