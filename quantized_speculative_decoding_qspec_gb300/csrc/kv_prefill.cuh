@@ -31,8 +31,8 @@ namespace att {
 // Per 16 keys of a tile: the keys' scale, the values' exponent, its inverse scale, whether there are keys at all.
 struct TileMeta {
   float4 group[8];
-  // [0]: all eight groups have keys; kShared: and, 2, all rows see all keys, 4 and 8, the query tiles that take part, 16, a page is
-  // missing among those that are seen; first key, end, sequence or -1
+  // [0]: all eight groups have keys; kShared: and, 2, all rows see all keys, 4 and 8, the query tiles that take part; first key,
+  // end, sequence or -1
   int whole[4];
 };
 
@@ -52,7 +52,7 @@ struct PrefillCfg {
   static constexpr int kSmem = kTiles + kState;
   // kShared: a plan of the item's stream, its segments, and what each row sees.  The state as it is, as 512 groups just fit.
   using SW = SharedWalk<kRows, kKeys>;
-  static constexpr int kBars = 2 * kNR + 2 * kNC + 2 * kMeta + 7;
+  static constexpr int kBars = 2 * kNR + 2 * kNC + 2 * kMeta + 9;
   static constexpr int kSharedState = static_cast<int>(sizeof(TileMeta) * kMeta + 8 * kBars + sizeof(ScanShared) + 16 + 16 * sizeof(SW));
   static constexpr int kPlan = static_cast<int>(sizeof(Plan) + 8 + sizeof(int4) * (kRows + 1) + sizeof(RowSight) * kRows);
   static constexpr int kSmemShared = kTiles + kSharedState + kPlan;
@@ -85,6 +85,8 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1) prefill_kernel(con
   constexpr int kRows = C::kRows, kKeys = C::kKeys, kNR = C::kNR, kNC = C::kNC, kMeta = C::kMeta;
   constexpr int kSub = kKeys * 128;  // bytes of a sub-tile: 128 rows of 128 bytes
   constexpr uint32_t kOCol = 256, kCols = 512;
+  // kShared: a warp for the products of each query tile
+  constexpr int kMmas = kShared ? 2 : 1, kConv0 = C::kConv0 + kMmas - 1, kConvs = C::kConvs - kMmas + 1;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* qs = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint8_t* conv = qs + 2 * C::kQ;
@@ -101,7 +103,8 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1) prefill_kernel(con
   uint64_t* odone = qfull + 1;
   uint64_t* ofree = odone + 1;
   uint64_t* metaempty = ofree + 1;     // [kMeta], kShared alone
-  ScanShared* scan = reinterpret_cast<ScanShared*>(metaempty + (kShared ? kMeta : 0));
+  uint64_t* drain = metaempty + kMeta;  // [2]
+  ScanShared* scan = reinterpret_cast<ScanShared*>(metaempty + (kShared ? kMeta + 2 : 0));
   volatile int* flags = reinterpret_cast<volatile int*>(scan + 1);  // abort, last to arrive, abort as the item ended
   uint32_t* tmem_base = reinterpret_cast<uint32_t*>(scan + 1) + 3;
   W* walks = reinterpret_cast<W*>(reinterpret_cast<int2*>(scan + 1) + 2);  // [16]
@@ -115,21 +118,24 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1) prefill_kernel(con
   if (threadIdx.x == 0) {
     for (int i = 0; i < kNR; ++i) {
       mbar_init(rawfull + i, 1);
-      mbar_init(rawempty + i, C::kConvs);
+      mbar_init(rawempty + i, kConvs);
     }
     for (int i = 0; i < kNC; ++i) {
-      mbar_init(convfull + i, C::kConvs);
-      mbar_init(convempty + i, 1);
+      mbar_init(convfull + i, kConvs);
+      mbar_init(convempty + i, kMmas);
     }
     for (int i = 0; i < kMeta; ++i) mbar_init(metafull + i, 1);
-    if (kShared)
+    if (kShared) {
       for (int i = 0; i < kMeta; ++i) mbar_init(metaempty + i, C::kSoftmax);
+      mbar_init(drain, 1);
+      mbar_init(drain + 1, 1);
+    }
     for (int i = 0; i < 2; ++i) {
       mbar_init(sfull + i, 1);
       mbar_init(pfull + i, 4);
     }
     mbar_init(qfull, 8);
-    mbar_init(odone, 1);
+    mbar_init(odone, kMmas);
     mbar_init(ofree, 8);
     flags[0] = 0;
     fence_mbar_init();
@@ -237,17 +243,8 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1) prefill_kernel(con
         int base, lim, low;
         unsigned long long bits;
       };
-      auto sight = [&](const TileMeta& md) {
+      auto sight = [&]() {
         Sight v;
-        if (kShared) {
-          const RowSight r = row_sees[threadIdx.x];
-          const int s = md.whole[3];
-          v.base = r.base;
-          v.lim = s < 0 ? md.whole[2] : s == r.seq ? r.lim : 0;
-          v.low = s < 0 ? r.low : max(r.low, it.hi);
-          v.bits = a.tree && there ? a.tree[it.tok0 + a.token_of(it.row0 + row)] : 0ull;
-          return v;
-        }
         const int token = a.token_of(it.row0 + (row < it.rows ? row : 0));
         v.base = it.kv - it.n;
         v.lim = a.tree ? it.kv : min(max(v.base + token + 1, 0), it.kv);
@@ -299,14 +296,14 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1) prefill_kernel(con
           const bool plain = kShared ? (md.whole[0] & 3) == 3 : key0 + kKeys <= all_hi && key0 >= all_lo && whole_tile;
           float top = -INFINITY;
           float s[4][32];
-          // kShared: the warp's rows see none of the tile; masks that are more than a row's range of positions; that range
-          bool nothing = false, general = false;
-          int low = 0, lim = 0x7FFFFFFF;
+          // kShared: the warp's rows see none of the tile; the positions that the row sees, and from where on its tree word tells
+          bool nothing = false;
+          int low = 0, lim = 0x7FFFFFFF, tree_from = 0x7FFFFFFF;
           if (kShared && !plain) {
             const int own = md.whole[3];
             const RowSight r = row_sees[threadIdx.x];
             nothing = !__any_sync(0xFFFFFFFFu, own < 0 || own == r.seq);
-            general = (md.whole[0] & 16) != 0 || (a.tree && own >= 0);
+            if (a.tree) tree_from = r.base;
             lim = own < 0 ? md.whole[2] : own == r.seq ? r.lim : 0;
             low = own < 0 ? r.low : max(r.low, it.hi);
           }
@@ -317,8 +314,7 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1) prefill_kernel(con
             // together, 3700 to 4800 where four or one do.  Rows see all of 64 keys or none of them but where their range begins or
             // ends; scores that are hidden there go back to TMEM as -inf.  (By integer operations on words of 32 keys; by a general
             // mask for each score a tile took 6000 cycles.)
-            if (nothing) {
-            } else if (!general) {
+            if (!nothing) {
 #pragma unroll 1
               for (int b = 0; b < 2; ++b) {
                 float sb[2][32];
@@ -327,24 +323,23 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1) prefill_kernel(con
                 tmem_wait_ld();
                 const int first = low - (key0 + 64 * b), end = lim - (key0 + 64 * b);
                 const bool seen = end > 0 && first < 64;
-                if (!__all_sync(0xFFFFFFFFu, !seen || (first <= 0 && end >= 64))) {
+                if (!__all_sync(0xFFFFFFFFu, !seen || (first <= 0 && end >= 64 && tree_from >= key0 + 64 * b + 64))) {
 #pragma unroll
                   for (int w = 0; w < 2; ++w) {
                     const int f = first - 32 * w, n = end - 32 * w;
                     uint32_t see = n >= 32 ? 0xFFFFFFFFu : n <= 0 ? 0u : (1u << n) - 1u;
                     if (f > 0) see &= f >= 32 ? 0u : ~((1u << f) - 1u);
+                    const int d = key0 + 64 * b + 32 * w - tree_from;
+                    if (d > -32) {
+                      const unsigned long long bits = there ? a.tree[it.tok0 + a.token_of(it.row0 + row)] : 0ull;
+                      see &= d >= 64 ? 0u : d >= 0 ? static_cast<uint32_t>(bits >> d) : static_cast<uint32_t>(bits << -d) | ((1u << -d) - 1u);
+                    }
 #pragma unroll
                     for (int e = 0; e < 32; ++e) {
                       const int keep = static_cast<int>(see << (31 - e)) >> 31;
                       sb[w][e] = __int_as_float((__float_as_int(sb[w][e]) & keep) | (static_cast<int>(0xFF800000u) & ~keep));
                     }
-#pragma unroll
-                    for (int e = 0; e < 32; e += 16) {
-                      uint32_t back[16];
-#pragma unroll
-                      for (int k = 0; k < 16; ++k) back[k] = __float_as_uint(sb[w][e + k]);
-                      tmem_st16(ts + 64 * b + 32 * w + e, back);
-                    }
+                    tmem_st32(ts + 64 * b + 32 * w, sb[w]);
                   }
                   tmem_wait_st();
                 }
@@ -365,7 +360,8 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1) prefill_kernel(con
               }
             }
           }
-          if (kShared ? false : plain) {
+          if (kShared) {
+          } else if (plain) {
             tmem_ld32(ts, s[0]);
             tmem_ld32(ts + 32, s[1]);
             tmem_wait_ld();
@@ -390,8 +386,8 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1) prefill_kernel(con
                 x = -INFINITY;
               }
             }
-          } else if (!kShared || (general && !nothing)) {
-            const Sight v = sight(md);
+          } else {
+            const Sight v = sight();
 #pragma unroll 1
             for (int g = 0; g < 8; ++g) {
               float sg[16];
@@ -412,7 +408,7 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1) prefill_kernel(con
             const float keep = ex2(m - m1);
             m = m1;
             l *= keep;
-            // (kShared: rows that have seen nothing yet are no such rows, and their sequences' neighbours need not go the long way)
+            // (kShared: rows that have seen nothing yet are no such rows)
             far = __any_sync(0xFFFFFFFFu, fabsf(m) > kFar && !(kShared && m == kNoMax));
             if (kShared ? begun : n > 0) {
 #pragma unroll 1
@@ -430,7 +426,20 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1) prefill_kernel(con
             const uint32_t zero[16] = {};
 #pragma unroll
             for (int f = 0; f < 4; ++f) tmem_st16(ts + f * 16, zero);
-          } else if (kShared && !far && !general) {
+          } else if (kShared) {
+            if (far) {  // scores in powers of two, rounded as their maximum was, take the products' place
+#pragma unroll 1
+              for (int g = 0; g < 8; ++g) {
+                const float4 gv = md.group[g];
+                uint32_t z[16];
+                tmem_ld16(ts + 16 * g, z);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 16; ++e) z[e] = __float_as_uint(fmaf(__uint_as_float(z[e]), fmaxf(fminf(mult * gv.x, 3e38f), 1e-37f), gv.y));
+                tmem_st16(ts + 16 * g, z);
+              }
+              tmem_wait_st();
+            }
 #pragma unroll 1
             for (int b = 0; b < 2; ++b) {
               float sb[2][32];
@@ -446,8 +455,8 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1) prefill_kernel(con
                 const int x = e - kLag0, f = e - kLag1;
                 if (e < 32 && e % kBlockPairs == 0) {
                   const float4 gv = md.group[4 * b + e / kBlockPairs];
-                  mm = twice(fmaxf(fminf(mult * gv.x, 3e38f), 1e-37f));  // (-inf times 0 would be NaN)
-                  bb = twice(seen ? gv.y - m : -INFINITY);
+                  mm = twice(far ? 1.0f : fmaxf(fminf(mult * gv.x, 3e38f), 1e-37f));  // (-inf times 0 would be NaN)
+                  bb = twice(!seen ? -INFINITY : far ? -m : gv.y - m);
                 }
                 if (e < 32) exponents(sb[e / 16][2 * e % 32], sb[e / 16][2 * e % 32 + 1], mm, bb);
                 if (x >= 0 && x < 32) ex2_in_order(sb[x / 16][2 * x % 32]);
@@ -487,7 +496,7 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1) prefill_kernel(con
               if (f >= 0 && f % 16 == 15) tmem_st16(ts + f / 16 * 16, p);
             }
           } else {
-            const Sight v = sight(md);
+            const Sight v = sight();
 #pragma unroll 1
             for (int g = 0; g < 8; ++g) {
               float sg[16];
@@ -700,9 +709,9 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1) prefill_kernel(con
     }
   } else {
     reg_give<C::kRegsOther>();
-    if (warp >= C::kConv0) {
+    if (warp >= kConv0) {
       // ------------------------------------------------------------------ converters
-      const int cw = warp - C::kConv0;
+      const int cw = warp - kConv0;
       int i = 0, tile0 = 0;  // sides, and tiles of the items before
       bool ok = true;
       while (ok && walk_next(walk)) {
@@ -725,11 +734,11 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1) prefill_kernel(con
             const int quad = lane & 3, sub = (lane >> 2) & 1;
             const bool all = (md.whole[0] & 1) != 0 && kv_in >= kKeys;
             // 16 steps of 8 keys, two or three to a warp; all loads first
-            constexpr int kMine = (kKeys / 8 + C::kConvs - 1) / C::kConvs;
+            constexpr int kMine = (kKeys / 8 + kConvs - 1) / kConvs;
             uint4 w[kMine][C::kHalves];
 #pragma unroll
             for (int n = 0; n < kMine; ++n) {
-              const int step = cw + n * C::kConvs, key = step * 8 + 2 * (lane >> 3) + sub;
+              const int step = cw + n * kConvs, key = step * 8 + 2 * (lane >> 3) + sub;
               if (n < kMine - 1 || step < kKeys / 8) {
                 const bool live = all || (md.group[key >> 4].w != 0.0f && key < kv_in);
 #pragma unroll
@@ -741,7 +750,7 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1) prefill_kernel(con
             }
 #pragma unroll
             for (int n = 0; n < kMine; ++n) {
-              const int step = cw + n * C::kConvs, key = step * 8 + 2 * (lane >> 3) + sub;
+              const int step = cw + n * kConvs, key = step * 8 + 2 * (lane >> 3) + sub;
               if (n < kMine - 1 || step < kKeys / 8) {
 #pragma unroll
                 for (int h = 0; h < C::kHalves; ++h) {
@@ -797,12 +806,11 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1) prefill_kernel(con
               l0 = seg0 - sb.seg0;
               const bool mine = lane >= l0 && lane < l0 + per_tile && sb.page >= 0;
               who = __ballot_sync(0xFFFFFFFFu, mine);
-              const int missing = __any_sync(0xFFFFFFFFu, lane >= l0 && lane < l0 + per_tile && ss.missing) ? 16 : 0;
               at = mine ? (static_cast<int64_t>(sb.page) * a.c.heads + it.head) * seg_bytes : -1;
               TileMeta& md = meta[tt % kMeta];
-              if (lane < 8) md.group[lane] = make_float4(0.0f, 0.0f, 1.0f, 0.0f);
+              if (lane < 8) md.group[lane] = make_float4(0.0f, -INFINITY, 1.0f, 0.0f);  // (no keys: no weight)
               if (lane == l0) {
-                md.whole[0] = (__popc(who) != per_tile ? 0 : ss.key0 >= ss.all_lo && ss.key0 + kKeys <= ss.all_hi ? 3 : 1) | ss.parts << 2 | missing;
+                md.whole[0] = (__popc(who) != per_tile ? 0 : ss.key0 >= ss.all_lo && ss.key0 + kKeys <= ss.all_hi ? 3 : 1) | ss.parts << 2;
                 md.whole[1] = ss.key0;
                 md.whole[2] = ss.end;
                 md.whole[3] = ss.seq;
@@ -919,62 +927,51 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1) prefill_kernel(con
         }
         __syncwarp();
       };
-      // kShared: each query tile has its own turn.  pend: the key tile whose scores it was given last, whose product with the
-      // values waits for the softmax, or -1.  Keys of tile n take the place of the values of tile n - 3 in the ring of three converted
-      // sides, so those are multiplied first (steps 0 and 1).  Rolled, so that each kind of product stands in the code once:
-      // sixteen warps in five roles share the instruction cache.
-      uint32_t tile = 0, np[2] = {0, 0}, side0 = 0;
+      // kShared: a warp to each query tile, so that the steps between a softmax and the next one of the same query tile are the warp's
+      // own: some 20 of them at about 200 cycles a tile, as each instruction comes from far while sixteen warps in five roles share the
+      // instruction caches.  (One warp for both: 3500 to 5500 cycles a key tile, never waiting for anything.)  The
+      // warps go through the converted sides in their order; one that does not concern a query tile is only let go.
+      uint32_t side0 = 0, tile0 = 0, turn = 0;
+      const uint32_t X = kShared ? __shfl_sync(0xFFFFFFFFu, warp - C::kMma, 0) : 0;
       while (kShared && ok && walk_next(walk)) {
         const int tiles = __shfl_sync(0xFFFFFFFFu, walk->it.kt1 - walk->it.kt0, 0);
-        bool begun[2] = {false, false};
-        int pend[2] = {-1, -1};
+        bool begun = false;
+        int pend = -1, early = -1;  // the key tile whose scores wait for their values; the one whose values were taken ahead of the next keys
         wait_all(qfull, item & 1);
 #pragma unroll 1
-        for (int n = 0; ok && n <= tiles + 1; ++n) {
-          const int must = n <= tiles ? n - 3 : tiles;  // (at the end nothing is left pending; the last values, too, take such a place)
-          uint32_t ks = 0;
-          int parts = 0;
-#pragma unroll 1
-          for (int step = 0; step < (n < tiles ? 4 : 2); ++step) {
-            const bool one = step & 1;
-            if (step == 2) {
-              const uint32_t i = side0 + side_of_keys(n);
-              ks = i % kNC;
-              wait_all(convfull + ks, (i / kNC) & 1);
-              if (!ok) break;
-              parts = __shfl_sync(0xFFFFFFFFu, meta[tile % kMeta].whole[0] >> 2, 0);
-              ++tile;
-            }
-            const uint32_t X = one ? 1 : 0;
-            const bool mine = step >= 2 && (parts >> X & 1);
-            const int j = one ? pend[1] : pend[0];
-            if (j >= 0 && (mine || (step < 2 && j <= must))) {
-              const uint32_t i = side0 + side_of_values(j, tiles), v = i % kNC, turn = one ? np[1]++ : np[0]++;
-              wait_all(convfull + v, (i / kNC) & 1);
-              wait_all(pfull + X, turn & 1);
-              if (item > 0 && !begun[0] && !begun[1]) wait_all(ofree, (item - 1) & 1);
-              if (!ok) break;
-              values(X, v, !(one ? begun[1] : begun[0]));
-              if (one) {
-                begun[1] = true;
-                pend[1] = -1;
-              } else {
-                begun[0] = true;
-                pend[0] = -1;
-              }
-              if ((one ? pend[0] : pend[1]) != j) commit(convempty + v);
-            }
-            if (mine) {
-              scores(X, ks);
-              if (one)
-                pend[1] = n;
-              else
-                pend[0] = n;
-            }
+        for (int i = 0; ok && i < 2 * tiles; ++i) {
+          const SideAt side = side_at(i, tiles);
+          if (side.v != 0 && early == side.tile) continue;
+          const uint32_t at = side0 + i, slot = at % kNC;
+          wait_all(convfull + slot, (at / kNC) & 1);
+          if (!ok) break;
+          const bool mine = side.v != 0 ? pend == side.tile : (meta[(tile0 + side.tile) % kMeta].whole[0] >> (2 + X) & 1) != 0;
+          if (!__any_sync(0xFFFFFFFFu, mine)) {
+            if (lane == 0) mbar_arrive(convempty + slot);
+            __syncwarp();
+            continue;
           }
-          if (n < tiles && ok) commit(convempty + ks);
+          if (pend >= 0) {  // the scores' place is taken by weights: they are multiplied first
+            const uint32_t v_at = side0 + side_of_values(pend, tiles), v = v_at % kNC;
+            wait_all(convfull + v, (v_at / kNC) & 1);
+            wait_all(pfull + X, turn & 1);
+            if (!begun && item > 0) wait_all(ofree, (item - 1) & 1);
+            if (!ok) break;
+            values(X, v, !begun);
+            commit(convempty + v);
+            ++turn;
+            begun = true;
+            early = side.v != 0 ? -1 : pend;
+            pend = -1;
+          }
+          if (side.v == 0) {
+            scores(X, slot);
+            commit(convempty + slot);
+            pend = side.tile;
+          }
         }
         side0 += 2 * tiles;
+        tile0 += tiles;
         if (ok) {
           commit(odone);
           ++item;
@@ -1020,8 +1017,8 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1) prefill_kernel(con
       // a wait ran out, one more commit
       if (!ok) {
         if (lane == 0) *abort_flag = 1;
-        commit(odone);
-        if (lane == 0) wait_bar_final(odone, item & 1, a.err);
+        commit(kShared ? drain + X : odone);
+        if (lane == 0) wait_bar_final(kShared ? drain + X : odone, kShared ? 0 : item & 1, a.err);
         __syncwarp();
       }
     }

@@ -123,8 +123,8 @@ struct SharedWalk {
     it.head = static_cast<int>(quotient(r, nk));
     it.ub = first + static_cast<long long>(it.head) * nk;
     it.ue = it.ub + nk;
-    it.kt0 = static_cast<int>(u - it.ub);
     const long long end = it.ue < u1 ? it.ue : u1;
+    it.kt0 = static_cast<int>(u - it.ub);
     it.kt1 = static_cast<int>(end - it.ub);
     u = end;
     return 1;
@@ -273,8 +273,12 @@ __device__ __forceinline__ void share_out(const AttArgs& a, int2* grp, ScanShare
 
 // An item's stream: its segments in order, [0] the prefix.  seg = {tiles up to its end, first key tile, sequence or -1, end of
 // what is seen}.
+// Own tiles of the prefill kernel's full items are taken in turn from the sequences of the first and of the second query tile, so
+// that one's softmax runs under the other's products (128 sequences of up to 4000 positions of their own: 321 -> @@ us): behind the prefix
+// come those of a sequence that has rows in both, then one of `half[0]` and one of `half[1]` each, then the rest.
 struct Plan {
   int count;
+  int prefix, half0, both, half1;  // tiles, in the order of the segments
   int seq0, seq1;        // the group's sequences
   int pre_lo;            // from here on every row sees the prefix
   int one_lo, one_hi;    // where all rows are of one sequence: what they all see of its own
@@ -283,11 +287,15 @@ struct Plan {
 // One warp makes the plan of the walk's item.
 template <int kKeys, class W>
 __device__ __forceinline__ void make_plan(const W* w, Plan* plan, int4* seg) {
+  // the rows of the second query tile begin here, counted in the group's rows
+  const long long half = static_cast<long long>(w->it.row0) + (W::kRowsOf > 128 && w->it.rows > W::kRowsOf / 2 ? W::kRowsOf / 2 : W::kRowsOf);
   const Item& it = w->it;
   const int lane = threadIdx.x & 31, s0 = w->grp[it.b].x, s1 = w->grp[it.b + 1].x, p = it.hi;
   const int t0 = it.tok0 + w->token_of(it.row0), t1 = it.tok0 + w->token_of(it.row0 + it.rows - 1);
   const int first = w->seq_of(t0, s0, s1);
   int end = tiles_between<kKeys>(it.lo, p), count = 1, pre_lo = 0, one_lo = 0, one_hi = 0;
+  int first_half = 0, in_both = 0;
+  const int prefix = end;
   if (lane == 0) seg[0] = make_int4(end, it.lo / kKeys, -1, p);
   for (int s_at = first;; s_at += 32) {
     const int s = s_at + lane;
@@ -303,6 +311,12 @@ __device__ __forceinline__ void make_plan(const W* w, Plan* plan, int4* seg) {
       }
     }
     const int mine = tiles_between<kKeys>(lo, hi);
+    if (mine > 0) {
+      if (static_cast<long long>(w->cu[s + 1] - it.tok0) * w->group <= half)
+        first_half += mine;
+      else if (static_cast<long long>(w->cu[s] - it.tok0) * w->group < half)
+        in_both += mine;
+    }
     int incl = mine;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
@@ -318,8 +332,24 @@ __device__ __forceinline__ void make_plan(const W* w, Plan* plan, int4* seg) {
   pre_lo = __reduce_max_sync(0xFFFFFFFFu, pre_lo);
   one_lo = __reduce_max_sync(0xFFFFFFFFu, one_lo);
   one_hi = __reduce_max_sync(0xFFFFFFFFu, one_hi);
-  if (lane == 0) *plan = Plan{count, s0, s1, pre_lo, one_lo, one_hi};
+  first_half = __reduce_add_sync(0xFFFFFFFFu, first_half);
+  in_both = __reduce_add_sync(0xFFFFFFFFu, in_both);
+  if (lane == 0)
+    *plan = Plan{count, prefix, first_half, in_both, end - prefix - first_half - in_both, s0, s1, pre_lo, one_lo, one_hi};
   __syncwarp();
+}
+
+// The v-th tile that is taken, counted in the order of the segments.
+__device__ __forceinline__ int in_turn(const Plan* plan, int v) {
+  int u = v - plan->prefix;
+  if (u < 0) return v;
+  const int n0 = plan->half0, n1 = plan->half1, both = plan->both;
+  if (u < both) return plan->prefix + n0 + u;
+  u -= both;
+  const int turns = min(n0, n1);
+  const bool second = u < 2 * turns ? (u & 1) != 0 : n1 > n0;
+  const int i = u < 2 * turns ? u >> 1 : u - turns;
+  return plan->prefix + (second ? n0 + both : 0) + i;
 }
 
 // Key tile v of the stream: its segment (or -1), the position of its first key.
@@ -344,7 +374,6 @@ __device__ __forceinline__ int seg_of(const int4* seg, int count, int v, int& ke
 // Which query tiles it concerns (bits 0 and 1): see the kernel.
 struct SharedSegs {
   int key0 = 0, end = 0, seq = -1, all_lo = 0, all_hi = 0, parts = 1;
-  bool missing = false;  // the lane's page has no place in the cache
 };
 template <int kKeys, class W>
 __device__ __forceinline__ SegBatch load_shared_segs(const AttArgs& a, const W& w, const Plan* plan, const int4* seg, int page0,
@@ -356,7 +385,7 @@ __device__ __forceinline__ SegBatch load_shared_segs(const AttArgs& a, const W& 
   x = SharedSegs{};
   const bool narrow = it.rows <= W::kRowsOf / 2;
   if (narrow) x.parts = 1 << (v & 1);
-  const int at = v < it.kt1 ? seg_of<kKeys>(seg, plan->count, v, x.key0) : -1;
+  const int at = v < it.kt1 ? seg_of<kKeys>(seg, plan->count, in_turn(plan, v), x.key0) : -1;
   if (at < 0) return s;
   const int4 sg = seg[at];
   x.end = sg.w;
@@ -389,7 +418,6 @@ __device__ __forceinline__ SegBatch load_shared_segs(const AttArgs& a, const W& 
       s.ek = min(max(static_cast<int>(a.c.k_exp[ph]), kKvMinExp), kKvMaxExp);
       s.ev = min(max(static_cast<int>(a.c.v_exp[ph]), kKvMinExp), kKvMaxExp);
     } else {
-      x.missing = true;
       atomicOr(a.err, kErrInvalid);
     }
   }

@@ -60,7 +60,7 @@ void check(int seed) {
   if (sh.total == 0) return;
   sh.runs = static_cast<int>(sh.total < grid ? sh.total : grid);
   long long at = 0;
-  int cut = 0;
+  int cut = 0, tile_after = 0;
   for (int c = 0; c < sh.runs; ++c) {
     W x = w;
     x.u = run_start(c, &sh);
@@ -69,8 +69,10 @@ void check(int seed) {
     x.start(0, 0, 0);
     while (x.next()) {
       const Item& it = x.it;
-      const long long n = it.kt1 - it.kt0;
-      REQUIRE(n > 0 && it.ub <= at && at + n <= it.ue && at - it.ub == it.kt0);
+      const long long n = x.u - at;                       // units; tiles go on where the run before stopped
+      REQUIRE(n > 0 && it.ub <= at && at + n <= it.ue && it.kt0 < it.kt1);
+      REQUIRE(at == it.ub ? it.kt0 == 0 : it.kt0 == tile_after);
+      tile_after = it.kt1;
       at += n;
       cut += it.ub < u0 || it.ue > u1;
       // the tiles of the item: the prefix's and each sequence's; every key that a row sees lies in one of them, once
@@ -95,6 +97,7 @@ void check(int seed) {
         }
       }
       REQUIRE(it.ue - it.ub == std::max(total, 1));
+      if (at == it.ue) REQUIRE(it.kt1 == std::max(total, 1));
     }
     REQUIRE(at == u1);
   }
