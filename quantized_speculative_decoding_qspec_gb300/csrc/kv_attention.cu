@@ -6,9 +6,10 @@ namespace qspec {
 namespace att {
 namespace {
 
-// The workspace: tickets, then two partial items per CTA.  Its layout does not depend on the call's shape.
+// The workspace: tickets, then two partial items per CTA, then the items that runs have cut.  Its layout does not depend on the call's shape.
 constexpr size_t kTicketBytes = 24576;  // three a CTA
 constexpr int kMaxGrid = 2048;
+constexpr size_t kCutBytes = sizeof(CutItem) * kMaxGrid;
 constexpr size_t slot_bytes(int rows) { return sizeof(float) * 2 * rows * (128 + 2); }  // of a CTA, heads of 128
 
 int max_grid(int ctas_per_sm) {
@@ -36,7 +37,10 @@ qspec_status launch_prefill(AttArgs& a, int64_t rows, cudaStream_t s) {
   if (cudaFuncSetAttribute(prefill_kernel<D, kBigPages, kShared>, cudaFuncAttributeMaxDynamicSharedMemorySize, fixed + each * (most + 1)) !=
       cudaSuccess)
     return QSPEC_ERR_CUDA;
-  return launch_pdl(prefill_kernel<D, kBigPages, kShared>, dim3(max_grid(1)), dim3(C::kThreads), fixed + each * (owners + 1), s, a);
+  const qspec_status st =
+      launch_pdl(prefill_kernel<D, kBigPages, kShared>, dim3(max_grid(1)), dim3(C::kThreads), fixed + each * (owners + 1), s, a);
+  if (!kShared || st != QSPEC_OK) return st;
+  return launch_pdl(merge_kernel<D>, dim3(max_grid(1), kMergeSplit), dim3(C::kRows), 0, s, a);
 }
 
 template <bool kShared>
@@ -62,7 +66,7 @@ using namespace qspec::att;
 
 extern "C" size_t qspec_kv_attention_workspace_size(void) {
   const size_t few = max_grid(4) * slot_bytes(DecodeCfg<128, 1>::kRows), many = max_grid(1) * slot_bytes(PrefillCfg<128>::kRows);
-  return kTicketBytes + (few > many ? few : many);
+  return kTicketBytes + (few > many ? few : many) + kCutBytes;
 }
 
 namespace {
@@ -88,6 +92,7 @@ qspec_status prepare(const qspec_kv_cache* cache, const qspec_kv_batch* batch, c
   if (!a.err) return QSPEC_ERR_CUDA;
   a.tickets = static_cast<unsigned int*>(ws);
   a.partial = reinterpret_cast<float*>(static_cast<char*>(ws) + kTicketBytes);
+  a.cuts = reinterpret_cast<CutItem*>(static_cast<char*>(ws) + qspec_kv_attention_workspace_size() - kCutBytes);
   a.q_token = q_token;
   a.out_token = out_token;
   a.heads_q = heads_q;

@@ -59,6 +59,50 @@ struct PrefillCfg {
   static_assert(kSharedState <= kState && kSmemShared + sizeof(int2) * (QSPEC_KV_MAX_GROUPS + 1) <= 227 * 1024, "shared memory");
 };
 
+// kShared: adds the parts of the items that runs have cut.  A CTA to an item (that begins in run blockIdx.x) and kMergeSplit of its
+// channels, a thread to a row: few items are cut into many parts here, and one SM reads at 125 GB/s (added by the last CTA to
+// arrive, ten parts of 256 rows took 27 us; by groups, the code alone slowed the softmax down by a tenth).
+constexpr int kMergeSplit = 8;
+template <int D>
+__global__ void __launch_bounds__(PrefillCfg<D>::kRows) merge_kernel(const AttArgs a) {
+  constexpr int kRows = PrefillCfg<D>::kRows, kSlot = kRows * (D + 2), kQuads = D / 4 / kMergeSplit;  // of four channels
+  ptx::grid_launch_dependents();
+  ptx::grid_dependency_wait();
+  const CutItem it = a.cuts[blockIdx.x];
+  const int r = threadIdx.x, c0 = blockIdx.x, q0 = blockIdx.y * kQuads;
+  if (r >= it.rows || it.parts == 0) return;
+  auto part = [&](int k) { return a.partial + (static_cast<int64_t>(c0 + k) * 2 + (k == 0 ? 1 : 0)) * kSlot; };
+  float mm = kNoMax, ll = 0.0f;
+#pragma unroll 8
+  for (int k = 0; k < it.parts; ++k) mm = fmaxf(mm, __ldcg(part(k) + kRows * D + 2 * r));
+  float4 acc[kQuads];
+#pragma unroll
+  for (int e = 0; e < kQuads; ++e) acc[e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+  for (int k = 0; k < it.parts; ++k) {
+    const float* p = part(k);
+    const float2 x = __ldcg(reinterpret_cast<const float2*>(p + kRows * D + 2 * r));
+    const float f = ex2(x.x - mm);
+    ll = fmaf(x.y, f, ll);
+#pragma unroll
+    for (int e = 0; e < kQuads; ++e) {
+      const float4 v = __ldcg(reinterpret_cast<const float4*>(p + ((q0 + e) * kRows + r) * 4));
+      acc[e].x = fmaf(v.x, f, acc[e].x);
+      acc[e].y = fmaf(v.y, f, acc[e].y);
+      acc[e].z = fmaf(v.z, f, acc[e].z);
+      acc[e].w = fmaf(v.w, f, acc[e].w);
+    }
+  }
+  const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
+  const int tk = a.token_of(it.row0 + r), hq = it.head * a.group + it.row0 + r - tk * a.group;
+  uint16_t* op = a.out + static_cast<int64_t>(it.tok0 + tk) * a.out_token + static_cast<int64_t>(hq) * D + 4 * q0;
+#pragma unroll
+  for (int e = 0; e < kQuads; ++e)
+    *reinterpret_cast<uint2*>(op + 4 * e) = make_uint2(pack_bf16(acc[e].x * inv, acc[e].y * inv), pack_bf16(acc[e].z * inv, acc[e].w * inv));
+  if (a.lse && blockIdx.y == 0)
+    a.lse[static_cast<int64_t>(it.tok0 + tk) * a.heads_q + hq] = ll == 0.0f ? -INFINITY : (mm + log2f(ll)) * 0.693147180559945f;
+}
+
 // Side i of an item of T tiles in that order: its tile, and whether it is the values.
 struct SideAt {
   int tile, v;
@@ -146,6 +190,7 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1) prefill_kernel(con
   }
   grid_launch_dependents();
   grid_dependency_wait();
+  if (kShared && threadIdx.x == 0) a.cuts[blockIdx.x].parts = 0;
   tc_fence_before();
   W* walk = walks + warp;  // (in shared memory: its state would cost every role 40 registers)
   long long run0, run1;
@@ -639,7 +684,9 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1) prefill_kernel(con
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(ofree);
-      if (!whole) {
+      if (kShared && !whole && it.ub >= run0 && threadIdx.x == 0)
+        a.cuts[blockIdx.x] = CutItem{owner_of(it.ue - 1, scan) - static_cast<int>(blockIdx.x) + 1, it.tok0, it.row0, it.rows, it.head};
+      if (!kShared && !whole) {
         const int c0 = owner_of(it.ub, scan), c1 = owner_of(it.ue - 1, scan);
         named_bar_sync(1, 256);
         if (threadIdx.x == 0) {
@@ -1033,7 +1080,7 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1) prefill_kernel(con
   // A run given up (the softmax left its walk half way) still arrives wherever it would have: the outputs are void, but
   // the workspace's tickets are back at zero when the call ends.  (Here and not where the softmax leaves: there the
   // walk's registers cost 376 -> 394 us, 4096 tokens over 8192 positions.)
-  if (*abort_flag && threadIdx.x == 0) {
+  if (!kShared && *abort_flag && threadIdx.x == 0) {
     const long long c = blockIdx.x, u0 = run_start(c, scan), u1 = run_start(c + 1, scan);
     while (walks->next_cut(u0, u1)) {
       const int c0 = owner_of(walks->it.ub, scan), c1 = owner_of(walks->it.ue - 1, scan);

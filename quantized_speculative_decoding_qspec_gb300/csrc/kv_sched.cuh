@@ -30,6 +30,11 @@ __device__ __forceinline__ float reference_of(float top) { return fabsf(top) < k
 
 constexpr int kSmemPerSm = 228 * 1024, kSmemReserved = 1024;  // of sm_103: an SM's shared memory, and what a CTA takes unseen
 
+struct CutItem {
+  int parts, tok0, row0, rows, head;  // parts: runs with a part of it, or 0: none
+  int pad[3];
+};
+
 struct AttArgs {
   qspec_kv_cache c;
   qspec_kv_batch b;
@@ -49,6 +54,7 @@ struct AttArgs {
   const int32_t* cu_seq;  // [groups + 1]
   const int32_t* prefix;  // [groups]
   int groups, group_tok;  // group_tok: new tokens of a group at most
+  CutItem* cuts;          // [grid], prefill kernel: the item that begins in each run and goes on in the next
 
   __device__ int token_of(int packed) const {
     return static_cast<int>(static_cast<uint64_t>(static_cast<uint32_t>(packed)) * group_mul >> group_shift);

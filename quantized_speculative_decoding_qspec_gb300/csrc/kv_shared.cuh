@@ -275,7 +275,7 @@ __device__ __forceinline__ void share_out(const AttArgs& a, int2* grp, ScanShare
 // what is seen}.
 // Own tiles of the prefill kernel's full items are taken in turn from the sequences of the first and of the second query tile, so
 // that one's softmax runs under the other's products (128 sequences of up to 4000 positions of their own: 321 -> @@ us): behind the prefix
-// come those of a sequence that has rows in both, then one of `half[0]` and one of `half[1]` each, then the rest.
+// come those of a sequence that has rows in both, then the others in proportion to what each query tile has.
 struct Plan {
   int count;
   int prefix, half0, both, half1;  // tiles, in the order of the segments
@@ -346,10 +346,10 @@ __device__ __forceinline__ int in_turn(const Plan* plan, int v) {
   const int n0 = plan->half0, n1 = plan->half1, both = plan->both;
   if (u < both) return plan->prefix + n0 + u;
   u -= both;
-  const int turns = min(n0, n1);
-  const bool second = u < 2 * turns ? (u & 1) != 0 : n1 > n0;
-  const int i = u < 2 * turns ? u >> 1 : u - turns;
-  return plan->prefix + (second ? n0 + both : 0) + i;
+  const int n = n0 + n1;
+  const auto first_of = [&](int k) { return static_cast<int>((static_cast<long long>(k) * n0 + n - 1) / n); };  // among the first k
+  const int before = first_of(u);
+  return plan->prefix + (first_of(u + 1) > before ? before : n0 + both + u - before);
 }
 
 // Key tile v of the stream: its segment (or -1), the position of its first key.
