@@ -3,8 +3,10 @@
 //     S(k, v) = score[k] + (logit[k, v] - lse[k]),   lse[k] = ln sum_v exp(logit[k, v])
 // Within a beam the order is that of its logits (bf16: ties are common, and go to the lowest token), so each beam offers its n
 // largest logits, and the beams' offers are ordered by S (times a weight).  One pass over the logits bounds it: a CTA
-// holds a tile of a row in registers, reduces maximum and sum of exponentials, and collects the few logits that
-// reach a lower bound of its n-th largest.  The last CTA of a sequence (atomic ticket) merges the offers.
+// streams a part of a row through registers, a tile of 16384 at a time.  A thread keeps its own maximum and sum of exponentials;
+// the first tile gives a lower bound of the n-th largest logit, and the few that reach it are collected in shared memory,
+// with the loads of two tiles under way.  The last CTA of a sequence (atomic ticket) merges the offers.
+// (A tile of 32768 to a CTA, selected and handed over before the next CTA began: [64, 8, 152064] 102 us.)
 #include <math.h>
 
 #include "kv_internal.h"
@@ -13,13 +15,14 @@ namespace qspec {
 namespace {
 
 constexpr int kThreads = 512, kWarps = kThreads / 32;
-constexpr int kVecs = 8;                          // 16-byte loads in flight a thread: 32 registers, two CTAs an SM
-constexpr int kTileVecs = kThreads * kVecs;       // 32768 logits
-constexpr int kTile = kTileVecs * 8;
-constexpr int kList = 1024;                       // logits collected at most; more: see exact_bound
+constexpr int kVecs = 4;                          // 16-byte loads in flight a thread
+constexpr int kTileVecs = kThreads * kVecs;       // 16384 logits
+constexpr int kList = 1024;                       // logits collected at most; a tile that brings more: see below
+constexpr int kListFull = 512;                    // from here on they are cut down to the n best
+constexpr int kCheck = 4;                         // tiles between looks at the list
+constexpr int kCtasPerSm = 2;                     // resident, and asked for
 constexpr int kMaxN = QSPEC_BEAM_MAX_N, kMaxBeams = QSPEC_BEAM_MAX_BEAMS;
 constexpr int kMaxLists = kThreads;               // (beam, chunk) pairs of a sequence: a thread each in the merge
-constexpr int kStage = 4096;                      // offers of a sequence that are merged from shared memory
 constexpr uint32_t kLowest = 0xFF80FF80u;         // two bf16 -inf
 
 struct BeamArgs {
@@ -68,42 +71,35 @@ __device__ __forceinline__ unsigned long long ordered64(double x) {
 
 struct BeamShared {
   union {
-    unsigned long long list[kList];
-    unsigned long long stage[kStage];
+    unsigned long long list[kList + kMaxN];
+    unsigned long long head[kMaxLists];
   };
+  unsigned long long pair_key[kMaxN * (kMaxN + 1) / 2];
+  uint16_t pair_order[kMaxN * (kMaxN + 1) / 2];
+  int best_list[kMaxN];
   unsigned long long top[kMaxN];
   uint32_t group[64];
   float2 warp_stat[kWarps];
-  unsigned int counts[2];
-  unsigned long long best[2][kWarps];
-  int best_at[2][kWarps];
+  int count;
   double lse[kMaxBeams];
+  float2 row_stat[kMaxBeams];
   int n_list, last;
 };
 
-struct Best {
-  unsigned long long key;
-  int at;
+struct Candidate {
+  unsigned long long key;  // of S times the weight
+  double S;
+  int row, tok;
 };
-// The largest key of the warp, the lowest lane among equal ones.
-__device__ __forceinline__ Best warp_best(unsigned long long key, int at) {
-  const uint32_t hi = __reduce_max_sync(0xFFFFFFFFu, static_cast<uint32_t>(key >> 32));
-  const uint32_t lo = __reduce_max_sync(0xFFFFFFFFu, static_cast<uint32_t>(key >> 32) == hi ? static_cast<uint32_t>(key) : 0u);
-  const unsigned long long top = static_cast<unsigned long long>(hi) << 32 | lo;
-  const int first = __reduce_min_sync(0xFFFFFFFFu, key == top ? at : 0x7FFFFFFF);
-  return {top, first};
-}
 
-// The last CTA of sequence b: the beams' sums, then n times the best of what the lists offer next.
+// The last CTA of sequence b: the beams' sums, then the n best of what the lists offer.
 __device__ __noinline__ void merge(const BeamArgs& a, BeamShared& sh, int b) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int lists = a.K * a.chunks, count = lists * a.n;
+  const int lists = a.K * a.chunks, n = a.n;
   const float2* stats = a.stats + static_cast<long long>(b) * lists;
-  const unsigned long long* offers = a.offers + static_cast<long long>(b) * count;
-  const bool staged = count <= kStage;
-  if (staged)
-    for (int i = tid; i < count; i += kThreads) sh.stage[i] = __ldcg(offers + i);
-  // lse[k]: a warp to a beam; NaN where the beam offers nothing
+  const unsigned long long* offers = a.offers + static_cast<long long>(b) * lists * n;
+  // lse[k], a warp to a beam; NaN where the beam offers nothing.  (fp64 runs at a fiftieth of fp32's rate: one logarithm for all beams
+  // at once, in a warp's lanes; with an exponential for each chunk and a logarithm in each warp this took 10 us.)
   for (int k = warp; k < a.K; k += kWarps) {
     float m = -INFINITY;
     bool nan = false;
@@ -115,79 +111,297 @@ __device__ __noinline__ void merge(const BeamArgs& a, BeamShared& sh, int b) {
 #pragma unroll
     for (int off = 16; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, off));
     nan = __any_sync(0xFFFFFFFFu, nan) || m == INFINITY;
-    double sum = 0.0;
+    float sum = 0.0f;
     if (!nan && m > -INFINITY)
       for (int c = lane; c < a.chunks; c += 32) {
         const float2 x = __ldcg(stats + k * a.chunks + c);
-        if (x.x > -INFINITY) sum += static_cast<double>(x.y) * exp(static_cast<double>(x.x) - static_cast<double>(m));
+        if (x.x > -INFINITY) sum += x.y * pow2((x.x - m) * kLog2e);
       }
 #pragma unroll
     for (int off = 16; off >= 1; off >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, off);
-    if (lane == 0) {
-      const float s = a.scores[static_cast<long long>(b) * a.K + k], w = a.weights ? a.weights[static_cast<long long>(b) * a.K + k] : 1.0f;
-      const bool done = a.done && a.done[static_cast<long long>(b) * a.K + k] != 0;
-      const bool odd = !(s < INFINITY) || !(w > 0.0f && w < INFINITY) || (nan && !done);
-      if (odd) atomicOr(a.err, kErrInvalid);
-      const bool none = odd || s == -INFINITY || (!done && !(m > -INFINITY));
-      sh.lse[k] = none ? NAN : done ? 0.0 : static_cast<double>(m) + log(sum);
-    }
+    if (lane == 0) sh.row_stat[k] = nan ? make_float2(NAN, 0.0f) : make_float2(m, sum);
+  }
+  __syncthreads();
+  if (tid < a.K) {
+    const long long at = static_cast<long long>(b) * a.K + tid;
+    const float2 x = sh.row_stat[tid];
+    const float s = a.scores[at], w = a.weights ? a.weights[at] : 1.0f;
+    const bool done = a.done && a.done[at] != 0;
+    const bool odd = !(s < INFINITY) || !(w > 0.0f && w < INFINITY) || (x.x != x.x && !done);
+    if (odd) atomicOr(a.err, kErrInvalid);
+    const bool none = odd || s == -INFINITY || (!done && !(x.x > -INFINITY));
+    const double lse = static_cast<double>(x.x) + log(static_cast<double>(x.y));
+    sh.lse[tid] = none ? NAN : done ? 0.0 : lse;
   }
   __syncthreads();
 
-  // ---- a thread to a list
-  const int k = tid / a.chunks, chunk = tid - k * a.chunks;
-  int at = 0;                                    // of the list's next offer
-  unsigned long long key = 0, offer = 0;
-  double S = 0.0, score = 0.0, lse = 0.0, weight = 1.0;
-  bool done = false;
-  if (tid < lists) {
-    lse = sh.lse[k];
-    score = a.scores[static_cast<long long>(b) * a.K + k];
-    if (a.weights) weight = a.weights[static_cast<long long>(b) * a.K + k];
-    done = a.done && a.done[static_cast<long long>(b) * a.K + k] != 0;
-    if (lse != lse || (done && chunk != 0)) at = a.n;
-  } else {
-    at = a.n;
-  }
-  auto look = [&]() {
-    key = 0;
-    if (at >= a.n) return;
-    if (done) {
-      S = score;
+  // ---- the best n lists by their first offers, in order: the r-th can give n - r of the n best.  (Choosing the n best one after
+  // the other by reductions over the lists took 5 to 7 us for eight.)
+  auto candidate = [&](int list, int e, Candidate& c) {  // false: no offer
+    const int k = list / a.chunks;
+    const long long at = static_cast<long long>(b) * a.K + k;
+    const double lse = sh.lse[k];
+    if (lse != lse) return false;
+    c.S = a.scores[at];
+    c.tok = a.end_tok;
+    c.row = static_cast<int>(at);
+    if (a.done && a.done[at] != 0) {
+      if (e > 0 || list != k * a.chunks) return false;
     } else {
-      offer = staged ? sh.stage[tid * a.n + at] : __ldcg(offers + static_cast<long long>(tid) * a.n + at);
-      if (offer == 0) return;
-      S = score + (static_cast<double>(value_of(static_cast<uint32_t>(offer >> 32))) - lse);
+      const unsigned long long offer = __ldcg(offers + static_cast<long long>(list) * n + e);
+      if (offer == 0) return false;
+      c.tok = static_cast<int>(~static_cast<uint32_t>(offer));
+      c.S += static_cast<double>(value_of(static_cast<uint32_t>(offer >> 32))) - lse;
     }
-    key = ordered64(S * weight);
+    c.key = ordered64(a.weights ? c.S * a.weights[at] : c.S);
+    return true;
   };
-  look();
-  const int warps = (lists + 31) / 32;
-  for (int i = 0; i < a.n; ++i) {
-    Best best = warp_best(key, tid);
-    if (warps > 1) {
-      if (lane == 0) {
-        sh.best[i & 1][warp] = best.key;
-        sh.best_at[i & 1][warp] = best.at;
-      }
-      __syncthreads();
-      best = lane < warps ? Best{sh.best[i & 1][lane], sh.best_at[i & 1][lane]} : Best{0, 0x7FFFFFFF};
-      best = warp_best(best.key, best.at);
+  Candidate c;
+  const unsigned long long head = tid < lists && candidate(tid, 0, c) ? c.key : 0;
+  sh.head[tid] = head;
+  if (tid < n) sh.best_list[tid] = -1;
+  if (tid == 0) sh.count = 0;
+  __syncthreads();
+  if (head != 0) {
+    int place = 0;
+    for (int j = 0; j < lists; ++j) place += sh.head[j] > head || (sh.head[j] == head && j < tid);
+    if (place < n) sh.best_list[place] = tid;
+  }
+  __syncthreads();
+  const int pairs = n * (n + 1) / 2;
+  for (int p = tid; p < pairs; p += kThreads) {
+    int r = 0, e = p;
+    while (e >= n - r) e -= n - r++;
+    const int list = sh.best_list[r];
+    const bool real = list >= 0 && candidate(list, e, c);
+    sh.pair_key[p] = real ? c.key : 0;
+    sh.pair_order[p] = static_cast<uint16_t>(list << 6 | e);
+    if (real) atomicAdd(&sh.count, 1);
+  }
+  static_assert(kMaxLists <= 1 << 9 && kMaxN <= 1 << 6, "a list and a place in it have 16 bits");
+  __syncthreads();
+  for (int p = tid; p < pairs; p += kThreads) {
+    const unsigned long long key = sh.pair_key[p];
+    const uint16_t order = sh.pair_order[p];
+    if (key == 0) continue;
+    int place = 0;
+    for (int j = 0; j < pairs; ++j) place += sh.pair_key[j] > key || (sh.pair_key[j] == key && sh.pair_order[j] < order);
+    if (place < n && candidate(order >> 6, order & 63, c)) {
+      const long long out = static_cast<long long>(b) * n + place;
+      a.parent[out] = c.row;
+      a.tok[out] = c.tok;
+      a.score[out] = static_cast<float>(c.S);
     }
-    const long long out = static_cast<long long>(b) * a.n + i;
-    if (best.key == 0) {
-      if (tid == 0) {
-        a.parent[out] = -1;
-        a.tok[out] = -1;
-        a.score[out] = -INFINITY;
-      }
-    } else if (best.at == tid) {
-      a.parent[out] = b * a.K + k;
-      a.tok[out] = done ? a.end_tok : static_cast<int>(~static_cast<uint32_t>(offer));
-      a.score[out] = static_cast<float>(S);
-      at = done ? a.n : at + 1;
-      look();
+  }
+  if (tid < n && tid >= sh.count) {
+    const long long out = static_cast<long long>(b) * n + tid;
+    a.parent[out] = -1;
+    a.tok[out] = -1;
+    a.score[out] = -INFINITY;
+  }
+}
+
+// A chunk of a row in aligned 16-byte vectors; all places count from the first of them (a row has at most 2^24 logits).
+struct Chunk {
+  const uint16_t* from;
+  int lo, hi, vecs;      // the chunk's logits are lo .. hi - 1
+  uint32_t first_token;  // of place 0 (wraps below a row's first)
+};
+
+// The thread's vectors of the tile at t0; -inf outside the chunk.
+__device__ __forceinline__ void load_tile(const Chunk& c, int t0, uint4 (&x)[kVecs]) {
+#pragma unroll
+  for (int i = 0; i < kVecs; ++i) {
+    const int v = t0 + i * kThreads + threadIdx.x;
+    x[i] = make_uint4(kLowest, kLowest, kLowest, kLowest);
+    if (v >= c.vecs) continue;
+    if (8 * v >= c.lo && 8 * v + 8 <= c.hi) {
+      x[i] = ld_stream_v4(c.from + 8 * v);
+    } else {  // the chunk's first or last vector: what is its own
+      uint32_t* w = reinterpret_cast<uint32_t*>(&x[i]);
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (8 * v + e >= c.lo && 8 * v + e < c.hi)
+          w[e >> 1] = e & 1 ? (w[e >> 1] & 0xFFFFu) | static_cast<uint32_t>(c.from[8 * v + e]) << 16
+                            : (w[e >> 1] & 0xFFFF0000u) | c.from[8 * v + e];
     }
+  }
+}
+__device__ __forceinline__ uint32_t key_of(const uint4 (&x)[kVecs], int i, int e) {
+  const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+  return ordered(e & 1 ? w[e >> 1] >> 16 : w[e >> 1] & 0xFFFFu);
+}
+// Collects a logit; false where the list is filling up.
+__device__ __forceinline__ bool collect(BeamShared& sh, uint32_t key, uint32_t token) {
+  const int at = atomicAdd(&sh.n_list, 1);
+  if (at < kList + kMaxN) sh.list[at] = static_cast<unsigned long long>(key) << 32 | (0xFFFFFFFFu - token);
+  return at < kListFull;
+}
+
+// Collects what reaches the bound among the vectors of the lanes `who`, whose logits begin at `token` + 8 lanes: the warp takes one
+// vector after the other, eight lanes a logit each.  False where the list is filling up.  (A short loop of its own: every other warp
+// comes here in each tile, and with the 32 comparisons of a lane written out for one lane it spent 2500 cycles, as code that is seldom run
+// comes from far: [64, 8, 152064] 95 us, without any collecting 48.)
+__device__ __noinline__ bool collect_vectors(BeamShared& sh, uint4 x, uint32_t who, uint32_t token, uint32_t bound) {
+  const int lane = threadIdx.x & 31;
+  bool room = true;
+#pragma unroll 1
+  for (; who; who &= who - 1) {
+    const int src = __ffs(who) - 1;
+    const uint32_t w0 = __shfl_sync(0xFFFFFFFFu, x.x, src), w1 = __shfl_sync(0xFFFFFFFFu, x.y, src);
+    const uint32_t w2 = __shfl_sync(0xFFFFFFFFu, x.z, src), w3 = __shfl_sync(0xFFFFFFFFu, x.w, src);
+    const uint32_t lo = lane & 2 ? w1 : w0, hi = lane & 2 ? w3 : w2, w = lane & 4 ? hi : lo;
+    const uint32_t key = ordered(lane & 1 ? w >> 16 : w & 0xFFFFu);
+    if (lane < 8 && key >= bound) room = collect(sh, key, token + 8 * src + lane) && room;
+  }
+  return room;
+}
+
+// The n best of the list's first `count` entries, in order, become the list (and top): a key's place is the number of larger
+// ones.  All threads; ends with a barrier.
+__device__ __noinline__ void cut_down(BeamShared& sh, int count, int n) {
+  const int tid = threadIdx.x;
+  if (tid < kMaxN) sh.top[tid] = 0;
+  __syncthreads();
+  for (int i = tid; i < count; i += kThreads) {
+    const unsigned long long key = sh.list[i];
+    int place = 0;
+    for (int j = 0; j < count; ++j) place += sh.list[j] > key;
+    if (place < n && key != 0) sh.top[place] = key;
+  }
+  __syncthreads();
+  if (tid < n) sh.list[tid] = sh.top[tid];
+  if (tid == 0) sh.n_list = n;
+  __syncthreads();
+}
+
+// The tiles from t0 on, kCheck of them, brought far more logits than the list has places, as with many equal ones: what came from
+// them is taken out again, and their exact n-th largest (logit, lowest token) found bit by bit.  Returns the number of entries.
+__device__ __noinline__ int exact_tiles(BeamShared& sh, const Chunk& c, int t0, int n) {
+  const int tid = threadIdx.x;
+  const uint32_t tile0 = c.first_token + 8 * t0;
+  for (int i = tid; i < kList; i += kThreads)
+    if (0xFFFFFFFFu - static_cast<uint32_t>(sh.list[i]) - tile0 < 8u * kCheck * kTileVecs) sh.list[i] = 0;
+  uint4 x[kVecs];
+  auto rank_of = [&](int k, int i, int e) {
+    return key_of(x, i, e) << 16 | (0xFFFFu - static_cast<uint32_t>((k * kTileVecs + i * kThreads + tid) * 8 + e));
+  };
+  static_assert(8 * kCheck * kTileVecs <= 0x10000, "a place in these tiles has 16 bits");
+  uint32_t exact = 0;
+  for (int bit = 31; bit >= 0; --bit) {
+    const uint32_t cand = exact | 1u << bit;
+    int count = 0;
+#pragma unroll 1
+    for (int k = 0; k < kCheck; ++k) {
+      load_tile(c, t0 + k * kTileVecs, x);
+#pragma unroll
+      for (int i = 0; i < kVecs; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) count += rank_of(k, i, e) >= cand;
+    }
+    count = __reduce_add_sync(0xFFFFFFFFu, count);
+    if (tid == 0) sh.count = 0;
+    __syncthreads();
+    if ((tid & 31) == 0 && count) atomicAdd(&sh.count, count);
+    __syncthreads();
+    if (sh.count >= n) exact = cand;
+    __syncthreads();
+  }
+  if (tid == 0) sh.n_list = kList;
+  __syncthreads();
+#pragma unroll 1
+  for (int k = 0; k < kCheck; ++k) {
+    load_tile(c, t0 + k * kTileVecs, x);
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const uint32_t key = key_of(x, i, e);
+        if (key > kKeyLowest && rank_of(k, i, e) >= exact) collect(sh, key, tile0 + 8 * (k * kTileVecs + i * kThreads + tid) + e);
+      }
+  }
+  __syncthreads();
+  return sh.n_list;
+}
+
+// What a thread carries from tile to tile.
+struct Running {
+  float m, s;      // its maximum and sum of exponentials
+  uint32_t bound;  // of the n-th largest logit, from below
+  bool bad;        // a NaN or +inf among its logits
+  bool crowded;    // it found the list filling up
+};
+
+__device__ __forceinline__ void take_tile(BeamShared& sh, const Chunk& c, int n, int t0, uint4 (&x)[kVecs], Running& r) {
+  const int tid = threadIdx.x, lane = tid & 31;
+  uint32_t pair = kLowest, most[kVecs];  // largest values, of even and odd places
+#pragma unroll
+  for (int i = 0; i < kVecs; ++i) {
+    most[i] = max2(max2(x[i].x, x[i].y), max2(x[i].z, x[i].w));
+    pair = max2(pair, most[i]);
+  }
+  auto top_of = [](uint32_t p) { return max(ordered(p & 0xFFFFu), ordered(p >> 16)); };
+  const uint32_t mine = top_of(pair);
+  r.bad = r.bad || mine >= kKeyInf;  // +inf or a NaN (max.NaN's is positive)
+  // ---- the sum of exponentials, by a tree in the tile: errors of few roundings
+  const float top = fmaxf(r.m, fmaxf(bf16_lo(pair), bf16_hi(pair)));
+  if (top > -INFINITY) {
+    float part[kVecs];
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) {
+      const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+      float p[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) p[e] = pow2((bf16_lo(w[e]) - top) * kLog2e) + pow2((bf16_hi(w[e]) - top) * kLog2e);
+      part[i] = (p[0] + p[1]) + (p[2] + p[3]);
+    }
+#pragma unroll
+    for (int h = kVecs / 2; h >= 1; h >>= 1)
+#pragma unroll
+      for (int i = 0; i < h; ++i) part[i] += part[i + h];
+    r.s = (r.m > -INFINITY ? r.s * pow2((r.m - top) * kLog2e) : 0.0f) + part[0];
+    r.m = top;
+  }
+  if (t0 == 0) {
+    // ---- 64 groups of threads: the n-th largest of their maxima is a bound
+    constexpr int kSize = kThreads / kMaxN;
+    uint32_t g = mine;
+#pragma unroll
+    for (int off = kSize / 2; off >= 1; off >>= 1) g = max(g, __shfl_xor_sync(0xFFFFFFFFu, g, off));
+    if (lane % kSize == 0) sh.group[tid / kSize] = g << 6 | (kMaxN - 1 - tid / kSize);  // (no two alike)
+    __syncthreads();
+    const uint32_t v0 = sh.group[lane], v1 = sh.group[lane + 32];
+    int before0 = 0, before1 = 0;
+#pragma unroll 4
+    for (int j = 0; j < kMaxN; ++j) {
+      const uint32_t v = sh.group[j];
+      before0 += v > v0;
+      before1 += v > v1;
+    }
+    static_assert(kMaxN == 64, "two groups a lane, six bits");
+    const uint32_t bound = before0 == n - 1 ? v0 >> 6 : before1 == n - 1 ? v1 >> 6 : 0;
+    r.bound = max(__reduce_max_sync(0xFFFFFFFFu, bound), kKeyLowest + 1);
+  }
+  if (__any_sync(0xFFFFFFFFu, mine >= r.bound)) {
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) {
+      const uint32_t who = __ballot_sync(0xFFFFFFFFu, top_of(most[i]) >= r.bound);
+      if (who && !collect_vectors(sh, x[i], who, c.first_token + 8 * (t0 + i * kThreads + (tid & ~31)), r.bound)) r.crowded = true;
+    }
+  }
+  load_tile(c, t0 + 2 * kTileVecs, x);
+}
+
+// After the kCheck tiles from t0 on (or those that were left): the list keeps its n best where it is filling up.  With every tile followed by
+// a barrier the warps waited for those that collect.
+__device__ __forceinline__ void check_list(BeamShared& sh, const Chunk& c, int n, int t0, Running& r) {
+  if (__syncthreads_or(r.crowded)) {
+    int count = sh.n_list;
+    __syncthreads();
+    if (count > kList) count = exact_tiles(sh, c, t0, n);
+    cut_down(sh, count, n);
+    r.bound = max(r.bound, static_cast<uint32_t>(sh.top[n - 1] >> 32));
+    r.crowded = false;
   }
 }
 
@@ -196,191 +410,63 @@ __global__ void __launch_bounds__(kThreads, 2) beam_kernel(const BeamArgs a) {
   BeamShared& sh = *reinterpret_cast<BeamShared*>(smem_raw);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int row = blockIdx.x / a.chunks, chunk = blockIdx.x - row * a.chunks, b = row / a.K;
-  // the chunk's logits, and the aligned 16-byte vectors that hold them
   const long long row0 = static_cast<long long>(row) * a.V;
   const long long e0 = row0 + static_cast<long long>(chunk) * a.chunk_len, e1 = min(e0 + a.chunk_len, row0 + a.V);
-  // (from here on all places count from the first of these vectors; a row has at most 2^24 logits)
-  const uint16_t* const from = a.logits + (e0 & ~7ll);
-  const int lo = static_cast<int>(e0 & 7), hi = lo + static_cast<int>(e1 - e0), vecs = (hi + 7) >> 3;
-  const int there = static_cast<int>(min(a.total - (e0 & ~7ll), 1ll << 26));   // logits of the whole tensor
-  const uint32_t first_token = static_cast<uint32_t>((e0 & ~7ll) - row0);      // (wraps below a row's first)
+  Chunk c{a.logits + (e0 & ~7ll), static_cast<int>(e0 & 7)};
+  c.hi = c.lo + static_cast<int>(e1 - e0);
+  c.vecs = (c.hi + 7) >> 3;
+  c.first_token = static_cast<uint32_t>((e0 & ~7ll) - row0);
+  if (tid == 0) sh.n_list = 0;
+  __syncthreads();
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   // a beam that has ended, or that has no score, offers nothing of its logits: they are not read
-  const bool idle = (a.done && a.done[row] != 0) || a.scores[row] == -INFINITY;
-  bool bad = false;                        // a NaN or +inf among the logits
-  float all_m = -INFINITY, all_s = 0.0f;   // (thread 0)
-  int have = 0;                            // of the best so far, in top
-  for (int t0 = idle ? vecs : 0; t0 < vecs; t0 += kTileVecs) {
-    uint4 x[kVecs];
-#pragma unroll
-    for (int i = 0; i < kVecs; ++i) {
-      const int v = t0 + i * kThreads + tid;
-      x[i] = make_uint4(kLowest, kLowest, kLowest, kLowest);
-      if (v < vecs) {
-        if (8 * v + 8 <= there) {
-          x[i] = ld_stream_v4(from + 8 * v);
-        } else {  // the tensor's last logits
-          uint32_t* w = reinterpret_cast<uint32_t*>(&x[i]);
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            if (8 * v + e < there)
-              w[e >> 1] = e & 1 ? (w[e >> 1] & 0xFFFFu) | static_cast<uint32_t>(from[8 * v + e]) << 16
-                                : (w[e >> 1] & 0xFFFF0000u) | from[8 * v + e];
-        }
-      }
+  if ((a.done && a.done[row] != 0) || a.scores[row] == -INFINITY) c.vecs = 0;
+
+  Running r{-INFINITY, 0.0f, 0, false, false};
+  if (c.vecs > 0) {  // two tiles under way
+    uint4 x[kVecs], y[kVecs];
+    load_tile(c, 0, x);
+    load_tile(c, kTileVecs, y);
+    static_assert(kCheck % 2 == 0, "tiles go in pairs");
+#pragma unroll 1
+    for (int t0 = 0; t0 < c.vecs; t0 += 2 * kTileVecs) {
+      take_tile(sh, c, a.n, t0, x, r);
+      take_tile(sh, c, a.n, t0 + kTileVecs, y, r);  // (-inf behind the end)
+      if (t0 / kTileVecs % kCheck == kCheck - 2 || t0 + 2 * kTileVecs >= c.vecs)
+        check_list(sh, c, a.n, t0 / (kCheck * kTileVecs) * (kCheck * kTileVecs), r);
     }
-    // what belongs to other rows or chunks
-#pragma unroll
-    for (int i = 0; i < kVecs; ++i) {
-      const int v = t0 + i * kThreads + tid;
-      if (v < vecs && (8 * v < lo || 8 * v + 8 > hi)) {
-        uint32_t* w = reinterpret_cast<uint32_t*>(&x[i]);
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (8 * v + e < lo || 8 * v + e >= hi)
-            w[e >> 1] = e & 1 ? (w[e >> 1] & 0xFFFFu) | (kLowest & 0xFFFF0000u) : (w[e >> 1] & 0xFFFF0000u) | (kLowest & 0xFFFFu);
-      }
-    }
-    uint32_t pair = kLowest;
-#pragma unroll
-    for (int i = 0; i < kVecs; ++i) pair = max2(pair, max2(max2(x[i].x, x[i].y), max2(x[i].z, x[i].w)));
-    const uint32_t mine = max(ordered(pair & 0xFFFFu), ordered(pair >> 16));
-    const float m = fmaxf(bf16_lo(pair), bf16_hi(pair));
-    const bool odd = mine >= kKeyInf;      // +inf or a NaN (max.NaN's is positive)
-    // ---- the sum of exponentials, by a tree: errors of few roundings
-    float part[kVecs];
-#pragma unroll
-    for (int i = 0; i < kVecs; ++i) {
-      const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-      float p[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) p[e] = pow2((bf16_lo(w[e]) - m) * kLog2e) + pow2((bf16_hi(w[e]) - m) * kLog2e);
-      part[i] = (p[0] + p[1]) + (p[2] + p[3]);
-    }
-#pragma unroll
-    for (int h = kVecs / 2; h >= 1; h >>= 1)
-#pragma unroll
-      for (int i = 0; i < h; ++i) part[i] += part[i + h];
-    float s = part[0], top = m;
-    if (!(m > -INFINITY)) s = 0.0f;        // (nothing, or a NaN, which `odd` says)
-    {
-      float wm = m > -INFINITY ? m : -INFINITY;
-#pragma unroll
-      for (int off = 16; off >= 1; off >>= 1) wm = fmaxf(wm, __shfl_xor_sync(0xFFFFFFFFu, wm, off));
-      s = m > -INFINITY ? s * pow2((m - wm) * kLog2e) : 0.0f;
-#pragma unroll
-      for (int off = 16; off >= 1; off >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, off);
-      top = wm;
-    }
-    // ---- groups of threads, at least n of them: the n-th largest of their maxima bounds the n-th largest logit from below
-    const int size = a.n <= 16 ? 32 : a.n <= 32 ? 16 : 8, groups = kThreads / size;
-    uint32_t g = mine;
-    for (int off = size / 2; off >= 1; off >>= 1) g = max(g, __shfl_xor_sync(0xFFFFFFFFu, g, off));
-    if (lane % size == 0) sh.group[tid / size] = g;
-    if (lane == 0) sh.warp_stat[warp] = make_float2(top, s);
-    if (tid == 0) sh.n_list = have;
-    if (tid < have) sh.list[tid] = sh.top[tid];
-    bad = __syncthreads_or(odd);
-    if (bad) break;
-    if (warp == 0) {
-      const float2 w = lane < kWarps ? sh.warp_stat[lane] : make_float2(-INFINITY, 0.0f);
-      float wm = w.x;
-#pragma unroll
-      for (int off = 16; off >= 1; off >>= 1) wm = fmaxf(wm, __shfl_xor_sync(0xFFFFFFFFu, wm, off));
-      const float both = fmaxf(wm, all_m);
-      float ws = w.x > -INFINITY ? w.y * pow2((w.x - both) * kLog2e) : 0.0f;
-#pragma unroll
-      for (int off = 16; off >= 1; off >>= 1) ws += __shfl_xor_sync(0xFFFFFFFFu, ws, off);
-      all_s = (all_m > -INFINITY ? all_s * pow2((all_m - both) * kLog2e) : 0.0f) + ws;
-      all_m = both;
-    }
-    uint32_t bound = 0;
-    for (int i = lane; i < groups; i += 32) {
-      const uint32_t v = sh.group[i];
-      int before = 0;
-      for (int j = 0; j < groups; ++j) before += sh.group[j] > v || (sh.group[j] == v && j < i);
-      if (before == a.n - 1) bound = v;
-    }
-    bound = __reduce_max_sync(0xFFFFFFFFu, bound);
-    if (have == a.n) bound = max(bound, static_cast<uint32_t>(sh.top[a.n - 1] >> 32));
-    bound = max(bound, kKeyLowest + 1);
-    auto token = [&](int i, int e) { return first_token + 8 * (t0 + i * kThreads + tid) + e; };
-    auto key_of = [&](int i, int e) {
-      const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-      return ordered(e & 1 ? w[e >> 1] >> 16 : w[e >> 1] & 0xFFFFu);
-    };
-    auto push = [&](uint32_t key, uint32_t t) {
-      const int at = atomicAdd(&sh.n_list, 1);
-      if (at < kList) sh.list[at] = static_cast<unsigned long long>(key) << 32 | (0xFFFFFFFFu - t);
-    };
-    if (mine >= bound) {
-#pragma unroll
-      for (int i = 0; i < kVecs; ++i)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const uint32_t key = key_of(i, e);
-          if (key >= bound) push(key, token(i, e));
-        }
-    }
-    __syncthreads();
-    int n = sh.n_list;
-    if (n > kList) {
-      // ---- too many equal (or so) logits: the exact n-th largest (logit, lowest token) of the tile, bit by bit
-      uint32_t exact = 0;
-      for (int bit = 31; bit >= 0; --bit) {
-        const uint32_t cand = exact | 1u << bit;
-        int c = 0;
-        if (mine >= cand >> 16) {
-#pragma unroll
-          for (int i = 0; i < kVecs; ++i)
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-              c += (key_of(i, e) << 16 | (0xFFFFu - static_cast<uint32_t>((i * kThreads + tid) * 8 + e))) >= cand;
-        }
-        c = __reduce_add_sync(0xFFFFFFFFu, c);
-        if (tid < 2) sh.counts[tid] = 0;
-        __syncthreads();
-        if (lane == 0 && c) atomicAdd(&sh.counts[0], c);
-        __syncthreads();
-        if (sh.counts[0] >= static_cast<unsigned int>(a.n)) exact = cand;
-        __syncthreads();
-      }
-      if (tid == 0) sh.n_list = have;
-      __syncthreads();
-      if (mine >= exact >> 16) {
-#pragma unroll
-        for (int i = 0; i < kVecs; ++i)
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const uint32_t key = key_of(i, e);
-            if (key > kKeyLowest && (key << 16 | (0xFFFFu - static_cast<uint32_t>((i * kThreads + tid) * 8 + e))) >= exact)
-              push(key, token(i, e));
-          }
-      }
-      __syncthreads();
-      n = sh.n_list;
-    }
-    // ---- in order: a key's place is the number of larger ones
-    for (int i = tid; i < n; i += kThreads) {
-      const unsigned long long key = sh.list[i];
-      int place = 0;
-      for (int j = 0; j < n; ++j) place += sh.list[j] > key;
-      if (place < a.n) sh.top[place] = key;
-    }
-    have = min(n, a.n);
-    __syncthreads();
   }
+  // ---- the CTA's maximum and sum
+  {
+    float top = r.m;
+#pragma unroll
+    for (int off = 16; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, off));
+    float s = r.m > -INFINITY ? r.s * pow2((r.m - top) * kLog2e) : 0.0f;
+#pragma unroll
+    for (int off = 16; off >= 1; off >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, off);
+    if (lane == 0) sh.warp_stat[warp] = make_float2(top, s);
+  }
+  const bool bad = __syncthreads_or(r.bad);
+  cut_down(sh, sh.n_list, a.n);
   const long long list = static_cast<long long>(row) * a.chunks + chunk;
-  if (tid < a.n) a.offers[list * a.n + tid] = tid < have && !bad ? sh.top[tid] : 0ull;
-  if (tid == 0) a.stats[list] = bad ? make_float2(NAN, 0.0f) : make_float2(all_m, all_s);
-  __syncthreads();
+  if (tid < a.n) a.offers[list * a.n + tid] = bad ? 0ull : sh.top[tid];
+  if (warp == 0) {
+    const float2 w = lane < kWarps ? sh.warp_stat[lane] : make_float2(-INFINITY, 0.0f);
+    float top = w.x;
+#pragma unroll
+    for (int off = 16; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, off));
+    float sum = w.x > -INFINITY ? w.y * pow2((w.x - top) * kLog2e) : 0.0f;
+#pragma unroll
+    for (int off = 16; off >= 1; off >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, off);
+    if (lane == 0) a.stats[list] = bad ? make_float2(NAN, 0.0f) : make_float2(top, sum);
+  }
+  __syncthreads();  // (the release below covers what the barrier made this thread see)
   if (tid == 0) {
-    __threadfence();
-    const bool last = atomicAdd(a.tickets + b, 1u) == static_cast<unsigned int>(a.K * a.chunks - 1);
-    if (last) a.tickets[b] = 0;
-    __threadfence();
-    sh.last = last;
+    unsigned int old;
+    asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(old) : "l"(a.tickets + b) : "memory");
+    sh.last = old == static_cast<unsigned int>(a.K * a.chunks - 1);
+    if (sh.last) a.tickets[b] = 0;
   }
   __syncthreads();
   if (sh.last) merge(a, sh, b);
@@ -391,16 +477,16 @@ struct BeamPlan {
   size_t stats, offers, total;
 };
 
-// Chunks of a row: as many as keep two CTAs on every SM busy, of 4096 logits at least, and no larger than a tile; at most a
-// list a thread in the merge (a larger vocabulary takes a chunk in several tiles).
+// Chunks of a row: as many as are resident at once, of 4096 logits at least; at most a list a thread in the merge.  (More of them cost
+// the merge and their own beginnings and ends: [16, 4, 128256] 20 us with four to a row, 29 with nine, 47 with nineteen.)
 bool beam_plan(int64_t B, int64_t K, int64_t V, int64_t n, BeamPlan& p) {
   if (B < 1 || K < 1 || K > kMaxBeams || V < 2 || V > QSPEC_MAX_V || n < 1 || n > kMaxN || n > K * V || B > 65535 ||
       B * K * V >= (int64_t(1) << 40))
     return false;
-  int64_t c = 2 * num_sms() / (B * K);
-  const int64_t most = (V + 4095) / 4096, least = (V + kTile - 9) / (kTile - 8);
+  int64_t c = kCtasPerSm * num_sms() / (B * K);
+  const int64_t most = (V + 4095) / 4096;
   if (c > most) c = most;
-  if (c < least) c = least;
+  if (c < 1) c = 1;
   if (c > kMaxLists / K) c = kMaxLists / K;
   p.chunk_len = static_cast<int>((V + c - 1) / c);
   p.chunks = static_cast<int>((V + p.chunk_len - 1) / p.chunk_len);

@@ -49,7 +49,9 @@ qspec_status launch(AttArgs& a, int64_t rows, cudaStream_t s) {
   // Up to 64 rows a key head the decode kernel reads a sequence's keys twice at most and wins everywhere (16
   // sequences of 4096, 64 rows: 71 against 77 us; one of 32768: 51 against 94); with 96 rows and more it reads them three
   // times and computes on the legacy tensor path (128 rows: 119 against 78 us).
-  if (rows > 64) {
+  // With shared prefixes the prefill kernel takes key tiles in turn with its two query tiles, and wins from 33 rows on (16 groups
+  // over 6001 + 300 positions, 32 rows: 109 us here, 104 there; 64 rows: 182 against 140; one group over 32768, 32 rows: 46 against 49).
+  if (rows > (kShared ? 32 : 64)) {
     if (a.c.page >= 64) return d128 ? launch_prefill<128, true, kShared>(a, rows, s) : launch_prefill<64, true, kShared>(a, rows, s);
     return d128 ? launch_prefill<128, false, kShared>(a, rows, s) : launch_prefill<64, false, kShared>(a, rows, s);
   }

@@ -769,7 +769,8 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1) prefill_kernel(con
           for (int side = 0; side < 2; ++side, ++i) {
             const int st = i % kNR, sc = i % kNC;
             ok = ok && wait_bar(rawfull + st, (i / kNR) & 1, abort_flag, a.err);
-            if (i >= kNC) ok = ok && wait_bar(convempty + sc, ((i / kNC) - 1) & 1, abort_flag, a.err);
+            // (kShared: the place is waited for once the codes are in registers)
+            if (!kShared && i >= kNC) ok = ok && wait_bar(convempty + sc, ((i / kNC) - 1) & 1, abort_flag, a.err);
             ok = __all_sync(0xFFFFFFFFu, ok);
             if (!ok) break;
             const uint8_t* src = raw + st * C::kRaw;
@@ -795,6 +796,13 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1) prefill_kernel(con
                 }
               }
             }
+            if (kShared) {
+              __syncwarp();
+              if (lane == 0) mbar_arrive(rawempty + st);
+              if (i >= kNC) ok = wait_bar(convempty + sc, ((i / kNC) - 1) & 1, abort_flag, a.err);
+              ok = __all_sync(0xFFFFFFFFu, ok);
+              if (!ok) break;
+            }
 #pragma unroll
             for (int n = 0; n < kMine; ++n) {
               const int step = cw + n * kConvs, key = step * 8 + 2 * (lane >> 3) + sub;
@@ -804,17 +812,25 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1) prefill_kernel(con
                   const int half = C::kHalves == 2 ? (h ^ sub) : 0;
                   const uint4 v = w[n][h];
                   uint8_t* row = dst + half * kSub + key * 128;
-                  *reinterpret_cast<uint4*>(row + (((2 * quad) ^ (key & 7)) << 4)) =
-                      make_uint4(e4m3x2_to_f16x2(v.x), e4m3x2_to_f16x2(v.x >> 16), e4m3x2_to_f16x2(v.y), e4m3x2_to_f16x2(v.y >> 16));
-                  *reinterpret_cast<uint4*>(row + (((2 * quad + 1) ^ (key & 7)) << 4)) =
-                      make_uint4(e4m3x2_to_f16x2(v.z), e4m3x2_to_f16x2(v.z >> 16), e4m3x2_to_f16x2(v.w), e4m3x2_to_f16x2(v.w >> 16));
+                  uint4 x, y;
+                  if (kShared) {
+                    e4m3x4_to_f16x4(v.x, x.x, x.y);
+                    e4m3x4_to_f16x4(v.y, x.z, x.w);
+                    e4m3x4_to_f16x4(v.z, y.x, y.y);
+                    e4m3x4_to_f16x4(v.w, y.z, y.w);
+                  } else {
+                    x = make_uint4(e4m3x2_to_f16x2(v.x), e4m3x2_to_f16x2(v.x >> 16), e4m3x2_to_f16x2(v.y), e4m3x2_to_f16x2(v.y >> 16));
+                    y = make_uint4(e4m3x2_to_f16x2(v.z), e4m3x2_to_f16x2(v.z >> 16), e4m3x2_to_f16x2(v.w), e4m3x2_to_f16x2(v.w >> 16));
+                  }
+                  *reinterpret_cast<uint4*>(row + (((2 * quad) ^ (key & 7)) << 4)) = x;
+                  *reinterpret_cast<uint4*>(row + (((2 * quad + 1) ^ (key & 7)) << 4)) = y;
                 }
               }
             }
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
-              mbar_arrive(rawempty + st);
+              if (!kShared) mbar_arrive(rawempty + st);
               mbar_arrive(convfull + sc);
             }
           }
