@@ -91,7 +91,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, RG>::kThreads, DecodeCfg<D, RG>::
   {
     W w;
     if constexpr (kShared)
-      share_out<C::kThreads>(a, seq, scan, w, reinterpret_cast<long long*>(ring));
+      share_out<C::kThreads>(a, seq, scan, w, reinterpret_cast<Count*>(ring));
     else
       share_out<C::kThreads>(a, seq, scan, w);
     run0 = w.u;
@@ -105,9 +105,8 @@ __global__ void __launch_bounds__(DecodeCfg<D, RG>::kThreads, DecodeCfg<D, RG>::
   while (true) {
     if constexpr (kShared) {
       if (warp == 0) {
-        const bool more = walk_next(walk);
+        const bool more = walk_next_planned(walk, plan, seg);
         if (lane == 0) flags[0] = more;
-        if (more) make_plan<kKeys>(walk, plan, seg);
       }
     } else {
       if (threadIdx.x == 0) flags[0] = walk->next();

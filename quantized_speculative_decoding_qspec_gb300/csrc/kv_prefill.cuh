@@ -197,7 +197,7 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1) prefill_kernel(con
   {
     W w;
     if constexpr (kShared)
-      share_out<C::kThreads>(a, seq, scan, w, reinterpret_cast<long long*>(qs));
+      share_out<C::kThreads>(a, seq, scan, w, reinterpret_cast<Count*>(qs));
     else
       share_out<C::kThreads>(a, seq, scan, w);  // (barriers inside)
     run0 = w.u;

@@ -176,15 +176,39 @@ struct WalkOf<true, kRows, kKeys> {
   using type = SharedWalk<kRows, kKeys>;
 };
 
-// Units of (group, row tile) pairs, worked out by several lanes each where the pairs are few, in shared memory.
+// Units of (group, row tile) pairs, counted ahead in shared memory where the pairs are few: by a thread to a sequence, which adds its own
+// tiles to the row tiles that it has tokens in.  (By a thread to a pair, one that goes through 64 sequences takes 5 us, and the
+// walk begins with three such counts.)
 constexpr int kCounted = 512;
+struct Count {
+  int own, lo;  // tiles of the sequences' own keys; the first position of the prefix that a row sees
+};
 template <class W>
 struct Counted {
   const W& w;
-  const long long* sum;  // null: not counted ahead
+  const Count* count;  // null: not counted ahead
   int max_tiles;
-  __device__ long long units(int g, int t) const { return sum ? sum[g * max_tiles + t] : w.units(g, t); }
+  __device__ long long units(int g, int t) const {
+    if (!count) return w.units(g, t);
+    int n;
+    if (t >= w.tiles(g, n)) return 0;
+    const Count c = count[g * max_tiles + t];
+    return static_cast<long long>(w.all_tiles(g, c.own, c.lo)) * w.heads;
+  }
 };
+
+// The group of sequence b: the last one that begins at or before it.
+__device__ __forceinline__ int group_of(const int2* grp, int groups, int b) {
+  int lo = 0, hi = groups;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (grp[mid].x <= b)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  return lo;
+}
 
 // Fills grp (all threads), shares the units out and positions the walk for this CTA.  Ends with a barrier.
 // A prefix ends where the new tokens of one of its sequences begin, at the latest.  A group with a sequence whose numbers are
@@ -192,7 +216,7 @@ struct Counted {
 // not in use yet.
 template <int kThreads, int kRows, int kKeys>
 __device__ __forceinline__ void share_out(const AttArgs& a, int2* grp, ScanShared* sh, SharedWalk<kRows, kKeys>& w,
-                                          long long* scratch) {
+                                          Count* scratch) {
   const int G = a.groups, B = a.b.B;
   bool bad = false;
   for (int g = threadIdx.x; g <= G; g += kThreads) {
@@ -212,14 +236,7 @@ __device__ __forceinline__ void share_out(const AttArgs& a, int2* grp, ScanShare
     if (blockIdx.x == 0 && threadIdx.x == 0) atomicOr(a.err, kErrInvalid);
   } else {
     for (int b = grp[0].x + threadIdx.x; b < grp[G].x; b += kThreads) {
-      int lo = 0, hi = G;
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (grp[mid].x <= b)
-          lo = mid;
-        else
-          hi = mid;
-      }
+      const int lo = group_of(grp, G, b);
       const SeqSpan s = seq_span(a.b, a.c.page, b);
       if (!s.ok && blockIdx.x == 0) atomicOr(a.err, kErrInvalid);
       if (!s.ok)
@@ -249,21 +266,22 @@ __device__ __forceinline__ void share_out(const AttArgs& a, int2* grp, ScanShare
   const uint32_t pairs = static_cast<uint32_t>(G) * a.max_tiles;
   const bool counted = pairs <= kCounted;
   if (counted) {
-    // (One thread that goes through 64 sequences takes 5 us, and the walk begins with three such counts: a group of 128 single tokens over
-    // 65536 positions spent 19 us here.)
-    int lanes = 32;
-    while (lanes > 1 && pairs * lanes > 2 * kThreads) lanes /= 2;
-    const int lane = threadIdx.x % lanes;
-    for (uint32_t e = threadIdx.x / lanes; e < (pairs + 31) / 32 * 32; e += kThreads / lanes) {  // (whole warps)
-      int n = 0, own = 0, lo = 0x7FFFFFFF;
-      const int g = e < pairs ? e / static_cast<uint32_t>(a.max_tiles) : 0, t = e - g * a.max_tiles;
-      const bool real = e < pairs && t < w.tiles(g, n);
-      if (real) own = w.own_tiles(g, t, n, lane, lanes, lo);
-      for (int off = lanes / 2; off >= 1; off >>= 1) {
-        own += __shfl_xor_sync(0xFFFFFFFFu, own, off);
-        lo = min(lo, __shfl_xor_sync(0xFFFFFFFFu, lo, off));
+    for (uint32_t e = threadIdx.x; e < pairs; e += kThreads) scratch[e] = Count{0, a.window > 0 ? 0x7FFFFFFF : 0};
+    __syncthreads();
+    for (int b = grp[0].x + threadIdx.x; b < grp[G].x; b += kThreads) {
+      const int g = group_of(grp, G, b), p = grp[g].y;
+      if (p < 0) continue;
+      const int c0 = w.cu[b], c1 = w.cu[b + 1], tok0 = w.cu[grp[g].x];
+      if (c1 == c0) continue;
+      const int row0 = (c0 - tok0) * a.group, row1 = (c1 - tok0) * a.group, all = (w.cu[grp[g + 1].x] - tok0) * a.group;
+      for (int t = row0 / kRows; t * kRows < row1; ++t) {
+        const int t0 = tok0 + w.token_of(t * kRows), t1 = tok0 + w.token_of(min((t + 1) * kRows, all) - 1);
+        Count* const at = scratch + g * a.max_tiles + t;
+        int lo, hi;
+        w.own_range(b, t0, t1, p, lo, hi);
+        atomicAdd(&at->own, tiles_between<kKeys>(lo, hi));
+        if (a.window > 0) atomicMin(&at->lo, min(window_start(w.kv[b] - c1 + max(t0, c0), a.window), p));
       }
-      if (e < pairs && lane == 0) scratch[e] = real ? static_cast<long long>(w.all_tiles(g, own, lo)) * w.heads : 0;
     }
     __syncthreads();
   }
@@ -284,9 +302,9 @@ struct Plan {
   int one_lo, one_hi;    // where all rows are of one sequence: what they all see of its own
 };
 
-// One warp makes the plan of the walk's item.
+// One warp makes the plan of the walk's item.  Returns its tiles.
 template <int kKeys, class W>
-__device__ __forceinline__ void make_plan(const W* w, Plan* plan, int4* seg) {
+__device__ __forceinline__ int make_plan(const W* w, Plan* plan, int4* seg) {
   // the rows of the second query tile begin here, counted in the group's rows
   const long long half = static_cast<long long>(w->it.row0) + (W::kRowsOf > 128 && w->it.rows > W::kRowsOf / 2 ? W::kRowsOf / 2 : W::kRowsOf);
   const Item& it = w->it;
@@ -337,6 +355,30 @@ __device__ __forceinline__ void make_plan(const W* w, Plan* plan, int4* seg) {
   if (lane == 0)
     *plan = Plan{count, prefix, first_half, in_both, end - prefix - first_half - in_both, s0, s1, pre_lo, one_lo, one_hi};
   __syncwarp();
+  return max(end, 1);
+}
+
+// As walk_next, by the warp that makes the plans: the count comes with the plan, which serves all heads of a row tile.
+template <int kRows, int kKeys>
+__device__ __forceinline__ bool walk_next_planned(SharedWalk<kRows, kKeys>* w, Plan* plan, int4* seg) {
+  const int lane = threadIdx.x & 31;
+  while (true) {
+    __syncwarp();
+    int s = 0;
+    if (lane == 0) s = w->step();
+    s = __shfl_sync(0xFFFFFFFFu, s, 0);
+    __syncwarp();
+    if (s != 0) return s > 0;
+    int lo = 0;
+    if (w->window > 0) {
+      w->own_tiles(w->it.b, w->it.tile, w->it.n, lane, 32, lo);
+      lo = __reduce_min_sync(0xFFFFFFFFu, lo);
+    }
+    if (lane == 0) w->it.lo = lo;
+    __syncwarp();
+    const int tiles = make_plan<kKeys>(w, plan, seg);
+    if (lane == 0) w->nk = tiles;
+  }
 }
 
 // The v-th tile that is taken, counted in the order of the segments.
