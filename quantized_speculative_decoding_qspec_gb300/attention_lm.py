@@ -16,7 +16,11 @@ quite the one that decoding token by token would have left: drafted and rejected
 the codes of accepted ones below e4m3's normal range were rounded again.  Where two logits are as near as that, the text can
 differ from plain W4A16 decoding.
 
-``python -m quantized_speculative_decoding_qspec_gb300.attention_lm`` runs it on one GPU.
+``Beams`` continues each prompt in several beams instead: their sequences share the prompt's pages and, where they go on from
+the same beam, its pages too; attention reads a prompt's keys once for all its beams, and a step ends with the choice of
+the next beams and their page tables, without a look at anything on the host.
+
+``python -m quantized_speculative_decoding_qspec_gb300.attention_lm`` runs both on one GPU.
 """
 from __future__ import annotations
 
@@ -56,8 +60,9 @@ class AttentionLM:
         (q.qspec_linear_w4a4 if draft_mode else q.qspec_linear_w4a16)(x, Wp, S, y, ws)
         return y
 
-    def forward(self, tok, batch, draft_mode, tree=None, pos=None):
-        """Logits [T, V] of the new tokens tok int32 [T] (sequence after sequence), whose keys join the cache."""
+    def forward(self, tok, batch, draft_mode, tree=None, pos=None, prefixes=None):
+        """Logits [T, V] of the new tokens tok int32 [T] (sequence after sequence), whose keys join the cache.  prefixes: what
+        the sequences share, or None."""
         T, hq, hk, d = tok.numel(), self.heads_q, self.heads, self.dim
         x = torch.empty(T, self.width, dtype=torch.bfloat16, device=self.device)
         q.qspec_gather_rows(self.E, tok, x)
@@ -66,7 +71,10 @@ class AttentionLM:
         qs, ks, vs = qkv[:, :hq], qkv[:, hq:hq + hk], qkv[:, hq + hk:]
         q.qspec_kv_append(self.cache, batch, ks, vs, rotary=self.rotary, q=qs, pos=pos)
         att = torch.empty(T, hq, d, dtype=torch.bfloat16, device=self.device)
-        q.qspec_kv_attention(self.cache, batch, qs, att, self.ws, tree=tree)
+        if prefixes is None:
+            q.qspec_kv_attention(self.cache, batch, qs, att, self.ws, tree=tree)
+        else:
+            q.qspec_kv_attention_shared(self.cache, batch, prefixes, qs, att, self.ws, tree=tree)
         return self._linear("out", x + self._linear("o", att.view(T, hq * d), draft_mode), draft_mode)
 
 
@@ -161,6 +169,108 @@ class Server:
         return self.out
 
 
+class Beams:
+    """Beam search: `beams` continuations of each prompt, by summed log probability.
+
+    end_tok ends a beam, which then stays among the best by its score alone; beams compare by their score divided by the length
+    of what they added to the power of `length_power`.  A prompt has 1 to max_len tokens; max_new tokens are added at most.
+    tokens [B, beams, max_new] and scores [B, beams] are best first.
+    """
+
+    def __init__(self, model, prompts, beams=4, max_len=256, max_new=64, end_tok=0, length_power=0.0):
+        if not prompts or beams < 1 or max_new < 1:
+            raise ValueError("at least one prompt, one beam and one new token")
+        for p in prompts:
+            if not 1 <= len(p) <= max_len:
+                raise ValueError(f"a prompt has 1 to {max_len} tokens, got {len(p)}")
+        if not 0 <= end_tok < model.V:
+            raise ValueError("end_tok must be a token")
+        page, dev = model.cache.page, model.device
+        B, K = len(prompts), beams
+        # a prompt's pages once, and of each beam its own: those of its new tokens and the page that they begin in, twice while they move
+        need = sum(-(-len(p) // page) for p in prompts) + 2 * B * K * (-(-max_new // page) + 1)
+        if need > model.cache.k.shape[0]:
+            raise ValueError(f"the cache has too few pages: {model.cache.k.shape[0]} of {need}")
+        self.model, self.B, self.K, self.end_tok, self.max_new, self.power = model, B, K, end_tok, max_new, length_power
+        i32 = dict(dtype=torch.int32, device=dev)
+        width = -(-(max_len + max_new) // page)
+        self.tables = [torch.zeros(B * K, width, **i32) for _ in range(2)]
+        self.refs = torch.zeros(model.cache.k.shape[0], **i32)
+        self.copies = [torch.zeros(B * K, **i32) for _ in range(3)]
+        self.left = torch.zeros(1, **i32)
+        self.prompt_len = torch.tensor([len(p) for p in prompts], **i32)
+        self.length = self.prompt_len.repeat_interleave(K)             # cached positions of each beam
+        self.tokens = torch.full((B, K, max_new), -1, **i32)
+        self.parent, self.tok = torch.zeros(B, K, **i32), torch.zeros(B, K, **i32)
+        self.score, self.done, self.added = torch.zeros(B, K, device=dev), torch.zeros(B, K, **i32), torch.zeros(B, K, **i32)
+        self.bws = q.new_beam_workspace(B, K, model.V, K, device=dev)
+        self.cu = torch.arange(B * K + 1, **i32)
+        self.prefixes = q.KVPrefixes(torch.arange(0, B * K + 1, K, **i32), self.prompt_len, K)
+        self.steps = 0
+        self._prefill(prompts)
+
+    def _pages(self, rows, parent, keep, need):
+        """The next page tables from the first `rows` rows of the present ones, and the copies that they ask for."""
+        old, new = self.tables
+        src, dst, size = self.copies
+        q.qspec_kv_pages(old[:rows], self.length[:rows], keep, need, self.refs, self.model.cache.page, new[:keep.numel()], self.refs,
+                         src[:keep.numel()], dst[:keep.numel()], size[:keep.numel()], self.left, parent=parent)
+        q.qspec_kv_copy_pages(self.model.cache, src[:keep.numel()], dst[:keep.numel()], lengths=size[:keep.numel()])
+        self.tables.reverse()
+
+    def _prefill(self, prompts):
+        B, K, dev = self.B, self.K, self.model.device
+        ends = torch.tensor([len(p) for p in prompts]).cumsum(0)
+        cu = torch.cat([torch.zeros(1, dtype=torch.int64), ends]).to(torch.int32).to(dev)
+        none = torch.full((B,), -1, dtype=torch.int32, device=dev)
+        self._pages(0, none, torch.zeros_like(none), self.prompt_len)
+        tok = torch.tensor([t for p in prompts for t in p], dtype=torch.int32, device=dev)
+        batch = q.KVBatch(cu, self.prompt_len, self.tables[0][:B], max(len(p) for p in prompts))
+        logits = self.model.forward(tok, batch, draft_mode=False)
+        last = logits[(ends - 1).to(dev)].view(B, 1, -1).contiguous()
+        ws = q.new_beam_workspace(B, 1, self.model.V, K, device=dev)
+        q.qspec_beam_select(last, torch.zeros(B, 1, device=dev), self.parent, self.tok, self.score, ws)
+        lengths, self.length = self.length, self.prompt_len            # the old rows are the prompts
+        self._fork(B, lengths)
+
+    def _fork(self, rows, lengths):
+        """The chosen beams go on from their parents' pages (of the first `rows` rows), with room for one token more."""
+        parent, n = self.parent.view(-1), self.steps
+        keep = lengths.contiguous()
+        self._pages(rows, parent, keep, keep + 1)
+        self.length = keep + 1
+        if n > 0:                                                      # (parents are rows of the beams before)
+            moved = torch.empty_like(self.tokens.view(-1, self.max_new))
+            q.qspec_gather_rows(self.tokens.view(-1, self.max_new), parent, moved)
+            self.tokens = moved.view_as(self.tokens)
+            at = parent.long()
+            self.done, self.added = self.done.view(-1)[at].view_as(self.done), self.added.view(-1)[at].view_as(self.added)
+        self.tokens[:, :, n] = torch.where(self.done != 0, torch.full_like(self.tok, -1), self.tok)
+        self.added += (self.done == 0).to(torch.int32)
+        self.done |= (self.tok == self.end_tok).to(torch.int32)
+        self.steps += 1
+
+    def step(self):
+        """One token more for every beam that has not ended."""
+        if self.steps >= self.max_new:
+            raise ValueError(f"the beams have {self.max_new} tokens")
+        B, K, V = self.B, self.K, self.model.V
+        batch = q.KVBatch(self.cu, self.length, self.tables[0], 1)
+        logits = self.model.forward(self.tok.view(-1), batch, draft_mode=False, prefixes=self.prefixes).view(B, K, V)
+        # an ended beam's length stays as it is, the others' grows
+        weights = (self.added + (self.done == 0).to(torch.int32)).float() ** -self.power if self.power else None
+        parent, tok, score = torch.empty_like(self.parent), torch.empty_like(self.tok), torch.empty_like(self.score)
+        q.qspec_beam_select(logits, self.score, parent, tok, score, self.bws, done=self.done, end_tok=self.end_tok, weights=weights)
+        self.parent, self.tok, self.score = parent, tok, score
+        self._fork(B * K, self.length)
+
+    def close(self):
+        """Gives all pages back."""
+        none = self.length[:0]
+        q.qspec_kv_pages(self.tables[0], self.length, none, none, self.refs, self.model.cache.page, self.tables[1][:0], self.refs, none,
+                         none, none, self.left)
+
+
 def main():
     model = AttentionLM()
     prompts = [[1, 2, 3, 4, 5], list(range(100, 140)), [7]]
@@ -174,6 +284,12 @@ def main():
         n = int(server.hist_len[b])
         print(f"sequence {b}: {n - len(p)} tokens, cache length {int(server.kv_len[b])}: {server.hist[b, len(p):n].tolist()}")
     print(f"accepted drafts per iteration: {sum(accepted) / len(accepted):.2f} of {server.gamma}")
+    search = Beams(model, prompts, beams=4, max_len=128, max_new=12, length_power=0.6)
+    for _ in range(11):
+        search.step()
+    q.qspec_check_status()
+    for b in range(len(prompts)):
+        print(f"beams of prompt {b}: " + ", ".join(f"{float(search.score[b, k]):.2f} {search.tokens[b, k, :6].tolist()}" for k in range(4)))
 
 
 if __name__ == "__main__":
