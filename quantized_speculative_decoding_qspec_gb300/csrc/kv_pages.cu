@@ -329,7 +329,7 @@ struct CompactArgs {
   const int32_t* count;
   unsigned int* err;
   int64_t n_pages;
-  int heads, page, T, first;
+  int heads, page, T, first, layers, layers_per;
 };
 
 // The smallest e with amax <= 448 * 2^e = 1.75 * 2^(e + 8), limited to the stored range; amax >= 0 as fp32 bits.
@@ -360,18 +360,20 @@ __device__ __forceinline__ uint4 rescaled(uint4 c, int from, int to) {
   return c;
 }
 
-// A block owns one side of up to eight heads of one sequence in one layer, a warp one head.  The warp holds the whole path of its
-// head in registers before it writes (the places written are places read), a lane 16 codes of a token at a time; paths of a
-// few tokens are one item a lane, so a step is one round trip to memory after the indices.  What is written follows
-// the append: a page begun here takes the scale of what it receives, another one grows where it must.
+// A block owns one side of up to eight heads of one sequence, a warp one head, in some layers one after the other (the chain of
+// indices, half of a step's latency, is paid once for them: 64 paths in 32 layers: 51 us with a block to each layer, 43 with one to three).  A lane takes 16 codes
+// of a token, the warp 16 tokens (with heads of 64: 32) at a time: paths of up to that length are read once, longer ones once for
+// the scales and once to be moved.  A path's nodes rise, so a token's new place is never behind the places that are still to be read, in the
+// order of the tokens.  What is written follows the append: a page begun here takes the scale of what it receives, another one
+// grows where it must.
 template <int D>
-__global__ void __launch_bounds__(32 * kCompactWarps) compact_kernel(const __grid_constant__ CompactArgs a) {
-  constexpr int kPerTok = D / 16, kItems = QSPEC_MAX_TREE * kPerTok / 32;
+__global__ void __launch_bounds__(32 * kCompactWarps, 4) compact_kernel(const __grid_constant__ CompactArgs a) {
+  constexpr int kPerTok = D / 16, kItems = 4, kAtOnce = 32 * kItems / kPerTok, kPages = QSPEC_MAX_TREE / 16 + 1;
   __shared__ int node_of[QSPEC_MAX_TREE];
-  __shared__ int page_of[QSPEC_MAX_TREE / 16 + 2];  // pages of the tree's positions, from the path's first on
+  __shared__ int page_of[kPages + 1];  // pages of the tree's positions, from the path's first on
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int b = blockIdx.x, side = blockIdx.z & 1, layer = blockIdx.z >> 1, lane = threadIdx.x & 31;
+  const int b = blockIdx.x, side = blockIdx.z & 1, lane = threadIdx.x & 31;
   const int head = blockIdx.y * kCompactWarps + (threadIdx.x >> 5);
   const SeqSpan sp = seq_span(a.b, a.page, b);
   const int n = a.count[b];
@@ -381,14 +383,15 @@ __global__ void __launch_bounds__(32 * kCompactWarps) compact_kernel(const __gri
   bool ok = sp.ok && n >= 0 && n <= a.T && n <= max(tree, 0) && sp.n <= sp.kv;
   if (ok && n > 0) {
     if (threadIdx.x < n) {
-      const int j = a.nodes[static_cast<int64_t>(b) * a.T + threadIdx.x];
+      const int32_t* at = a.nodes + static_cast<int64_t>(b) * a.T + threadIdx.x;
+      const int j = at[0];
       node_of[threadIdx.x] = j;
-      ok = j >= 0 && j < tree;
+      ok = j >= 0 && j < tree && (threadIdx.x == 0 || j > at[-1]);
     }
     const int t = threadIdx.x - QSPEC_MAX_TREE;
     if (tree > QSPEC_MAX_TREE) {
       ok = false;
-    } else if (t >= 0 && t < QSPEC_MAX_TREE / 16 + 2) {
+    } else if (t >= 0 && t < kPages + 1) {
       int p = 0;
       if (pg0 + t <= (sp.kv - 1) / P) {
         p = a.b.pages[static_cast<int64_t>(b) * a.b.max_pages + pg0 + t];
@@ -403,59 +406,79 @@ __global__ void __launch_bounds__(32 * kCompactWarps) compact_kernel(const __gri
     return;
   }
   if (n == 0 || head >= a.heads) return;
-  uint8_t* const codes = a.l.codes[side][layer] + static_cast<int64_t>(head) * P * D;
-  int8_t* const exps = a.l.exps[side][layer] + head;
   const int64_t page_codes = static_cast<int64_t>(a.heads) * P * D;
-  auto exp_at = [&](int page) { return min(max(static_cast<int>(exps[static_cast<int64_t>(page) * a.heads]), kKvMinExp), kKvMaxExp); };
-
-  uint4 c[kItems];
-  int e_of[kItems];
-#pragma unroll
-  for (int k = 0; k < kItems; ++k) {
-    const int i = k * 32 + lane, t = i / kPerTok;
-    c[k] = make_uint4(0, 0, 0, 0);
-    e_of[k] = 0;
-    if (t < n) {
-      const int pos = base + node_of[t], page = page_of[pos / P - pg0];
-      c[k] = *reinterpret_cast<const uint4*>(codes + page * page_codes + (pos % P) * D + (i % kPerTok) * 16);
-      e_of[k] = exp_at(page);
-    }
-  }
   const int pages = (base + n - 1) / P - pg0 + 1;
-  int old[QSPEC_MAX_TREE / 16 + 1];  // before any is written: later pages' scales are read as sources above
+  const int layer0 = (blockIdx.z >> 1) * a.layers_per, layer1 = min(layer0 + a.layers_per, a.layers);
+#pragma unroll 1
+  for (int layer = layer0; layer < layer1; ++layer) {
+    uint8_t* const codes = a.l.codes[side][layer] + static_cast<int64_t>(head) * P * D;
+    int8_t* const exps = a.l.exps[side][layer] + head;
+    auto exp_at = [&](int q) {
+      return min(max(static_cast<int>(exps[static_cast<int64_t>(page_of[q]) * a.heads]), kKvMinExp), kKvMaxExp);
+    };
+    uint4 c[kItems];
+    int e_of[kItems];
+    auto load = [&](int t0) {  // tokens t0 ...: the codes of the lane's items and their scales
 #pragma unroll
-  for (int q = 0; q < QSPEC_MAX_TREE / 16 + 1; ++q) old[q] = q < pages ? exp_at(page_of[q]) : 0;
-  __syncwarp();
+      for (int k = 0; k < kItems; ++k) {
+        const int i = k * 32 + lane, t = t0 + i / kPerTok;
+        c[k] = make_uint4(0, 0, 0, 0);
+        e_of[k] = 0;
+        if (t < n) {
+          const int pos = base + node_of[t], q = pos / P - pg0;
+          c[k] = *reinterpret_cast<const uint4*>(codes + page_of[q] * page_codes + (pos % P) * D + (i % kPerTok) * 16);
+          e_of[k] = exp_at(q);
+        }
+      }
+    };
+    const int old = exp_at(0);  // (the first page alone can be one that goes on)
+    uint32_t amax[kPages] = {};
+#pragma unroll 1
+    for (int t0 = 0; t0 < n; t0 += kAtOnce) {
+      load(t0);
 #pragma unroll
-  for (int q = 0; q < QSPEC_MAX_TREE / 16 + 1; ++q) {
-    if (q >= pages) break;
-    const int p0 = (pg0 + q) * P, t0 = max(p0 - base, 0), t1 = min(p0 + P - base, n);  // the path's tokens in this page
-    const bool begun = p0 >= base;
-    uint32_t amax = 0;
+      for (int k = 0; k < kItems; ++k) {
+        const int t = t0 + (k * 32 + lane) / kPerTok, q = (base + t) / P - pg0;
+        const uint32_t v = __float_as_uint(__uint_as_float(amax_codes(c[k])) * exp2_int(e_of[k]));
 #pragma unroll
-    for (int k = 0; k < kItems; ++k) {
-      const int t = (k * 32 + lane) / kPerTok;
-      if (k * 32 / kPerTok < t1 && t >= t0 && t < t1)
-        amax = max(amax, __float_as_uint(__uint_as_float(amax_codes(c[k])) * exp2_int(e_of[k])));
-    }
-    amax = __reduce_max_sync(0xFFFFFFFFu, amax);
-    const int e = begun ? exp_of_f32(amax) : max(old[q], exp_of_f32(amax));
-    uint8_t* at = codes + page_of[q] * page_codes;
-    if (!begun && e > old[q]) {  // the page grows: its other slots again
-      for (int i = lane; i < P * kPerTok; i += 32) {
-        const int t = p0 + i / kPerTok - base;
-        if (t >= t0 && t < t1) continue;
-        uint4* w = reinterpret_cast<uint4*>(at) + i;
-        *w = rescaled(*w, old[q], e);
+        for (int p = 0; p < kPages; ++p)
+          if (t < n && q == p) amax[p] = max(amax[p], v);
       }
     }
+    int e_new[kPages];
 #pragma unroll
-    for (int k = 0; k < kItems; ++k) {
-      const int i = k * 32 + lane, t = i / kPerTok;
-      if (t >= t0 && t < t1)
-        *reinterpret_cast<uint4*>(at + (base + t - p0) * D + (i % kPerTok) * 16) = rescaled(c[k], e_of[k], e);
+    for (int p = 0; p < kPages; ++p) {
+      e_new[p] = exp_of_f32(__reduce_max_sync(0xFFFFFFFFu, amax[p]));
+      if ((pg0 + p) * P < base) e_new[p] = max(old, e_new[p]);
     }
-    if (lane == 0) exps[static_cast<int64_t>(page_of[q]) * a.heads] = static_cast<int8_t>(e);
+#pragma unroll 1
+    for (int t0 = 0; t0 < n; t0 += kAtOnce) {
+      if (n > kAtOnce) load(t0);
+      __syncwarp();  // (what these tokens' places hold has been read by all lanes)
+#pragma unroll
+      for (int k = 0; k < kItems; ++k) {
+        const int i = k * 32 + lane, t = t0 + i / kPerTok, pos = base + t, q = pos / P - pg0;
+        if (t < n) {
+          int e = e_new[0];
+#pragma unroll
+          for (int p = 1; p < kPages; ++p) e = q == p ? e_new[p] : e;
+          *reinterpret_cast<uint4*>(codes + page_of[q] * page_codes + (pos % P) * D + (i % kPerTok) * 16) = rescaled(c[k], e_of[k], e);
+        }
+      }
+      __syncwarp();
+    }
+    if (pg0 * P < base && e_new[0] > old) {  // the page grows: its other slots again
+      uint4* at = reinterpret_cast<uint4*>(codes + page_of[0] * page_codes);
+      for (int i = lane; i < P * kPerTok; i += 32) {
+        const int t = pg0 * P + i / kPerTok - base;
+        if (t < 0 || t >= n) at[i] = rescaled(at[i], old, e_new[0]);
+      }
+    }
+    if (lane == 0) {
+#pragma unroll
+      for (int p = 0; p < kPages; ++p)
+        if (p < pages) exps[static_cast<int64_t>(page_of[p]) * a.heads] = static_cast<int8_t>(e_new[p]);
+    }
   }
 }
 
@@ -575,7 +598,12 @@ extern "C" qspec_status qspec_kv_compact(const qspec_kv_cache* caches, int32_t n
   a.page = caches->page;
   a.T = T;
   a.first = first;
-  const dim3 grid(batch->B, (a.heads + kCompactWarps - 1) / kCompactWarps, 2 * n_caches);
+  // layers of a block: one, unless the blocks are more than twice what is resident
+  const int64_t all = static_cast<int64_t>(batch->B) * ((a.heads + kCompactWarps - 1) / kCompactWarps) * 2 * n_caches;
+  const int64_t per = all / (8 * num_sms());
+  a.layers = n_caches;
+  a.layers_per = per < 1 ? 1 : per > n_caches ? n_caches : static_cast<int>(per);
+  const dim3 grid(batch->B, (a.heads + kCompactWarps - 1) / kCompactWarps, 2 * ((n_caches + a.layers_per - 1) / a.layers_per));
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   return caches->dim == 128 ? launch_pdl(compact_kernel<128>, grid, dim3(32 * kCompactWarps), 0, s, a)
                             : launch_pdl(compact_kernel<64>, grid, dim3(32 * kCompactWarps), 0, s, a);

@@ -333,7 +333,7 @@ def test_compacting_layers_at_once():
 
 def test_bad_paths_leave_their_sequence_alone():
     q = lib()
-    for change in ("node", "negative", "count", "page", "length", "wide"):
+    for change in ("node", "negative", "order", "twice", "count", "page", "length", "wide"):
         tok, kv = [9, 9], [40, 40]
         if change == "wide":
             tok, kv = [66, 9], [70, 40]       # 65 nodes
@@ -343,6 +343,10 @@ def test_bad_paths_leave_their_sequence_alone():
             nodes[0][2] = 8
         elif change == "negative":
             nodes[0][0] = -1
+        elif change == "order":
+            nodes[0] = [3, 0, 7]
+        elif change == "twice":
+            nodes[0] = [0, 3, 3]
         elif change == "count":
             count[0] = 9
         elif change == "page":
