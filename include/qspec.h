@@ -609,9 +609,9 @@ qspec_status qspec_kv_attention(const qspec_kv_cache* cache, const qspec_kv_batc
  * offer nothing (the logits of such a beam and of a finished one are not read).
  *
  *   logits [B, beams, V] bf16 (16-byte aligned);  scores [B, beams] fp32;  done [B, beams] int32 or NULL: none;
- *   weights [B, beams] fp32 or NULL: 1;  parent, tok [B, n] int32, score [B, n] fp32 (outputs)
+ *   weights [B, beams] fp32 or NULL: 1;  parent, tok [B, n] int32, score [B, n] fp32 (outputs; not scores itself)
  *   ws, ws_bytes  device workspace, >= qspec_beam_workspace_size(B, beams, V, n), zero-filled before its first use and left ready for
- *          the next call of the same shape; calls that can overlap need one each
+ *          the next call, of any shape that it is large enough for; calls that can overlap need one each
  *   1 <= beams <= QSPEC_BEAM_MAX_BEAMS, 1 <= n <= min(QSPEC_BEAM_MAX_N, beams * V), 2 <= V <= 2^24, B <= 65535,
  *   B*beams*V < 2^40; the other arrays 4-byte aligned
  * Sums of exponentials are fp32 by trees of at most 2^15 terms and fp64 beyond, log probabilities and comparisons fp64, score is
@@ -686,7 +686,8 @@ qspec_status qspec_kv_compact(const qspec_kv_cache* caches, int32_t n_caches, co
 /*
  * qspec_kv_attention_shared -- qspec_kv_attention for sequences that share a prefix, which is read and multiplied once for all of
  * them.  Group g is the sequences cu_seq[g] .. cu_seq[g+1] - 1; the first len[g] cache positions of all of them hold the same
- * tokens, and are read through the page table of the group's first sequence that has new tokens.  (A group of one sequence, or
+ * tokens, and are read through the page table of the group's first sequence that has new tokens: entries of pages that lie wholly in the
+ * prefix are not read in the others' tables.  (A group of one sequence, or
  * of any sequences with len = 0, is plain attention.)  len[g] may exceed what its sequences have in common with their new tokens
  * taken off: the prefix ends where the new tokens of one of them begin, at the latest.
  *   cu_seq [n_groups+1] int32, non-decreasing within [0, B];  len [n_groups] int32 (both DEVICE, 4-byte aligned)

@@ -34,7 +34,7 @@ struct BeamArgs {
   int32_t* tok;
   float* score;
   unsigned int* err;
-  unsigned int* tickets;        // [B]
+  unsigned int* tickets;        // [65536]
   float2* stats;                // [B, K, chunks]: maximum, sum of exponentials
   unsigned long long* offers;   // [B, K, chunks, n]: ordered logit << 32 | ~token; 0: none
   long long total;              // logits in all
@@ -491,7 +491,7 @@ bool beam_plan(int64_t B, int64_t K, int64_t V, int64_t n, BeamPlan& p) {
   p.chunk_len = static_cast<int>((V + c - 1) / c);
   p.chunks = static_cast<int>((V + p.chunk_len - 1) / p.chunk_len);
   const size_t lists = static_cast<size_t>(B) * K * p.chunks;
-  p.stats = (sizeof(unsigned int) * B + 255) & ~size_t(255);
+  p.stats = sizeof(unsigned int) * 65536;  // (tickets of the largest batch: they are where they were for calls of any shape)
   p.offers = (p.stats + sizeof(float2) * lists + 255) & ~size_t(255);
   p.total = p.offers + sizeof(unsigned long long) * lists * n;
   return true;
@@ -519,6 +519,7 @@ extern "C" qspec_status qspec_beam_select(const uint16_t* logits, const float* s
       !aligned4(score) || !aligned16(ws))
     return QSPEC_ERR_MISALIGNED;
   if (!ws || ws_bytes < p.total) return QSPEC_ERR_WORKSPACE;
+  if (score < scores + static_cast<int64_t>(B) * beams && scores < score + static_cast<int64_t>(B) * n) return QSPEC_ERR_INVALID_ARG;
   char* w = static_cast<char*>(ws);
   BeamArgs a{logits, scores, done, weights, parent, tok, score, linear_error_word(), reinterpret_cast<unsigned int*>(w),
              reinterpret_cast<float2*>(w + p.stats), reinterpret_cast<unsigned long long*>(w + p.offers),

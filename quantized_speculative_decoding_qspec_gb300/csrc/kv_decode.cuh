@@ -133,14 +133,11 @@ __global__ void __launch_bounds__(DecodeCfg<D, RG>::kThreads, DecodeCfg<D, RG>::
         const int4 sg = seg[at];
         const int key = key0 + 16 * kw, table = at == 0 ? it.kv : sg.z;
         const int all_lo = at == 0 ? plan->pre_lo : plan->one_lo, all_hi = at == 0 ? it.hi : plan->one_hi;
-        int own_lo = 0;  // positions before a window may have no page any more
-        if (a.window > 0) {
-          if (at == 0) {
-            own_lo = it.lo;
-          } else {
-            int own_hi;
-            walk->own_range(sg.z, it.tok0 + a.token_of(it.row0), it.tok0 + a.token_of(it.row0 + it.rows - 1), it.hi, own_lo, own_hi);
-          }
+        // positions before a window may have no page any more, those of the prefix none in this sequence's table
+        int own_lo = at == 0 ? it.lo : it.hi;
+        if (a.window > 0 && at > 0) {
+          int own_hi;
+          walk->own_range(sg.z, it.tok0 + a.token_of(it.row0), it.tok0 + a.token_of(it.row0 + it.rows - 1), it.hi, own_lo, own_hi);
         }
         if (key < sg.w && key + 16 > own_lo) {
           const int page = a.b.pages[static_cast<int64_t>(table) * a.b.max_pages + key / a.c.page];

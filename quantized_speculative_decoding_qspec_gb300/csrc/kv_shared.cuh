@@ -442,14 +442,11 @@ __device__ __forceinline__ SegBatch load_shared_segs(const AttArgs& a, const W& 
                 (static_cast<int64_t>(w.cu[sg.z + 1] - it.tok0) * a.group > half ? 2 : 0);
     }
   }
-  int own_lo = 0;  // positions before a window may have no page any more
-  if (a.window > 0) {
-    if (at == 0) {
-      own_lo = it.lo;
-    } else {
-      int own_hi;
-      w.own_range(sg.z, it.tok0 + a.token_of(it.row0), it.tok0 + a.token_of(it.row0 + it.rows - 1), it.hi, own_lo, own_hi);
-    }
+  // positions before a window may have no page any more, those of the prefix none in this sequence's table
+  int own_lo = at == 0 ? it.lo : it.hi;
+  if (a.window > 0 && at > 0) {
+    int own_hi;
+    w.own_range(sg.z, it.tok0 + a.token_of(it.row0), it.tok0 + a.token_of(it.row0 + it.rows - 1), it.hi, own_lo, own_hi);
   }
   const int key = x.key0 + (at_page - v * per_tile) * a.c.page;
   if (key < sg.w && key + a.c.page > own_lo) {

@@ -688,7 +688,7 @@ def qspec_beam_workspace_size(B, beams, V, n):
 
 
 def new_beam_workspace(B, beams, V, n, device="cuda"):
-    """A zero-filled beam-selection workspace (zero once; calls of this shape keep it ready)."""
+    """A zero-filled beam-selection workspace (zero once; calls keep it ready, for this shape and smaller ones)."""
     size = qspec_beam_workspace_size(B, beams, V, n)
     if size == 0:
         raise ValueError("invalid beam shape")

@@ -15,7 +15,7 @@ def lib():
 
 
 def call(lib, **change):
-    a = dict(logits=FAKE, scores=FAKE, done=None, end_tok=0, weights=None, B=2, beams=4, V=1000, n=4, parent=FAKE, tok=FAKE, score=FAKE,
+    a = dict(logits=FAKE, scores=FAKE, done=None, end_tok=0, weights=None, B=2, beams=4, V=1000, n=4, parent=FAKE, tok=FAKE, score=FAKE + 4096,
              ws=FAKE, ws_bytes=1 << 30)
     a.update(change)
     return lib.qspec_beam_select(*a.values(), None)
@@ -25,8 +25,8 @@ def call(lib, **change):
     (dict(logits=None), 1), (dict(scores=None), 1), (dict(parent=None), 1), (dict(tok=None), 1), (dict(score=None), 1), (dict(B=0), 1),
     (dict(beams=0), 1), (dict(V=0), 1), (dict(n=0), 1), (dict(n=-1), 1), (dict(beams=33), 2), (dict(n=65), 2), (dict(V=1), 2),
     (dict(V=(1 << 24) + 1), 2), (dict(B=65536), 2), (dict(V=2, beams=1, n=3), 2), (dict(B=65535, beams=32, V=1 << 24), 2),
-    (dict(logits=FAKE + 8), 3), (dict(scores=FAKE + 2), 3), (dict(done=FAKE + 1), 3), (dict(weights=FAKE + 2), 3), (dict(tok=FAKE + 2), 3),
-    (dict(ws=FAKE + 8), 3), (dict(ws=None), 4), (dict(ws_bytes=511), 4)])
+    (dict(score=FAKE), 1), (dict(score=FAKE + 28), 1), (dict(score=FAKE - 28), 1), (dict(logits=FAKE + 8), 3), (dict(scores=FAKE + 2), 3), (dict(done=FAKE + 1), 3), (dict(weights=FAKE + 2), 3), (dict(tok=FAKE + 2), 3),
+    (dict(ws=FAKE + 8), 3), (dict(ws=None), 4), (dict(ws_bytes=65536 * 4), 4)])
 def test_arguments(lib, change, code):
     assert call(lib, **change) == code
 
@@ -35,7 +35,7 @@ def test_workspace_sizes(lib):
     assert lib.qspec_beam_workspace_size(0, 4, 1000, 4) == 0 and lib.qspec_beam_workspace_size(1, 33, 1000, 4) == 0
     assert lib.qspec_beam_workspace_size(1, 4, 1000, 65) == 0 and lib.qspec_beam_workspace_size(1, 1, 2, 3) == 0
     small, large = lib.qspec_beam_workspace_size(1, 1, 1000, 1), lib.qspec_beam_workspace_size(64, 8, 152064, 16)
-    assert 0 < small < large < 1 << 22
+    assert 0 < small < large < 1 << 22 and small > 4 * 65536
 
 
 def test_the_binding_refuses_short_tensors():

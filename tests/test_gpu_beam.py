@@ -194,3 +194,12 @@ def test_a_workspace_serves_call_after_call_in_a_graph_and_on_another_stream():
         graph.replay()
         check((parent.cpu(), tok.cpu(), score.cpu()), x, scores, n)
     q.qspec_check_status()
+
+
+def test_a_workspace_serves_smaller_shapes_too():
+    q = lib()
+    ws = q.new_beam_workspace(20, 5, 9000, 10)
+    for B, K, V, n in ((20, 5, 9000, 10), (3, 5, 9000, 2), (20, 1, 70, 10), (7, 4, 8191, 5), (20, 5, 9000, 10)):
+        x, scores, _ = inputs(B + V, B, K, V)
+        check(call(q, x, scores, n, ws=ws), x, scores, n)
+    q.qspec_check_status()

@@ -296,3 +296,15 @@ def test_strided_rows_graphs_streams_and_repeats():
         graph.replay()
         check(bt, wide[:, 1:9].cpu(), room[:, 2:10].double().cpu(), lse.double().cpu())
     q.qspec_check_status()
+
+
+def test_pages_of_the_prefix_are_looked_up_for_the_first_sequence_alone():
+    q = lib()
+    for members, tok in (([3], 1), ([4], 20)):
+        for prefix in (100, 128, 250):
+            bt = shared_batch(prefix, members, lambda r: tok, [prefix], lambda r: 70, 2, 16, 64)
+            qt, out, lse = call(q, bt, 8, [prefix])
+            bt.table[1:, :prefix // 16] = -5
+            _, out2, lse2 = call(q, bt, 8, [prefix])
+            q.qspec_check_status()
+            assert torch.equal(out, out2) and torch.equal(lse, lse2)
