@@ -18,6 +18,8 @@ namespace cg = cooperative_groups;
 //   3  free pages (count 0) are counted by ranges of ids, the counts exchanged through distributed shared memory;
 //   4  the k-th free page goes to the k-th page that the rows lack.
 // Every result goes by indices alone, never by the order in which atomics arrive.
+// 64 rows of 64 entries, 256 rows of 40 and one of four: 10 to 16 us, a chain of some twenty reads of memory, cluster barriers and
+// scans; the bytes are a few hundred KB at most.
 constexpr int kPageThreads = 1024;
 constexpr int kMaxRows = QSPEC_KV_MAX_B;
 constexpr int kHash = 2 * kMaxRows;
@@ -280,7 +282,7 @@ struct CopyArgs {
 };
 
 // A block copies one side (z) of some heads of one pair of pages (x) in one layer (y): four 16-byte loads a thread, then
-// the stores.
+// the stores.  One round of memory bounds it: 2 to 4 us for up to 13 MB.
 __global__ void __launch_bounds__(kCopyThreads) copy_pages_kernel(const __grid_constant__ CopyArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -361,11 +363,12 @@ __device__ __forceinline__ uint4 rescaled(uint4 c, int from, int to) {
 }
 
 // A block owns one side of up to eight heads of one sequence, a warp one head, in some layers one after the other (the chain of
-// indices, half of a step's latency, is paid once for them: 64 paths in 32 layers: 51 us with a block to each layer, 43 with one to three).  A lane takes 16 codes
-// of a token, the warp 16 tokens (with heads of 64: 32) at a time: paths of up to that length are read once, longer ones once for
-// the scales and once to be moved.  A path's nodes rise, so a token's new place is never behind the places that are still to be read, in the
-// order of the tokens.  What is written follows the append: a page begun here takes the scale of what it receives, another one
-// grows where it must.
+// indices, half of a step's latency, is paid once for them: 64 paths in 32 layers: 51 us with a block to each layer, 43 with one
+// to three).  A lane takes 16 codes of a token, the warp 16 tokens (with heads of 64: 32) at a time: paths of up to that length are
+// read once, longer ones once for the scales and once to be moved.  A path's nodes rise, so a token's new place is never behind the
+// places that are still to be read, in the order of the tokens.  What is written follows the append: a page begun here takes the
+// scale of what it receives, another one grows where it must.  One path in one layer takes 4.5 us; in those 64 the latency of three
+// reads that follow one another, with few bytes each, bounds it at 0.8 TB/s.
 template <int D>
 __global__ void __launch_bounds__(32 * kCompactWarps, 4) compact_kernel(const __grid_constant__ CompactArgs a) {
   constexpr int kPerTok = D / 16, kItems = 4, kAtOnce = 32 * kItems / kPerTok, kPages = QSPEC_MAX_TREE / 16 + 1;

@@ -292,7 +292,7 @@ __device__ __forceinline__ void share_out(const AttArgs& a, int2* grp, ScanShare
 // An item's stream: its segments in order, [0] the prefix.  seg = {tiles up to its end, first key tile, sequence or -1, end of
 // what is seen}.
 // Own tiles of the prefill kernel's full items are taken in turn from the sequences of the first and of the second query tile, so
-// that one's softmax runs under the other's products (128 sequences of up to 4000 positions of their own: 321 -> @@ us): behind the prefix
+// that one's softmax runs under the other's products (128 sequences of up to 4000 positions of their own: 310 -> 278 us): behind the prefix
 // come those of a sequence that has rows in both, then the others in proportion to what each query tile has.
 struct Plan {
   int count;
