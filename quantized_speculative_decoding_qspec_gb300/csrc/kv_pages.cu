@@ -331,7 +331,7 @@ struct CompactArgs {
   const int32_t* count;
   unsigned int* err;
   int64_t n_pages;
-  int heads, page, T, first, layers, layers_per;
+  int heads, page, shift, T, first, layers, layers_per;
 };
 
 // The smallest e with amax <= 448 * 2^e = 1.75 * 2^(e + 8), limited to the stored range; amax >= 0 as fp32 bits.
@@ -382,7 +382,7 @@ __global__ void __launch_bounds__(32 * kCompactWarps, 4) compact_kernel(const __
   const int n = a.count[b];
   const int tree = sp.n - a.first;  // nodes that were appended
   const int base = sp.kv - tree;    // the position of node 0, and of the path's first token
-  const int P = a.page, pg0 = base / P;
+  const int P = a.page, pg0 = base >> a.shift;
   bool ok = sp.ok && n >= 0 && n <= a.T && n <= max(tree, 0) && sp.n <= sp.kv;
   if (ok && n > 0) {
     if (threadIdx.x < n) {
@@ -396,7 +396,7 @@ __global__ void __launch_bounds__(32 * kCompactWarps, 4) compact_kernel(const __
       ok = false;
     } else if (t >= 0 && t < kPages + 1) {
       int p = 0;
-      if (pg0 + t <= (sp.kv - 1) / P) {
+      if (pg0 + t <= (sp.kv - 1) >> a.shift) {
         p = a.b.pages[static_cast<int64_t>(b) * a.b.max_pages + pg0 + t];
         ok = p >= 0 && p < a.n_pages;
       }
@@ -410,7 +410,7 @@ __global__ void __launch_bounds__(32 * kCompactWarps, 4) compact_kernel(const __
   }
   if (n == 0 || head >= a.heads) return;
   const int64_t page_codes = static_cast<int64_t>(a.heads) * P * D;
-  const int pages = (base + n - 1) / P - pg0 + 1;
+  const int pages = ((base + n - 1) >> a.shift) - pg0 + 1;
   const int layer0 = (blockIdx.z >> 1) * a.layers_per, layer1 = min(layer0 + a.layers_per, a.layers);
 #pragma unroll 1
   for (int layer = layer0; layer < layer1; ++layer) {
@@ -425,11 +425,12 @@ __global__ void __launch_bounds__(32 * kCompactWarps, 4) compact_kernel(const __
 #pragma unroll
       for (int k = 0; k < kItems; ++k) {
         const int i = k * 32 + lane, t = t0 + i / kPerTok;
+        if (t0 + k * (32 / kPerTok) >= n) break;
         c[k] = make_uint4(0, 0, 0, 0);
         e_of[k] = 0;
         if (t < n) {
-          const int pos = base + node_of[t], q = pos / P - pg0;
-          c[k] = *reinterpret_cast<const uint4*>(codes + page_of[q] * page_codes + (pos % P) * D + (i % kPerTok) * 16);
+          const int pos = base + node_of[t], q = (pos >> a.shift) - pg0;
+          c[k] = *reinterpret_cast<const uint4*>(codes + page_of[q] * page_codes + (pos & (P - 1)) * D + (i % kPerTok) * 16);
           e_of[k] = exp_at(q);
         }
       }
@@ -441,7 +442,8 @@ __global__ void __launch_bounds__(32 * kCompactWarps, 4) compact_kernel(const __
       load(t0);
 #pragma unroll
       for (int k = 0; k < kItems; ++k) {
-        const int t = t0 + (k * 32 + lane) / kPerTok, q = (base + t) / P - pg0;
+        if (t0 + k * (32 / kPerTok) >= n) break;
+        const int t = t0 + (k * 32 + lane) / kPerTok, q = ((base + t) >> a.shift) - pg0;
         const uint32_t v = __float_as_uint(__uint_as_float(amax_codes(c[k])) * exp2_int(e_of[k]));
 #pragma unroll
         for (int p = 0; p < kPages; ++p)
@@ -451,6 +453,8 @@ __global__ void __launch_bounds__(32 * kCompactWarps, 4) compact_kernel(const __
     int e_new[kPages];
 #pragma unroll
     for (int p = 0; p < kPages; ++p) {
+      e_new[p] = 0;
+      if (p >= pages) break;
       e_new[p] = exp_of_f32(__reduce_max_sync(0xFFFFFFFFu, amax[p]));
       if ((pg0 + p) * P < base) e_new[p] = max(old, e_new[p]);
     }
@@ -460,12 +464,13 @@ __global__ void __launch_bounds__(32 * kCompactWarps, 4) compact_kernel(const __
       __syncwarp();  // (what these tokens' places hold has been read by all lanes)
 #pragma unroll
       for (int k = 0; k < kItems; ++k) {
-        const int i = k * 32 + lane, t = t0 + i / kPerTok, pos = base + t, q = pos / P - pg0;
+        if (t0 + k * (32 / kPerTok) >= n) break;
+        const int i = k * 32 + lane, t = t0 + i / kPerTok, pos = base + t, q = (pos >> a.shift) - pg0;
         if (t < n) {
           int e = e_new[0];
 #pragma unroll
           for (int p = 1; p < kPages; ++p) e = q == p ? e_new[p] : e;
-          *reinterpret_cast<uint4*>(codes + page_of[q] * page_codes + (pos % P) * D + (i % kPerTok) * 16) = rescaled(c[k], e_of[k], e);
+          *reinterpret_cast<uint4*>(codes + page_of[q] * page_codes + (pos & (P - 1)) * D + (i % kPerTok) * 16) = rescaled(c[k], e_of[k], e);
         }
       }
       __syncwarp();
@@ -599,6 +604,7 @@ extern "C" qspec_status qspec_kv_compact(const qspec_kv_cache* caches, int32_t n
   a.n_pages = caches->n_pages;
   a.heads = caches->heads;
   a.page = caches->page;
+  for (a.shift = 0; (1 << a.shift) < a.page;) ++a.shift;
   a.T = T;
   a.first = first;
   // layers of a block: one, unless the blocks are more than twice what is resident
