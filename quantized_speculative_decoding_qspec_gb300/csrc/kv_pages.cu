@@ -363,16 +363,18 @@ __device__ __forceinline__ uint4 rescaled(uint4 c, int from, int to) {
 }
 
 // A block owns one side of up to eight heads of one sequence, a warp one head, in some layers one after the other (the chain of
-// indices, half of a step's latency, is paid once for them: 64 paths in 32 layers: 51 us with a block to each layer, 43 with one
-// to three).  A lane takes 16 codes of a token, the warp 16 tokens (with heads of 64: 32) at a time: paths of up to that length are
-// read once, longer ones once for the scales and once to be moved.  A path's nodes rise, so a token's new place is never behind the
-// places that are still to be read, in the order of the tokens.  What is written follows the append: a page begun here takes the
-// scale of what it receives, another one grows where it must.  One path in one layer takes 4.5 us; in those 64 the latency of three
-// reads that follow one another, with few bytes each, bounds it at 0.8 TB/s.
+// indices is paid once for them).  A lane takes 16 codes of a token, the warp 16 tokens (with heads of 64: 32) at a time: paths of
+// up to that length are read once, longer ones once for the scales and once to be moved.  A path's nodes rise, so a token's new
+// place is never behind the places that are still to be read, in the order of the tokens.  What is written follows the append: a
+// page begun here takes the scale of what it receives, another one grows where it must.
+// One path in one layer takes 4 us.  64 paths in 32 layers take 22 us, 1.5 TB/s in reads and writes of 64 or 128 bytes; with the
+// places worked out for each layer anew, by divisions, it took 43, so instructions bounded it.  (The next layer's codes loaded
+// ahead: 23 us.)
 template <int D>
 __global__ void __launch_bounds__(32 * kCompactWarps, 4) compact_kernel(const __grid_constant__ CompactArgs a) {
   constexpr int kPerTok = D / 16, kItems = 4, kAtOnce = 32 * kItems / kPerTok, kPages = QSPEC_MAX_TREE / 16 + 1;
-  __shared__ int node_of[QSPEC_MAX_TREE];
+  __shared__ int64_t from_of[QSPEC_MAX_TREE], to_of[QSPEC_MAX_TREE];  // a token's codes of head 0
+  __shared__ int64_t exp_of[QSPEC_MAX_TREE];                          // and the scale that they have
   __shared__ int page_of[kPages + 1];  // pages of the tree's positions, from the path's first on
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -384,11 +386,11 @@ __global__ void __launch_bounds__(32 * kCompactWarps, 4) compact_kernel(const __
   const int base = sp.kv - tree;    // the position of node 0, and of the path's first token
   const int P = a.page, pg0 = base >> a.shift;
   bool ok = sp.ok && n >= 0 && n <= a.T && n <= max(tree, 0) && sp.n <= sp.kv;
+  int j = 0;
   if (ok && n > 0) {
     if (threadIdx.x < n) {
       const int32_t* at = a.nodes + static_cast<int64_t>(b) * a.T + threadIdx.x;
-      const int j = at[0];
-      node_of[threadIdx.x] = j;
+      j = at[0];
       ok = j >= 0 && j < tree && (threadIdx.x == 0 || j > at[-1]);
     }
     const int t = threadIdx.x - QSPEC_MAX_TREE;
@@ -408,17 +410,23 @@ __global__ void __launch_bounds__(32 * kCompactWarps, 4) compact_kernel(const __
     if (threadIdx.x == 0) atomicOr(a.err, kErrInvalid);
     return;
   }
-  if (n == 0 || head >= a.heads) return;
+  if (n == 0) return;
   const int64_t page_codes = static_cast<int64_t>(a.heads) * P * D;
+  if (threadIdx.x < n) {
+    const int from = base + j, to = base + threadIdx.x, page = page_of[(from >> a.shift) - pg0];
+    exp_of[threadIdx.x] = static_cast<int64_t>(page) * a.heads;
+    from_of[threadIdx.x] = page * page_codes + (from & (P - 1)) * D;
+    to_of[threadIdx.x] = page_of[(to >> a.shift) - pg0] * page_codes + (to & (P - 1)) * D;
+  }
+  __syncthreads();
+  if (head >= a.heads) return;
   const int pages = ((base + n - 1) >> a.shift) - pg0 + 1;
   const int layer0 = (blockIdx.z >> 1) * a.layers_per, layer1 = min(layer0 + a.layers_per, a.layers);
 #pragma unroll 1
   for (int layer = layer0; layer < layer1; ++layer) {
     uint8_t* const codes = a.l.codes[side][layer] + static_cast<int64_t>(head) * P * D;
     int8_t* const exps = a.l.exps[side][layer] + head;
-    auto exp_at = [&](int q) {
-      return min(max(static_cast<int>(exps[static_cast<int64_t>(page_of[q]) * a.heads]), kKvMinExp), kKvMaxExp);
-    };
+    auto exp_at = [&](int64_t i) { return min(max(static_cast<int>(exps[i]), kKvMinExp), kKvMaxExp); };
     uint4 c[kItems];
     int e_of[kItems];
     auto load = [&](int t0) {  // tokens t0 ...: the codes of the lane's items and their scales
@@ -429,13 +437,12 @@ __global__ void __launch_bounds__(32 * kCompactWarps, 4) compact_kernel(const __
         c[k] = make_uint4(0, 0, 0, 0);
         e_of[k] = 0;
         if (t < n) {
-          const int pos = base + node_of[t], q = (pos >> a.shift) - pg0;
-          c[k] = *reinterpret_cast<const uint4*>(codes + page_of[q] * page_codes + (pos & (P - 1)) * D + (i % kPerTok) * 16);
-          e_of[k] = exp_at(q);
+          c[k] = *reinterpret_cast<const uint4*>(codes + from_of[t] + (i % kPerTok) * 16);
+          e_of[k] = exp_at(exp_of[t]);
         }
       }
     };
-    const int old = exp_at(0);  // (the first page alone can be one that goes on)
+    const int old = exp_at(static_cast<int64_t>(page_of[0]) * a.heads);  // (the first page alone can be one that goes on)
     uint32_t amax[kPages] = {};
 #pragma unroll 1
     for (int t0 = 0; t0 < n; t0 += kAtOnce) {
@@ -465,12 +472,12 @@ __global__ void __launch_bounds__(32 * kCompactWarps, 4) compact_kernel(const __
 #pragma unroll
       for (int k = 0; k < kItems; ++k) {
         if (t0 + k * (32 / kPerTok) >= n) break;
-        const int i = k * 32 + lane, t = t0 + i / kPerTok, pos = base + t, q = (pos >> a.shift) - pg0;
+        const int i = k * 32 + lane, t = t0 + i / kPerTok, q = ((base + t) >> a.shift) - pg0;
         if (t < n) {
           int e = e_new[0];
 #pragma unroll
           for (int p = 1; p < kPages; ++p) e = q == p ? e_new[p] : e;
-          *reinterpret_cast<uint4*>(codes + page_of[q] * page_codes + (pos & (P - 1)) * D + (i % kPerTok) * 16) = rescaled(c[k], e_of[k], e);
+          *reinterpret_cast<uint4*>(codes + to_of[t] + (i % kPerTok) * 16) = rescaled(c[k], e_of[k], e);
         }
       }
       __syncwarp();
@@ -607,9 +614,10 @@ extern "C" qspec_status qspec_kv_compact(const qspec_kv_cache* caches, int32_t n
   for (a.shift = 0; (1 << a.shift) < a.page;) ++a.shift;
   a.T = T;
   a.first = first;
-  // layers of a block: one, unless the blocks are more than twice what is resident
+  // layers of a block: one, unless the blocks are more than three times what is resident (64 paths in 32 layers: two 22 us, three 24,
+  // six 33)
   const int64_t all = static_cast<int64_t>(batch->B) * ((a.heads + kCompactWarps - 1) / kCompactWarps) * 2 * n_caches;
-  const int64_t per = all / (8 * num_sms());
+  const int64_t per = all / (12 * num_sms());
   a.layers = n_caches;
   a.layers_per = per < 1 ? 1 : per > n_caches ? n_caches : static_cast<int>(per);
   const dim3 grid(batch->B, (a.heads + kCompactWarps - 1) / kCompactWarps, 2 * ((n_caches + a.layers_per - 1) / a.layers_per));
