@@ -674,7 +674,7 @@ qspec_status qspec_kv_copy_pages(const qspec_kv_cache* caches, int32_t n_caches,
  * values of node nodes[b, t] move to position kv_len - n + first + t, as if qspec_kv_append wrote their (dequantised) values there:
  * a page whose slot 0 is written takes the smallest scale that holds what it receives, another page's scale grows where it
  * must.  The sequence's length after it is kv_len - n + first + count[b].
- *   caches, n_caches  as for qspec_kv_copy_pages;  batch: as it was for the append
+ *   caches, n_caches  as for qspec_kv_copy_pages, none of them twice;  batch: as it was for the append
  *   nodes [B, T] int32, count [B] int32 DEVICE, 4-byte aligned: what qspec_verify_tree_greedy returns.  1 <= T <=
  *   QSPEC_MAX_TREE;  first >= 0;  nodes rising in [0, n - first), n - first <= QSPEC_MAX_TREE, count[b] <= min(T, n - first)
  * A sequence whose numbers, nodes or pages are out of range is left as it is and makes the next qspec_check_status return

@@ -601,6 +601,9 @@ extern "C" qspec_status qspec_kv_compact(const qspec_kv_cache* caches, int32_t n
   qspec_status st = check_layers(caches, n_caches, a.l);
   if (st != QSPEC_OK) return st;
   if ((st = check_kv(caches, batch)) != QSPEC_OK) return st;
+  for (int i = 1; i < n_caches; ++i)  // (a path that moved twice at once)
+    for (int j = 0; j < i; ++j)
+      if (a.l.codes[0][i] == a.l.codes[0][j] || a.l.codes[1][i] == a.l.codes[1][j]) return QSPEC_ERR_INVALID_ARG;
   if (T > QSPEC_MAX_TREE) return QSPEC_ERR_UNSUPPORTED_SHAPE;
   if (!aligned4(nodes) || !aligned4(count)) return QSPEC_ERR_MISALIGNED;
   a.b = *batch;

@@ -96,3 +96,10 @@ def test_the_binding_refuses_short_tensors():
         q.qspec_kv_copy_pages(None, z(3), z(3), lengths=z(2))
     with pytest.raises(ValueError, match="at least one"):
         q.KVLayers([])
+
+
+def test_a_cache_listed_twice_is_not_compacted(lib):
+    batch = q.KVBatchDesc(FAKE, FAKE, FAKE, 2, 4, 8, 0, 16)
+    for change in (dict(k=FAKE), dict(v=FAKE)):
+        arr = (q.KVCacheDesc * 3)(cache(), cache(k=FAKE * 2, v=FAKE * 3), cache(**dict(dict(k=FAKE * 4, v=FAKE * 5), **change)))
+        assert lib.qspec_kv_compact(arr, 3, ctypes.byref(batch), FAKE, FAKE, 8, 1, None) == 1
