@@ -102,7 +102,10 @@ struct BeamShared {
   float2 warp_stat[kWarps];
   int count;
   double lse[kMaxBeams];
+  float row_score[kMaxBeams], row_weight[kMaxBeams];
+  bool row_done[kMaxBeams];
   float2 row_stat[kMaxBeams];
+  uint32_t bound;
   int n_list, last;
 };
 
@@ -112,14 +115,35 @@ struct Candidate {
   int row, tok;
 };
 
+// ln s for 1 <= s: the power of two apart, so that the error is that of logf near 1, 2^-24.  (fp64 runs at a fiftieth of fp32's rate:
+// its logarithm took 1 us of the merge.)
+__device__ __forceinline__ double ln_of_sum(float s) {
+  int e = static_cast<int>(__float_as_uint(s) >> 23) - 127;
+  float m = __uint_as_float((__float_as_uint(s) & 0x7FFFFFu) | 0x3F800000u);
+  if (m > 1.41421356f) {
+    m *= 0.5f;
+    ++e;
+  }
+  return e * 0.69314718055994531 + static_cast<double>(logf(m));
+}
+
 // The last CTA of sequence b: the beams' sums, then the n best of what the lists offer.
 __device__ __noinline__ void merge(const BeamArgs& a, BeamShared& sh, int b) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int lists = a.K * a.chunks, n = a.n;
   const float2* stats = a.stats + static_cast<long long>(b) * lists;
   const unsigned long long* offers = a.offers + static_cast<long long>(b) * lists * n;
-  // lse[k], a warp to a beam; NaN where the beam offers nothing.  (fp64 runs at a fiftieth of fp32's rate: one logarithm for all beams
-  // at once, in a warp's lanes; with an exponential for each chunk and a logarithm in each warp this took 10 us.)
+  // (what comes from memory is asked for at once: each round of it takes 0.6 us)
+  const unsigned long long first = tid < lists ? __ldcg(offers + static_cast<long long>(tid) * n) : 0;
+  float score = 0.0f, weight = 1.0f;
+  bool done = false;
+  if (tid < a.K) {
+    const long long at = static_cast<long long>(b) * a.K + tid;
+    score = a.scores[at];
+    if (a.weights) weight = a.weights[at];
+    done = a.done && a.done[at] != 0;
+  }
+  // the beams' maxima and sums, a warp to a beam; NaN where the beam offers nothing
   for (int k = warp; k < a.K; k += kWarps) {
     float m = -INFINITY;
     bool nan = false;
@@ -143,57 +167,64 @@ __device__ __noinline__ void merge(const BeamArgs& a, BeamShared& sh, int b) {
   }
   __syncthreads();
   if (tid < a.K) {
-    const long long at = static_cast<long long>(b) * a.K + tid;
     const float2 x = sh.row_stat[tid];
-    const float s = a.scores[at], w = a.weights ? a.weights[at] : 1.0f;
-    const bool done = a.done && a.done[at] != 0;
-    const bool odd = !(s < INFINITY) || !(w > 0.0f && w < INFINITY) || (x.x != x.x && !done);
+    const bool odd = !(score < INFINITY) || !(weight > 0.0f && weight < INFINITY) || (x.x != x.x && !done);
     if (odd) atomicOr(a.err, kErrInvalid);
-    const bool none = odd || s == -INFINITY || (!done && !(x.x > -INFINITY));
-    const double lse = static_cast<double>(x.x) + log(static_cast<double>(x.y));
-    sh.lse[tid] = none ? NAN : done ? 0.0 : lse;
+    const bool none = odd || score == -INFINITY || (!done && !(x.x > -INFINITY));
+    sh.lse[tid] = none ? NAN : done ? 0.0 : static_cast<double>(x.x) + ln_of_sum(x.y);
+    sh.row_score[tid] = score;
+    sh.row_weight[tid] = weight;
+    sh.row_done[tid] = done;
   }
   __syncthreads();
 
   // ---- the best n lists by their first offers, in order: the r-th can give n - r of the n best.  (Choosing the n best one after
   // the other by reductions over the lists took 5 to 7 us for eight.)
-  auto candidate = [&](int list, int e, Candidate& c) {  // false: no offer
+  auto candidate = [&](int list, int e, unsigned long long offer, Candidate& c) {  // false: no offer
     const int k = list / a.chunks;
-    const long long at = static_cast<long long>(b) * a.K + k;
     const double lse = sh.lse[k];
     if (lse != lse) return false;
-    c.S = a.scores[at];
+    c.S = sh.row_score[k];
     c.tok = a.end_tok;
-    c.row = static_cast<int>(at);
-    if (a.done && a.done[at] != 0) {
+    c.row = b * a.K + k;
+    if (sh.row_done[k]) {
       if (e > 0 || list != k * a.chunks) return false;
     } else {
-      const unsigned long long offer = __ldcg(offers + static_cast<long long>(list) * n + e);
       if (offer == 0) return false;
       c.tok = static_cast<int>(~static_cast<uint32_t>(offer));
       c.S += static_cast<double>(value_of(static_cast<uint32_t>(offer >> 32))) - lse;
     }
-    c.key = ordered64(a.weights ? c.S * a.weights[at] : c.S);
+    c.key = ordered64(a.weights ? c.S * sh.row_weight[k] : c.S);
     return true;
   };
   Candidate c;
-  const unsigned long long head = tid < lists && candidate(tid, 0, c) ? c.key : 0;
+  const unsigned long long head = tid < lists && candidate(tid, 0, first, c) ? c.key : 0;
   sh.head[tid] = head;
   if (tid < n) sh.best_list[tid] = -1;
   if (tid == 0) sh.count = 0;
   __syncthreads();
   if (head != 0) {
     int place = 0;
-    for (int j = 0; j < lists; ++j) place += sh.head[j] > head || (sh.head[j] == head && j < tid);
+#pragma unroll 4
+    for (int j = 0; j < lists; ++j) {
+      const unsigned long long x = sh.head[j];
+      place += (x > head) | ((x == head) & (j < tid));
+    }
     if (place < n) sh.best_list[place] = tid;
   }
   __syncthreads();
   const int pairs = n * (n + 1) / 2;
+  auto pair = [&](int p, int& list, int& e) {
+    int r = 0;
+    for (e = p; e >= n - r;) e -= n - r++;
+    list = sh.best_list[r];
+    return list >= 0 && candidate(list, e, __ldcg(offers + static_cast<long long>(list) * n + e), c);
+  };
+  Candidate mine;
   for (int p = tid; p < pairs; p += kThreads) {
-    int r = 0, e = p;
-    while (e >= n - r) e -= n - r++;
-    const int list = sh.best_list[r];
-    const bool real = list >= 0 && candidate(list, e, c);
+    int list, e;
+    const bool real = pair(p, list, e);
+    if (p == tid) mine = c;
     sh.pair_key[p] = real ? c.key : 0;
     sh.pair_order[p] = static_cast<uint16_t>(list << 6 | e);
     if (real) atomicAdd(&sh.count, 1);
@@ -205,13 +236,20 @@ __device__ __noinline__ void merge(const BeamArgs& a, BeamShared& sh, int b) {
     const uint16_t order = sh.pair_order[p];
     if (key == 0) continue;
     int place = 0;
-    for (int j = 0; j < pairs; ++j) place += sh.pair_key[j] > key || (sh.pair_key[j] == key && sh.pair_order[j] < order);
-    if (place < n && candidate(order >> 6, order & 63, c)) {
-      const long long out = static_cast<long long>(b) * n + place;
-      a.parent[out] = c.row;
-      a.tok[out] = c.tok;
-      a.score[out] = static_cast<float>(c.S);
+#pragma unroll 4
+    for (int j = 0; j < pairs; ++j) {  // (both reads of a step at once: with the second behind a branch a step took 120 cycles)
+      const unsigned long long x = sh.pair_key[j];
+      const uint16_t o = sh.pair_order[j];
+      place += (x > key) | ((x == key) & (o < order));
     }
+    if (place >= n) continue;
+    c = mine;
+    int list, e;
+    if (p != tid) pair(p, list, e);
+    const long long out = static_cast<long long>(b) * n + place;
+    a.parent[out] = c.row;
+    a.tok[out] = c.tok;
+    a.score[out] = static_cast<float>(c.S);
   }
   if (tid < n && tid >= sh.count) {
     const long long out = static_cast<long long>(b) * n + tid;
@@ -286,6 +324,7 @@ __device__ __noinline__ void cut_down(BeamShared& sh, int count, int n) {
   for (int i = tid; i < count; i += kThreads) {
     const unsigned long long key = sh.list[i];
     int place = 0;
+#pragma unroll 8
     for (int j = 0; j < count; ++j) place += sh.list[j] > key;
     if (place < n && key != 0) sh.top[place] = key;
   }
@@ -386,24 +425,25 @@ __device__ __forceinline__ void take_tile(BeamShared& sh, const Chunk& c, int n,
     r.m = top;
   }
   if (t0 == 0) {
-    // ---- 64 groups of threads: the n-th largest of their maxima is a bound
+    // ---- 64 groups of threads: the n-th largest of their maxima is a bound.  A warp finds the places of four, with eight lanes to
+    // each (all of them in every warp: 1.5 us, the warps' issue slots)
     constexpr int kSize = kThreads / kMaxN;
     uint32_t g = mine;
 #pragma unroll
     for (int off = kSize / 2; off >= 1; off >>= 1) g = max(g, __shfl_xor_sync(0xFFFFFFFFu, g, off));
     if (lane % kSize == 0) sh.group[tid / kSize] = g << 6 | (kMaxN - 1 - tid / kSize);  // (no two alike)
     __syncthreads();
-    const uint32_t v0 = sh.group[lane], v1 = sh.group[lane + 32];
-    int before0 = 0, before1 = 0;
-#pragma unroll 4
-    for (int j = 0; j < kMaxN; ++j) {
-      const uint32_t v = sh.group[j];
-      before0 += v > v0;
-      before1 += v > v1;
-    }
-    static_assert(kMaxN == 64, "two groups a lane, six bits");
-    const uint32_t bound = before0 == n - 1 ? v0 >> 6 : before1 == n - 1 ? v1 >> 6 : 0;
-    r.bound = max(__reduce_max_sync(0xFFFFFFFFu, bound), kKeyLowest + 1);
+    constexpr int kLanes = kThreads / kMaxN, kEach = kMaxN / kLanes;
+    static_assert(kMaxN == 64 && kLanes >= 1 && kLanes <= 32, "six bits; a group's lanes in one warp");
+    const uint32_t v = sh.group[tid / kLanes];
+    int before = 0;
+#pragma unroll
+    for (int j = 0; j < kEach; ++j) before += sh.group[j * kLanes + tid % kLanes] > v;
+#pragma unroll
+    for (int off = kLanes / 2; off >= 1; off >>= 1) before += __shfl_xor_sync(0xFFFFFFFFu, before, off);
+    if (before == n - 1) sh.bound = v >> 6;
+    __syncthreads();
+    r.bound = max(sh.bound, kKeyLowest + 1);
   }
   if (__any_sync(0xFFFFFFFFu, mine >= r.bound)) {
 #pragma unroll
@@ -455,7 +495,7 @@ __global__ void __launch_bounds__(kThreads, 2) beam_kernel(const BeamArgs a) {
 #pragma unroll 1
     for (int t0 = 0; t0 < c.vecs; t0 += 2 * kTileVecs) {
       take_tile(sh, c, a.n, t0, x, r);
-      take_tile(sh, c, a.n, t0 + kTileVecs, y, r);  // (-inf behind the end)
+      if (t0 + kTileVecs < c.vecs) take_tile(sh, c, a.n, t0 + kTileVecs, y, r);
       if (t0 / kTileVecs % kCheck == kCheck - 2 || t0 + 2 * kTileVecs >= c.vecs)
         check_list(sh, c, a.n, t0 / (kCheck * kTileVecs) * (kCheck * kTileVecs), r);
     }
