@@ -3,12 +3,12 @@
 //     S(k, v) = score[k] + (logit[k, v] - lse[k]),   lse[k] = ln sum_v exp(logit[k, v])
 // Within a beam the order is that of its logits (bf16: ties are common, and go to the lowest token), so each beam offers its n
 // largest logits, and the beams' offers are ordered by S (times a weight).  One pass over the logits bounds it: a CTA
-// streams a part of a row through registers, a tile of 16384 at a time.  A thread keeps its own maximum and sum of exponentials;
-// the first tile gives a lower bound of the n-th largest logit, and the few that reach it are collected in shared memory,
-// with the loads of two tiles under way.  The last CTA of a sequence (atomic ticket) merges the offers.
-// (A tile of 32768 to a CTA, selected and handed over before the next CTA began: [64, 8, 152064] 102 us.)
-// [64, 8, 152064]: 61 us, 2.6 TB/s; [16, 4, 128256] 20, [1, 4, 32000] 12.  Loads and maxima alone take 40 of the 61
-// (512 chunks go in two rounds on 304 places); the rest is the first tile's bound, the lists and the merge, all latency.
+// streams a part of a row through registers, a tile of 16384 at a time, two tiles under way.  A thread keeps its own maximum and sum of
+// exponentials; the maxima give a lower bound of the n-th largest logit, from the first tile on and better with every look, and the few
+// vectors that reach it are collected in shared memory.  The last CTA of a sequence (atomic ticket) merges the offers.
+// [64, 8, 152064]: 49 us, 3.2 TB/s (a tile of 32768 to a CTA, selected and handed over before the next CTA began: 102); [16, 4, 128256] 14,
+// [1, 4, 32000] 8.6.  Loads and maxima alone take 40 of the 49 (512 rows go in two rounds on 304 places); the smaller ones are a chain of
+// latencies: the first tile 2 us, its bound 0.5, the list 1.5, the ticket 1, the merge 4.
 #include <math.h>
 
 #include "kv_internal.h"
@@ -19,10 +19,11 @@ namespace {
 constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kVecs = 4;                          // 16-byte loads in flight a thread
 constexpr int kTileVecs = kThreads * kVecs;       // 16384 logits
-constexpr int kList = 1024;                       // logits collected at most; a tile that brings more: see below
+constexpr int kList = 1024;                       // logits collected at most; tiles that bring more: see below
 constexpr int kListFull = 512;                    // from here on they are cut down to the n best
-constexpr int kCheck = 4;                         // tiles between looks at the list
-constexpr int kCtasPerSm = 2;                     // resident, and asked for
+constexpr int kVecList = 512;                     // vectors collected between looks at them
+constexpr int kCheck = 4;                         // tiles between looks
+constexpr int kCtasPerSm = 2;                     // resident
 constexpr int kMaxN = QSPEC_BEAM_MAX_N, kMaxBeams = QSPEC_BEAM_MAX_BEAMS;
 constexpr int kMaxLists = kThreads;               // (beam, chunk) pairs of a sequence: a thread each in the merge
 constexpr uint32_t kLowest = 0xFF80FF80u;         // two bf16 -inf
@@ -106,7 +107,9 @@ struct BeamShared {
   bool row_done[kMaxBeams];
   float2 row_stat[kMaxBeams];
   uint32_t bound;
-  int n_list, last;
+  uint4 vec[kVecList];
+  uint32_t token[kVecList];  // of a vector's first logit
+  int n_vec, n_list, last;
 };
 
 struct Candidate {
@@ -289,30 +292,10 @@ __device__ __forceinline__ uint32_t key_of(const uint4 (&x)[kVecs], int i, int e
   const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
   return ordered(e & 1 ? w[e >> 1] >> 16 : w[e >> 1] & 0xFFFFu);
 }
-// Collects a logit; false where the list is filling up.
-__device__ __forceinline__ bool collect(BeamShared& sh, uint32_t key, uint32_t token) {
+// Collects a logit.
+__device__ __forceinline__ void collect(BeamShared& sh, uint32_t key, uint32_t token) {
   const int at = atomicAdd(&sh.n_list, 1);
   if (at < kList + kMaxN) sh.list[at] = static_cast<unsigned long long>(key) << 32 | (0xFFFFFFFFu - token);
-  return at < kListFull;
-}
-
-// Collects what reaches the bound among the vectors of the lanes `who`, whose logits begin at `token` + 8 lanes: the warp takes one
-// vector after the other, eight lanes a logit each.  False where the list is filling up.  (A short loop of its own: every other warp
-// comes here in each tile, and with the 32 comparisons of a lane written out for one lane it spent 2500 cycles, as code that is seldom run
-// comes from far: [64, 8, 152064] 95 us, without any collecting 48.)
-__device__ __noinline__ bool collect_vectors(BeamShared& sh, uint4 x, uint32_t who, uint32_t token, uint32_t bound) {
-  const int lane = threadIdx.x & 31;
-  bool room = true;
-#pragma unroll 1
-  for (; who; who &= who - 1) {
-    const int src = __ffs(who) - 1;
-    const uint32_t w0 = __shfl_sync(0xFFFFFFFFu, x.x, src), w1 = __shfl_sync(0xFFFFFFFFu, x.y, src);
-    const uint32_t w2 = __shfl_sync(0xFFFFFFFFu, x.z, src), w3 = __shfl_sync(0xFFFFFFFFu, x.w, src);
-    const uint32_t lo = lane & 2 ? w1 : w0, hi = lane & 2 ? w3 : w2, w = lane & 4 ? hi : lo;
-    const uint32_t key = ordered(lane & 1 ? w >> 16 : w & 0xFFFFu);
-    if (lane < 8 && key >= bound) room = collect(sh, key, token + 8 * src + lane) && room;
-  }
-  return room;
 }
 
 // The n best of the list's first `count` entries, in order, become the list (and top): a key's place is the number of larger
@@ -334,13 +317,14 @@ __device__ __noinline__ void cut_down(BeamShared& sh, int count, int n) {
   __syncthreads();
 }
 
-// The tiles from t0 on, kCheck of them, brought far more logits than the list has places, as with many equal ones: what came from
-// them is taken out again, and their exact n-th largest (logit, lowest token) found bit by bit.  Returns the number of entries.
-__device__ __noinline__ int exact_tiles(BeamShared& sh, const Chunk& c, int t0, int n) {
+// The tiles from t0 on, kCheck of them, brought far more logits than there are places, as with many equal ones: what of them is among
+// the list's first `count` entries is taken out again, and their exact n-th largest (logit, lowest token) found bit by bit.  Returns
+// the number of entries.
+__device__ __noinline__ int exact_tiles(BeamShared& sh, const Chunk& c, int t0, int count, int n) {
   const int tid = threadIdx.x;
   const uint32_t tile0 = c.first_token + 8 * t0;
   for (int i = tid; i < kList; i += kThreads)
-    if (0xFFFFFFFFu - static_cast<uint32_t>(sh.list[i]) - tile0 < 8u * kCheck * kTileVecs) sh.list[i] = 0;
+    if (i >= count || 0xFFFFFFFFu - static_cast<uint32_t>(sh.list[i]) - tile0 < 8u * kCheck * kTileVecs) sh.list[i] = 0;
   uint4 x[kVecs];
   auto rank_of = [&](int k, int i, int e) {
     return key_of(x, i, e) << 16 | (0xFFFFu - static_cast<uint32_t>((k * kTileVecs + i * kThreads + tid) * 8 + e));
@@ -349,19 +333,19 @@ __device__ __noinline__ int exact_tiles(BeamShared& sh, const Chunk& c, int t0, 
   uint32_t exact = 0;
   for (int bit = 31; bit >= 0; --bit) {
     const uint32_t cand = exact | 1u << bit;
-    int count = 0;
+    int above = 0;
 #pragma unroll 1
     for (int k = 0; k < kCheck; ++k) {
       load_tile(c, t0 + k * kTileVecs, x);
 #pragma unroll
       for (int i = 0; i < kVecs; ++i)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) count += rank_of(k, i, e) >= cand;
+        for (int e = 0; e < 8; ++e) above += rank_of(k, i, e) >= cand;
     }
-    count = __reduce_add_sync(0xFFFFFFFFu, count);
+    above = __reduce_add_sync(0xFFFFFFFFu, above);
     if (tid == 0) sh.count = 0;
     __syncthreads();
-    if ((tid & 31) == 0 && count) atomicAdd(&sh.count, count);
+    if ((tid & 31) == 0 && above) atomicAdd(&sh.count, above);
     __syncthreads();
     if (sh.count >= n) exact = cand;
     __syncthreads();
@@ -388,11 +372,32 @@ struct Running {
   float m, s;      // its maximum and sum of exponentials
   uint32_t bound;  // of the n-th largest logit, from below
   bool bad;        // a NaN or +inf among its logits
-  bool crowded;    // it found the list filling up
 };
 
+// The n-th largest of 64 groups of threads' maxima: a bound of the n-th largest logit that they have seen.  A warp finds the places of
+// four, with eight lanes to each (all of them in every warp: 1.5 us, the warps' issue slots).  All threads; two barriers.
+__device__ __forceinline__ uint32_t bound_of(BeamShared& sh, uint32_t mine, int n) {
+  const int tid = threadIdx.x;
+  constexpr int kSize = kThreads / kMaxN;
+#pragma unroll
+  for (int off = kSize / 2; off >= 1; off >>= 1) mine = max(mine, __shfl_xor_sync(0xFFFFFFFFu, mine, off));
+  if (tid % kSize == 0) sh.group[tid / kSize] = mine << 6 | (kMaxN - 1 - tid / kSize);  // (no two alike)
+  __syncthreads();
+  constexpr int kLanes = kThreads / kMaxN, kEach = kMaxN / kLanes;
+  static_assert(kMaxN == 64 && kLanes >= 1 && kLanes <= 32, "six bits; a group's lanes in one warp");
+  const uint32_t v = sh.group[tid / kLanes];
+  int before = 0;
+#pragma unroll
+  for (int j = 0; j < kEach; ++j) before += sh.group[j * kLanes + tid % kLanes] > v;
+#pragma unroll
+  for (int off = kLanes / 2; off >= 1; off >>= 1) before += __shfl_xor_sync(0xFFFFFFFFu, before, off);
+  if (before == n - 1) sh.bound = v >> 6;
+  __syncthreads();
+  return sh.bound;
+}
+
 __device__ __forceinline__ void take_tile(BeamShared& sh, const Chunk& c, int n, int t0, uint4 (&x)[kVecs], Running& r) {
-  const int tid = threadIdx.x, lane = tid & 31;
+  const int tid = threadIdx.x;
   uint32_t pair = kLowest, most[kVecs];  // largest values, of even and odd places
 #pragma unroll
   for (int i = 0; i < kVecs; ++i) {
@@ -424,51 +429,49 @@ __device__ __forceinline__ void take_tile(BeamShared& sh, const Chunk& c, int n,
     r.s = (r.m > -INFINITY ? r.s * pow2((r.m - top) * kLog2e) : 0.0f) + (even + odd);
     r.m = top;
   }
-  if (t0 == 0) {
-    // ---- 64 groups of threads: the n-th largest of their maxima is a bound.  A warp finds the places of four, with eight lanes to
-    // each (all of them in every warp: 1.5 us, the warps' issue slots)
-    constexpr int kSize = kThreads / kMaxN;
-    uint32_t g = mine;
-#pragma unroll
-    for (int off = kSize / 2; off >= 1; off >>= 1) g = max(g, __shfl_xor_sync(0xFFFFFFFFu, g, off));
-    if (lane % kSize == 0) sh.group[tid / kSize] = g << 6 | (kMaxN - 1 - tid / kSize);  // (no two alike)
-    __syncthreads();
-    constexpr int kLanes = kThreads / kMaxN, kEach = kMaxN / kLanes;
-    static_assert(kMaxN == 64 && kLanes >= 1 && kLanes <= 32, "six bits; a group's lanes in one warp");
-    const uint32_t v = sh.group[tid / kLanes];
-    int before = 0;
-#pragma unroll
-    for (int j = 0; j < kEach; ++j) before += sh.group[j * kLanes + tid % kLanes] > v;
-#pragma unroll
-    for (int off = kLanes / 2; off >= 1; off >>= 1) before += __shfl_xor_sync(0xFFFFFFFFu, before, off);
-    if (before == n - 1) sh.bound = v >> 6;
-    __syncthreads();
-    r.bound = max(sh.bound, kKeyLowest + 1);
-  }
+  if (t0 == 0) r.bound = max(bound_of(sh, mine, n), kKeyLowest + 1);
+  // ---- vectors with a logit that reaches the bound, as they are.  (Their logits taken out here, by a lane or by eight of them, kept some warps
+  // for 500 cycles each while the others waited at the next barrier: [64, 8, 152064] 60 us, without any collecting 46.)
   if (__any_sync(0xFFFFFFFFu, mine >= r.bound)) {
 #pragma unroll
-    for (int i = 0; i < kVecs; ++i) {
-      const uint32_t who = __ballot_sync(0xFFFFFFFFu, top_of(most[i]) >= r.bound);
-      if (who && !collect_vectors(sh, x[i], who, c.first_token + 8 * (t0 + i * kThreads + (tid & ~31)), r.bound)) r.crowded = true;
-    }
+    for (int i = 0; i < kVecs; ++i)
+      if (top_of(most[i]) >= r.bound) {
+        const int at = atomicAdd(&sh.n_vec, 1);
+        if (at < kVecList) {
+          sh.vec[at] = x[i];
+          sh.token[at] = c.first_token + 8 * (t0 + i * kThreads + tid);
+        }
+      }
   }
   load_tile(c, t0 + 2 * kTileVecs, x);
 }
 
-// After the kCheck tiles from t0 on (or those that were left): the list keeps its n best where it is filling up.  With every tile followed by
-// a barrier the warps waited for those that collect.
-__device__ __forceinline__ void check_list(BeamShared& sh, const Chunk& c, int n, int t0, Running& r) {
-  if (__syncthreads_or(r.crowded)) {
-    int count = sh.n_list;
+// After the kCheck tiles from t0 on (or those that were left): the collected vectors' logits go to the list, which keeps its n best
+// where it is filling up, and the bound rises to what all tiles so far allow.
+__device__ __forceinline__ void take_stock(BeamShared& sh, const Chunk& c, int n, int t0, Running& r) {
+  const int tid = threadIdx.x;
+  __syncthreads();
+  const int vecs = sh.n_vec;
+  if (vecs <= kVecList) {
+    const uint16_t* x = reinterpret_cast<const uint16_t*>(sh.vec);
+    for (int i = tid; i < 8 * vecs; i += kThreads) {
+      const uint32_t key = ordered(x[i]);
+      if (key >= r.bound) collect(sh, key, sh.token[i >> 3] + (i & 7));
+    }
+  }
+  r.bound = max(r.bound, bound_of(sh, ordered(__float_as_uint(r.m) >> 16), n));  // (barriers inside)
+  int count = sh.n_list;
+  if (vecs > kVecList || count > kListFull) {
     __syncthreads();
-    if (count > kList) count = exact_tiles(sh, c, t0, n);
+    if (vecs > kVecList || count > kList) count = exact_tiles(sh, c, t0, min(count, kList), n);
     cut_down(sh, count, n);
     r.bound = max(r.bound, static_cast<uint32_t>(sh.top[n - 1] >> 32));
-    r.crowded = false;
   }
+  if (tid == 0) sh.n_vec = 0;
+  __syncthreads();
 }
 
-__global__ void __launch_bounds__(kThreads, 2) beam_kernel(const BeamArgs a) {
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) beam_kernel(const BeamArgs a) {
   extern __shared__ __align__(16) uint8_t smem_raw[];
   BeamShared& sh = *reinterpret_cast<BeamShared*>(smem_raw);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -479,14 +482,14 @@ __global__ void __launch_bounds__(kThreads, 2) beam_kernel(const BeamArgs a) {
   c.hi = c.lo + static_cast<int>(e1 - e0);
   c.vecs = (c.hi + 7) >> 3;
   c.first_token = static_cast<uint32_t>((e0 & ~7ll) - row0);
-  if (tid == 0) sh.n_list = 0;
+  if (tid == 0) sh.n_list = sh.n_vec = 0;
   __syncthreads();
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   // a beam that has ended, or that has no score, offers nothing of its logits: they are not read
   if ((a.done && a.done[row] != 0) || a.scores[row] == -INFINITY) c.vecs = 0;
 
-  Running r{-INFINITY, 0.0f, 0, false, false};
+  Running r{-INFINITY, 0.0f, 0, false};
   if (c.vecs > 0) {  // two tiles under way
     uint4 x[kVecs], y[kVecs];
     load_tile(c, 0, x);
@@ -497,7 +500,7 @@ __global__ void __launch_bounds__(kThreads, 2) beam_kernel(const BeamArgs a) {
       take_tile(sh, c, a.n, t0, x, r);
       if (t0 + kTileVecs < c.vecs) take_tile(sh, c, a.n, t0 + kTileVecs, y, r);
       if (t0 / kTileVecs % kCheck == kCheck - 2 || t0 + 2 * kTileVecs >= c.vecs)
-        check_list(sh, c, a.n, t0 / (kCheck * kTileVecs) * (kCheck * kTileVecs), r);
+        take_stock(sh, c, a.n, t0 / (kCheck * kTileVecs) * (kCheck * kTileVecs), r);
     }
   }
   // ---- the CTA's maximum and sum
@@ -540,13 +543,13 @@ struct BeamPlan {
   size_t stats, offers, total;
 };
 
-// Chunks of a row: as many as are resident at once, of 4096 logits at least; at most a list a thread in the merge.  (More of them cost
-// the merge and their own beginnings and ends: [16, 4, 128256] 20 us with four to a row, 29 with nine, 47 with nineteen.)
+// Chunks of a row: as many as there are SMs, of 4096 logits at least; at most a list a thread in the merge.  (More of them cost the merge
+// and their own beginnings and ends: [16, 4, 128256], 16 MB, that come from memory: 21.6 us with two to a row, 23.7 with four.)
 bool beam_plan(int64_t B, int64_t K, int64_t V, int64_t n, BeamPlan& p) {
   if (B < 1 || K < 1 || K > kMaxBeams || V < 2 || V > QSPEC_MAX_V || n < 1 || n > kMaxN || n > K * V || B > 65535 ||
       B * K * V >= (int64_t(1) << 40))
     return false;
-  int64_t c = kCtasPerSm * num_sms() / (B * K);
+  int64_t c = num_sms() / (B * K);
   const int64_t most = (V + 4095) / 4096;
   if (c > most) c = most;
   if (c < 1) c = 1;
