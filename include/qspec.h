@@ -539,7 +539,7 @@ typedef struct {
  *                   quantised again: code = e4m3(code * 2^(old - new))
  *     code = e4m3(x * 2^-exp), round to nearest even, saturating
  * Dropping rejected tokens of a chain needs no call: use a smaller kv_len next time.  The accepted path of a tree is no
- * prefix of what was appended: append its tokens' keys and values again, at the kv_len of the path.  A page's scale does
+ * prefix of what was appended: qspec_kv_compact moves it there (or append its tokens' keys and values again).  A page's scale does
  * not shrink until the page is begun again, so tokens that were dropped leave a mark: where they raised the scale, the
  * codes of the page's other tokens have been rounded again (those alone that fell below e4m3's normal range change).
  * A non-finite key or value is stored as 0 and makes the next
@@ -614,8 +614,9 @@ qspec_status qspec_kv_attention(const qspec_kv_cache* cache, const qspec_kv_batc
  *          the next call, of any shape that it is large enough for; calls that can overlap need one each
  *   1 <= beams <= QSPEC_BEAM_MAX_BEAMS, 1 <= n <= min(QSPEC_BEAM_MAX_N, beams * V), 2 <= V <= 2^24, B <= 65535,
  *   B*beams*V < 2^40; the other arrays 4-byte aligned
- * Sums of exponentials are fp32 by trees of at most 2^15 terms and fp64 beyond, log probabilities and comparisons fp64, score is
- * rounded to fp32 once; so two candidates of different beams can change places only where S is equal to about 1e-7.
+ * Sums of exponentials are fp32, by trees within 16384 logits and one addition for each 16384 more (together within
+ * (25 + V / 16384) * 2^-24), their logarithms are within 2^-24, log probabilities and comparisons are fp64 and score is rounded to fp32
+ * once; so two candidates of different beams can change places only where S is as near as that.
  * A beam with a NaN or +inf among its logits, a score that is NaN or +inf, or a weight that is not positive and finite offers
  * nothing and makes the next qspec_check_status return QSPEC_ERR_INVALID_ARG.
  */
