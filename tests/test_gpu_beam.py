@@ -203,3 +203,16 @@ def test_a_workspace_serves_smaller_shapes_too():
         x, scores, _ = inputs(B + V, B, K, V)
         check(call(q, x, scores, n, ws=ws), x, scores, n)
     q.qspec_check_status()
+
+
+@pytest.mark.parametrize("m", [300, 700, 1500, 5000, 20000, 152064])
+@pytest.mark.parametrize("rising", [True, False])
+@pytest.mark.parametrize("n", [1, 8, 64])
+def test_ever_better_logits(m, rising, n):
+    """m logits that rise (or fall) along the row, the rest below them: later ones pass every bound that the earlier ones gave."""
+    V = 152064
+    x, scores, g = inputs(31 + m, 1, 1, V, 0.5)
+    at = torch.randperm(V, generator=g)[:m].sort().values
+    ramp = torch.linspace(8, 40, m)
+    x[0, 0, at.to(DEV)] = (ramp if rising else ramp.flip(0)).to(torch.bfloat16).to(DEV)
+    check(call(lib(), x, scores, n), x, scores, n)
