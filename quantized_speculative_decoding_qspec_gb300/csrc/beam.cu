@@ -6,8 +6,8 @@
 // streams a part of a row through registers, a tile of 16384 at a time, two tiles under way.  A thread keeps its own maximum and sum of
 // exponentials; the maxima give a lower bound of the n-th largest logit, from the first tile on and better with every look, and the few
 // vectors that reach it are collected in shared memory.  The last CTA of a sequence (atomic ticket) merges the offers.
-// [64, 8, 152064]: 49 us, 3.2 TB/s (a tile of 32768 to a CTA, selected and handed over before the next CTA began: 102); [16, 4, 128256] 14,
-// [1, 4, 32000] 8.6.  Loads and maxima alone take 40 of the 49 (512 rows go in two rounds on 304 places); the smaller ones are a chain of
+// [64, 8, 152064]: 47 us, 3.3 TB/s (a tile of 32768 to a CTA, selected and handed over before the next CTA began: 102); [16, 4, 128256] 14,
+// [1, 4, 32000] 8.6.  Loads and maxima alone take 40 of the 47 (512 rows go in two rounds on 304 places); the smaller ones are a chain of
 // latencies: the first tile 2 us, its bound 0.5, the list 1.5, the ticket 1, the merge 4.
 #include <math.h>
 
@@ -269,8 +269,14 @@ struct Chunk {
   uint32_t first_token;  // of place 0 (wraps below a row's first)
 };
 
-// The thread's vectors of the tile at t0; -inf outside the chunk.
+// The thread's vectors of the tile at t0; -inf outside the chunk.  (Tiles that lie wholly in it apart: [64, 8, 152064] 48.7 -> 46.8 us.)
 __device__ __forceinline__ void load_tile(const Chunk& c, int t0, uint4 (&x)[kVecs]) {
+  if (8 * t0 >= c.lo && 8 * (t0 + kTileVecs) <= c.hi) {
+    const uint4* at = reinterpret_cast<const uint4*>(c.from) + t0 + threadIdx.x;
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) x[i] = ld_stream_v4(at + i * kThreads);
+    return;
+  }
 #pragma unroll
   for (int i = 0; i < kVecs; ++i) {
     const int v = t0 + i * kThreads + threadIdx.x;
