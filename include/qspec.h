@@ -614,8 +614,8 @@ qspec_status qspec_kv_attention(const qspec_kv_cache* cache, const qspec_kv_batc
  *          the next call, of any shape that it is large enough for; calls that can overlap need one each
  *   1 <= beams <= QSPEC_BEAM_MAX_BEAMS, 1 <= n <= min(QSPEC_BEAM_MAX_N, beams * V), 2 <= V <= 2^24, B <= 65535,
  *   B*beams*V < 2^40; the other arrays 4-byte aligned
- * Sums of exponentials are fp32, by trees within 16384 logits and one addition for each 16384 more (together within
- * (25 + V / 16384) * 2^-24), their logarithms are within 2^-24, log probabilities and comparisons are fp64 and score is rounded to fp32
+ * Sums of exponentials are fp32, by trees within 8192 logits and one addition for each 8192 more (together within
+ * (25 + V / 8192) * 2^-24), their logarithms are within 2^-24, log probabilities and comparisons are fp64 and score is rounded to fp32
  * once; so two candidates of different beams can change places only where S is as near as that.
  * A beam with a NaN or +inf among its logits, a score that is NaN or +inf, or a weight that is not positive and finite offers
  * nothing and makes the next qspec_check_status return QSPEC_ERR_INVALID_ARG.

@@ -3,12 +3,13 @@
 //     S(k, v) = score[k] + (logit[k, v] - lse[k]),   lse[k] = ln sum_v exp(logit[k, v])
 // Within a beam the order is that of its logits (bf16: ties are common, and go to the lowest token), so each beam offers its n
 // largest logits, and the beams' offers are ordered by S (times a weight).  One pass over the logits bounds it: a CTA
-// streams a part of a row through registers, a tile of 16384 at a time, two tiles under way.  A thread keeps its own maximum and sum of
+// streams a part of a row through registers, a tile of 8192 at a time, two tiles under way.  A thread keeps its own maximum and sum of
 // exponentials; the maxima give a lower bound of the n-th largest logit, from the first tile on and better with every look, and the few
 // vectors that reach it are collected in shared memory.  The last CTA of a sequence (atomic ticket) merges the offers.
-// [64, 8, 152064]: 47 us, 3.3 TB/s (a tile of 32768 to a CTA, selected and handed over before the next CTA began: 102); [16, 4, 128256] 14,
-// [1, 4, 32000] 8.6.  Loads and maxima alone take 40 of the 47 (512 rows go in two rounds on 304 places); the smaller ones are a chain of
-// latencies: the first tile 2 us, its bound 0.5, the list 1.5, the ticket 1, the merge 4.
+// [64, 8, 152064]: 39 us, 4.0 TB/s; [16, 4, 128256] 14, [1, 4, 32000] 7.9.  512 blocks of 256 threads are resident at once, three or four
+// to an SM, and wait at their barriers in turn (two of 512 threads: 47 us; eight of 128: 57; a tile of 32768 to a CTA, selected and
+// handed over before the next CTA began: 102).  The smaller ones are a chain of latencies: the first tile 2 us, its bound 0.5, the list 1.5,
+// the ticket 1, the merge 4.
 #include <math.h>
 
 #include "kv_internal.h"
@@ -16,14 +17,14 @@
 namespace qspec {
 namespace {
 
-constexpr int kThreads = 512, kWarps = kThreads / 32;
+constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kVecs = 4;                          // 16-byte loads in flight a thread
-constexpr int kTileVecs = kThreads * kVecs;       // 16384 logits
+constexpr int kTileVecs = kThreads * kVecs;       // 8192 logits
 constexpr int kList = 1024;                       // logits collected at most; tiles that bring more: see below
 constexpr int kListFull = 512;                    // from here on they are cut down to the n best
 constexpr int kVecList = 512;                     // vectors collected between looks at them
 constexpr int kCheck = 4;                         // tiles between looks
-constexpr int kCtasPerSm = 2;                     // resident
+constexpr int kCtasPerSm = 4;                     // resident
 constexpr int kMaxN = QSPEC_BEAM_MAX_N, kMaxBeams = QSPEC_BEAM_MAX_BEAMS;
 constexpr int kMaxLists = kThreads;               // (beam, chunk) pairs of a sequence: a thread each in the merge
 constexpr uint32_t kLowest = 0xFF80FF80u;         // two bf16 -inf
@@ -269,7 +270,7 @@ struct Chunk {
   uint32_t first_token;  // of place 0 (wraps below a row's first)
 };
 
-// The thread's vectors of the tile at t0; -inf outside the chunk.  (Tiles that lie wholly in it apart: [64, 8, 152064] 48.7 -> 46.8 us.)
+// The thread's vectors of the tile at t0; -inf outside the chunk.  (Tiles that lie wholly in it apart: [64, 8, 152064] 48.7 -> 46.8 us, with 512 threads.)
 __device__ __forceinline__ void load_tile(const Chunk& c, int t0, uint4 (&x)[kVecs]) {
   if (8 * t0 >= c.lo && 8 * (t0 + kTileVecs) <= c.hi) {
     const uint4* at = reinterpret_cast<const uint4*>(c.from) + t0 + threadIdx.x;
@@ -381,7 +382,8 @@ struct Running {
 };
 
 // The n-th largest of 64 groups of threads' maxima: a bound of the n-th largest logit that they have seen.  A warp finds the places of
-// four, with eight lanes to each (all of them in every warp: 1.5 us, the warps' issue slots).  All threads; two barriers.
+// four, with eight lanes to each (all of them in every warp: 1.5 us, the warps' issue slots).  All threads; two barriers,
+// and the list of vectors, which all have read, is empty.
 __device__ __forceinline__ uint32_t bound_of(BeamShared& sh, uint32_t mine, int n) {
   const int tid = threadIdx.x;
   constexpr int kSize = kThreads / kMaxN;
@@ -398,6 +400,7 @@ __device__ __forceinline__ uint32_t bound_of(BeamShared& sh, uint32_t mine, int 
 #pragma unroll
   for (int off = kLanes / 2; off >= 1; off >>= 1) before += __shfl_xor_sync(0xFFFFFFFFu, before, off);
   if (before == n - 1) sh.bound = v >> 6;
+  if (tid == 0) sh.n_vec = 0;
   __syncthreads();
   return sh.bound;
 }
@@ -473,8 +476,6 @@ __device__ __forceinline__ void take_stock(BeamShared& sh, const Chunk& c, int n
     cut_down(sh, count, n);
     r.bound = max(r.bound, static_cast<uint32_t>(sh.top[n - 1] >> 32));
   }
-  if (tid == 0) sh.n_vec = 0;
-  __syncthreads();
 }
 
 __global__ void __launch_bounds__(kThreads, kCtasPerSm) beam_kernel(const BeamArgs a) {
@@ -549,13 +550,13 @@ struct BeamPlan {
   size_t stats, offers, total;
 };
 
-// Chunks of a row: as many as there are SMs, of 4096 logits at least; at most a list a thread in the merge.  (More of them cost the merge
-// and their own beginnings and ends: [16, 4, 128256], 16 MB, that come from memory: 21.6 us with two to a row, 23.7 with four.)
+// Chunks of a row: two to an SM, of 4096 logits at least; at most a list a thread in the merge.  (More of them cost the merge
+// and their own beginnings and ends: [16, 4, 128256] 14.0 us with four to a row, 15.2 with nine, 15.0 with two.)
 bool beam_plan(int64_t B, int64_t K, int64_t V, int64_t n, BeamPlan& p) {
   if (B < 1 || K < 1 || K > kMaxBeams || V < 2 || V > QSPEC_MAX_V || n < 1 || n > kMaxN || n > K * V || B > 65535 ||
       B * K * V >= (int64_t(1) << 40))
     return false;
-  int64_t c = num_sms() / (B * K);
+  int64_t c = 2 * num_sms() / (B * K);
   const int64_t most = (V + 4095) / 4096;
   if (c > most) c = most;
   if (c < 1) c = 1;
