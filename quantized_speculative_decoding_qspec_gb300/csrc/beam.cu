@@ -94,10 +94,13 @@ __device__ __forceinline__ unsigned long long ordered64(double x) {
 struct BeamShared {
   union {
     unsigned long long list[kList + kMaxN];
-    unsigned long long head[kMaxLists];
+    struct {
+      unsigned long long head[kMaxLists];
+      uint32_t head_order[kMaxLists];
+    };
   };
   unsigned long long pair_key[kMaxN * (kMaxN + 1) / 2];
-  uint16_t pair_order[kMaxN * (kMaxN + 1) / 2];
+  uint32_t pair_order[kMaxN * (kMaxN + 1) / 2];
   int best_list[kMaxN];
   unsigned long long top[kMaxN];
   uint32_t group[64];
@@ -115,6 +118,7 @@ struct BeamShared {
 
 struct Candidate {
   unsigned long long key;  // of S times the weight
+  uint32_t order;          // among equal keys, lowest first: by beam, logit (largest first), place in the row
   double S;
   int row, tok;
 };
@@ -184,8 +188,14 @@ __device__ __noinline__ void merge(const BeamArgs& a, BeamShared& sh, int b) {
 
   // ---- the best n lists by their first offers, in order: the r-th can give n - r of the n best.  (Choosing the n best one after
   // the other by reductions over the lists took 5 to 7 us for eight.)
+  // S is fp64, so different logits of a beam can have equal ones (far scores; logits much nearer than the logarithm's size): a chunk's
+  // offers are in their order, those of different chunks are put in it by the logit.
+  const int at_bits = 6 + (32 - __clz(a.chunks - 1));
+  static_assert(kMaxN <= 1 << 6 && kMaxLists <= 1 << 8 && kMaxBeams <= 1 << 5, "beam and chunk have 9 bits, logit and place 22");
   auto candidate = [&](int list, int e, unsigned long long offer, Candidate& c) {  // false: no offer
     const int k = list / a.chunks;
+    c.order = static_cast<uint32_t>(k) << (at_bits + 16) | (0xFFFFu - static_cast<uint32_t>(offer >> 32)) << at_bits |
+              static_cast<uint32_t>(list - k * a.chunks) << 6 | e;
     const double lse = sh.lse[k];
     if (lse != lse) return false;
     c.S = sh.row_score[k];
@@ -201,9 +211,11 @@ __device__ __noinline__ void merge(const BeamArgs& a, BeamShared& sh, int b) {
     c.key = ordered64(a.weights ? c.S * sh.row_weight[k] : c.S);
     return true;
   };
-  Candidate c;
+  Candidate c{};
   const unsigned long long head = tid < lists && candidate(tid, 0, first, c) ? c.key : 0;
+  const uint32_t head_order = c.order;
   sh.head[tid] = head;
+  sh.head_order[tid] = head_order;
   if (tid < n) sh.best_list[tid] = -1;
   if (tid == 0) sh.count = 0;
   __syncthreads();
@@ -212,7 +224,8 @@ __device__ __noinline__ void merge(const BeamArgs& a, BeamShared& sh, int b) {
 #pragma unroll 4
     for (int j = 0; j < lists; ++j) {
       const unsigned long long x = sh.head[j];
-      place += (x > head) | ((x == head) & (j < tid));
+      const uint32_t o = sh.head_order[j];
+      place += (x > head) | ((x == head) & (o < head_order));
     }
     if (place < n) sh.best_list[place] = tid;
   }
@@ -230,20 +243,19 @@ __device__ __noinline__ void merge(const BeamArgs& a, BeamShared& sh, int b) {
     const bool real = pair(p, list, e);
     if (p == tid) mine = c;
     sh.pair_key[p] = real ? c.key : 0;
-    sh.pair_order[p] = static_cast<uint16_t>(list << 6 | e);
+    sh.pair_order[p] = c.order;
     if (real) atomicAdd(&sh.count, 1);
   }
-  static_assert(kMaxLists <= 1 << 9 && kMaxN <= 1 << 6, "a list and a place in it have 16 bits");
   __syncthreads();
   for (int p = tid; p < pairs; p += kThreads) {
     const unsigned long long key = sh.pair_key[p];
-    const uint16_t order = sh.pair_order[p];
+    const uint32_t order = sh.pair_order[p];
     if (key == 0) continue;
     int place = 0;
 #pragma unroll 4
     for (int j = 0; j < pairs; ++j) {  // (both reads of a step at once: with the second behind a branch a step took 120 cycles)
       const unsigned long long x = sh.pair_key[j];
-      const uint16_t o = sh.pair_order[j];
+      const uint32_t o = sh.pair_order[j];
       place += (x > key) | ((x == key) & (o < order));
     }
     if (place >= n) continue;
