@@ -611,7 +611,8 @@ qspec_status qspec_kv_attention(const qspec_kv_cache* cache, const qspec_kv_batc
  *   logits [B, beams, V] bf16 (16-byte aligned);  scores [B, beams] fp32;  done [B, beams] int32 or NULL: none;
  *   weights [B, beams] fp32 or NULL: 1;  parent, tok [B, n] int32, score [B, n] fp32 (outputs; not scores itself)
  *   ws, ws_bytes  device workspace, >= qspec_beam_workspace_size(B, beams, V, n), zero-filled before its first use and left ready for
- *          the next call, of any shape that it is large enough for; calls that can overlap need one each
+ *          the next call, of any shape that it is large enough for: of every one that is no larger in any of B, beams, V and n.
+ *          Calls that can overlap need one each
  *   1 <= beams <= QSPEC_BEAM_MAX_BEAMS, 1 <= n <= min(QSPEC_BEAM_MAX_N, beams * V), 2 <= V <= 2^24, B <= 65535,
  *   B*beams*V < 2^40; the other arrays 4-byte aligned
  * Sums of exponentials are fp32, by trees within 8192 logits and one addition for each 8192 more (together within

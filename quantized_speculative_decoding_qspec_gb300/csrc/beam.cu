@@ -559,7 +559,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) beam_kernel(const BeamAr
 
 struct BeamPlan {
   int chunks, chunk_len;
-  size_t stats, offers, total;
+  size_t stats, offers;  // where they lie
+  size_t total;          // what this shape and every smaller one need
 };
 
 // Chunks of a row: two to an SM, of 4096 logits at least; at most a list a thread in the merge.  (More of them cost the merge
@@ -568,17 +569,21 @@ bool beam_plan(int64_t B, int64_t K, int64_t V, int64_t n, BeamPlan& p) {
   if (B < 1 || K < 1 || K > kMaxBeams || V < 2 || V > QSPEC_MAX_V || n < 1 || n > kMaxN || n > K * V || B > 65535 ||
       B * K * V >= (int64_t(1) << 40))
     return false;
-  int64_t c = 2 * num_sms() / (B * K);
-  const int64_t most = (V + 4095) / 4096;
+  const int64_t places = 2 * num_sms(), most = (V + 4095) / 4096;
+  int64_t c = places / (B * K);
   if (c > most) c = most;
   if (c < 1) c = 1;
   if (c > kMaxLists / K) c = kMaxLists / K;
   p.chunk_len = static_cast<int>((V + c - 1) / c);
   p.chunks = static_cast<int>((V + p.chunk_len - 1) / p.chunk_len);
-  const size_t lists = static_cast<size_t>(B) * K * p.chunks;
   p.stats = sizeof(unsigned int) * 65536;  // (tickets of the largest batch: they are where they were for calls of any shape)
-  p.offers = (p.stats + sizeof(float2) * lists + 255) & ~size_t(255);
-  p.total = p.offers + sizeof(unsigned long long) * lists * n;
+  auto offers_at = [&](int64_t lists) { return (p.stats + sizeof(float2) * lists + 255) & ~size_t(255); };
+  p.offers = offers_at(B * K * p.chunks);
+  // Fewer rows have more chunks each, so a smaller batch can have more lists: never more than two to an SM, or one to a row, or one to
+  // 4096 logits of these rows.
+  int64_t lists = B * K * most < places ? B * K * most : places;
+  if (lists < B * K) lists = B * K;
+  p.total = offers_at(lists) + sizeof(unsigned long long) * lists * n;
   return true;
 }
 
