@@ -382,10 +382,10 @@ __device__ __forceinline__ bool walk_next_planned(SharedWalk<kRows, kKeys>* w, P
 }
 
 // The v-th tile that is taken, counted in the order of the segments.
-__device__ __forceinline__ int in_turn(const Plan* plan, int v) {
+__host__ __device__ __forceinline__ int in_turn(const Plan* plan, int v) {
   int u = v - plan->prefix;
-  if (u < 0) return v;
   const int n0 = plan->half0, n1 = plan->half1, both = plan->both;
+  if (u < 0 || n0 + n1 == 0) return v;  // (an item that sees nothing has a tile all the same, which is in no segment)
   if (u < both) return plan->prefix + n0 + u;
   u -= both;
   const int n = n0 + n1;
@@ -396,7 +396,7 @@ __device__ __forceinline__ int in_turn(const Plan* plan, int v) {
 
 // Key tile v of the stream: its segment (or -1), the position of its first key.
 template <int kKeys>
-__device__ __forceinline__ int seg_of(const int4* seg, int count, int v, int& key0) {
+__host__ __device__ __forceinline__ int seg_of(const int4* seg, int count, int v, int& key0) {
   int lo = 0, hi = count;  // the first segment that ends behind v
   while (lo < hi) {
     const int mid = (lo + hi) >> 1;
