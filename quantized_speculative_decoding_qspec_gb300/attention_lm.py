@@ -78,8 +78,20 @@ class AttentionLM:
         return self._linear("out", x + self._linear("o", att.view(T, hq * d), draft_mode), draft_mode)
 
 
+def _take(cache):
+    """The cache's pages are the caller's from now on; what shares them out beside it keeps the token."""
+    cache.claim = claim = object()
+    return claim
+
+
+def _still_has(cache, claim):
+    if getattr(cache, "claim", None) is not claim:
+        raise ValueError("the cache's pages are another serving loop's or beam search's by now")
+
+
 class Server:
-    """B sequences decoded together: gamma drafted tokens and one verify pass an iteration.
+    """B sequences decoded together: gamma drafted tokens and one verify pass an iteration.  It takes the model's cache: a serving
+    loop or beam search that had it before makes no step any more.
 
     penalties: (repetition, frequency, presence) of every sequence, or None; allowed: int32 [ceil(V/32)]
     words of the tokens that may be emitted, or None.  A prompt has 1 to max_len tokens; step() refuses once a
@@ -111,6 +123,7 @@ class Server:
         self.vws = q.new_verify_workspace(B, gamma, model.V, device=dev)
         self.n, self.out = torch.zeros(B, **i32), torch.zeros(B, gamma + 1, **i32)
         self.rows = torch.arange(B, device=dev)
+        self.claim = _take(model.cache)
         self._prefill(prompts)
 
     def _batch(self, n):
@@ -146,6 +159,7 @@ class Server:
             if self.longest > self.max_len:
                 raise ValueError(f"a sequence has {self.longest} positions in the cache, beyond max_len {self.max_len}")
         self.longest += gamma + 1
+        _still_has(m.cache, self.claim)
         base, length = self.kv_len.clone(), self.hist_len.clone()  # the last token of hist is not in the cache yet
         tokens = torch.empty(B, gamma + 1, dtype=torch.int32, device=m.device)
         tokens[:, 0] = self.hist[self.rows, (length - 1).long()]
@@ -174,7 +188,8 @@ class Beams:
 
     end_tok ends a beam, which then stays among the best by its score alone; beams compare by their score divided by the length
     of what they added to the power of `length_power`.  A prompt has 1 to max_len tokens; max_new tokens are added at most.
-    tokens [B, beams, max_new] and scores [B, beams] are best first.
+    tokens [B, beams, max_new] and scores [B, beams] are best first.  The search takes the model's cache, with all its pages free:
+    a serving loop or beam search that had it before makes no step any more.
     """
 
     def __init__(self, model, prompts, beams=4, max_len=256, max_new=64, end_tok=0, length_power=0.0):
@@ -206,7 +221,8 @@ class Beams:
         self.bws = q.new_beam_workspace(B, K, model.V, K, device=dev)
         self.cu = torch.arange(B * K + 1, **i32)
         self.prefixes = q.KVPrefixes(torch.arange(0, B * K + 1, K, **i32), self.prompt_len, K)
-        self.steps = 0
+        self.steps, self.closed = 0, False
+        self.claim = _take(model.cache)
         self._prefill(prompts)
 
     def _pages(self, rows, parent, keep, need):
@@ -252,8 +268,11 @@ class Beams:
 
     def step(self):
         """One token more for every beam that has not ended."""
+        if self.closed:
+            raise ValueError("the search is closed")
         if self.steps >= self.max_new:
             raise ValueError(f"the beams have {self.max_new} tokens")
+        _still_has(self.model.cache, self.claim)
         B, K, V = self.B, self.K, self.model.V
         batch = q.KVBatch(self.cu, self.length, self.tables[0], 1)
         logits = self.model.forward(self.tok.view(-1), batch, draft_mode=False, prefixes=self.prefixes).view(B, K, V)
@@ -265,7 +284,10 @@ class Beams:
         self._fork(B * K, self.length)
 
     def close(self):
-        """Gives all pages back."""
+        """Gives all pages back; no step can follow."""
+        if self.closed:
+            return
+        self.closed = True
         none = self.length[:0]
         q.qspec_kv_pages(self.tables[0], self.length, none, none, self.refs, self.model.cache.page, self.tables[1][:0], self.refs, none,
                          none, none, self.left)
