@@ -225,11 +225,11 @@ class Beams:
         self.claim = _take(model.cache)
         self._prefill(prompts)
 
-    def _pages(self, rows, parent, keep, need):
-        """The next page tables from the first `rows` rows of the present ones, and the copies that they ask for."""
+    def _pages(self, lengths, parent, keep, need):
+        """The next page tables from the present ones, whose first rows hold `lengths` positions, and the copies that they ask for."""
         old, new = self.tables
         src, dst, size = self.copies
-        q.qspec_kv_pages(old[:rows], self.length[:rows], keep, need, self.refs, self.model.cache.page, new[:keep.numel()], self.refs,
+        q.qspec_kv_pages(old[:lengths.numel()], lengths, keep, need, self.refs, self.model.cache.page, new[:keep.numel()], self.refs,
                          src[:keep.numel()], dst[:keep.numel()], size[:keep.numel()], self.left, parent=parent)
         q.qspec_kv_copy_pages(self.model.cache, src[:keep.numel()], dst[:keep.numel()], lengths=size[:keep.numel()])
         self.tables.reverse()
@@ -239,29 +239,29 @@ class Beams:
         ends = torch.tensor([len(p) for p in prompts]).cumsum(0)
         cu = torch.cat([torch.zeros(1, dtype=torch.int64), ends]).to(torch.int32).to(dev)
         none = torch.full((B,), -1, dtype=torch.int32, device=dev)
-        self._pages(0, none, torch.zeros_like(none), self.prompt_len)
+        self._pages(none[:0], none, torch.zeros_like(none), self.prompt_len)
         tok = torch.tensor([t for p in prompts for t in p], dtype=torch.int32, device=dev)
         batch = q.KVBatch(cu, self.prompt_len, self.tables[0][:B], max(len(p) for p in prompts))
         logits = self.model.forward(tok, batch, draft_mode=False)
         last = logits[(ends - 1).to(dev)].view(B, 1, -1).contiguous()
         ws = q.new_beam_workspace(B, 1, self.model.V, K, device=dev)
         q.qspec_beam_select(last, torch.zeros(B, 1, device=dev), self.parent, self.tok, self.score, ws)
-        lengths, self.length = self.length, self.prompt_len            # the old rows are the prompts
-        self._fork(B, lengths)
+        self._fork(self.prompt_len)                                    # the old rows are the prompts
 
-    def _fork(self, rows, lengths):
-        """The chosen beams go on from their parents' pages (of the first `rows` rows), with room for one token more."""
+    def _fork(self, lengths):
+        """The chosen beams go on from their parents' pages (the first rows, of these lengths), with room for one token more.  A beam that
+        nothing continues (parent -1: the prompt's logits are not finite) has no pages and no positions, so nothing is written for it."""
         parent, n = self.parent.view(-1), self.steps
-        keep = lengths.contiguous()
-        self._pages(rows, parent, keep, keep + 1)
-        self.length = keep + 1
+        at, lives = parent.long().clamp(min=0), parent >= 0
+        keep = torch.where(lives, lengths[at], 0)
+        self.length = keep + lives.to(torch.int32)
+        self._pages(lengths, parent, keep, self.length)
         if n > 0:                                                      # (parents are rows of the beams before)
             moved = torch.empty_like(self.tokens.view(-1, self.max_new))
-            q.qspec_gather_rows(self.tokens.view(-1, self.max_new), parent, moved)
-            self.tokens = moved.view_as(self.tokens)
-            at = parent.long()
+            q.qspec_gather_rows(self.tokens.view(-1, self.max_new), parent.clamp(min=0), moved)
+            self.tokens = torch.where(lives[:, None], moved, -1).view_as(self.tokens)
             self.done, self.added = self.done.view(-1)[at].view_as(self.done), self.added.view(-1)[at].view_as(self.added)
-        self.tokens[:, :, n] = torch.where(self.done != 0, torch.full_like(self.tok, -1), self.tok)
+        self.tokens[:, :, n] = torch.where(self.done != 0, -1, self.tok)
         self.added += (self.done == 0).to(torch.int32)
         self.done |= (self.tok == self.end_tok).to(torch.int32)
         self.steps += 1
@@ -281,7 +281,7 @@ class Beams:
         parent, tok, score = torch.empty_like(self.parent), torch.empty_like(self.tok), torch.empty_like(self.score)
         q.qspec_beam_select(logits, self.score, parent, tok, score, self.bws, done=self.done, end_tok=self.end_tok, weights=weights)
         self.parent, self.tok, self.score = parent, tok, score
-        self._fork(B * K, self.length)
+        self._fork(self.length)
 
     def close(self):
         """Gives all pages back; no step can follow."""
