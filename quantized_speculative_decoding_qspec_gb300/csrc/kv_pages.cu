@@ -578,10 +578,11 @@ extern "C" qspec_status qspec_kv_pages(const int32_t* pages, const int32_t* room
 
 extern "C" qspec_status qspec_kv_copy_pages(const qspec_kv_cache* caches, int32_t n_caches, const int32_t* src, const int32_t* dst,
                                             const int32_t* len, int32_t n, qspec_stream_t stream) {
-  if (!src || !dst || n <= 0) return QSPEC_ERR_INVALID_ARG;
+  const bool none = n == 0 && !src && !dst && !len;
+  if (!none && (!src || !dst || n <= 0)) return QSPEC_ERR_INVALID_ARG;
   CopyArgs a;
   const qspec_status st = check_layers(caches, n_caches, a.l);
-  if (st != QSPEC_OK) return st;
+  if (st != QSPEC_OK || none) return st;
   if (!aligned4(src) || !aligned4(dst) || !aligned4(len)) return QSPEC_ERR_MISALIGNED;
   a.src = src;
   a.dst = dst;

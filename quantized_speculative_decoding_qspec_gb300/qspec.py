@@ -754,6 +754,8 @@ def qspec_kv_copy_pages(caches, src, dst, lengths=None, stream=None):
     _dt(src, _int32, "src"); _dt(dst, _int32, "dst"); _dt(lengths, _int32, "lengths")
     n = src.numel()
     _need(dst, n, "dst"); _need(lengths, n, "lengths")
+    if n == 0:                     # (the last rows have ended: no pairs, no arrays)
+        src = dst = lengths = None
     ref, layers, _ = _layers(caches)
     _check("qspec_kv_copy_pages", load().qspec_kv_copy_pages(ref, layers, _ptr(src), _ptr(dst), _ptr(lengths), n, _stream(stream)))
 
