@@ -609,7 +609,8 @@ qspec_status qspec_kv_attention(const qspec_kv_cache* cache, const qspec_kv_batc
  * offer nothing (the logits of such a beam and of a finished one are not read).
  *
  *   logits [B, beams, V] bf16 (16-byte aligned);  scores [B, beams] fp32;  done [B, beams] int32 or NULL: none;
- *   weights [B, beams] fp32 or NULL: 1;  parent, tok [B, n] int32, score [B, n] fp32 (outputs; not scores itself)
+ *   weights [B, beams] fp32 or NULL: 1;  parent, tok [B, n] int32, score [B, n] fp32 (outputs;
+ *          none of them over another array)
  *   ws, ws_bytes  device workspace, >= qspec_beam_workspace_size(B, beams, V, n), zero-filled before its first use and left ready for
  *          the next call, of any shape that it is large enough for: of every one that is no larger in any of B, beams, V and n.
  *          Calls that can overlap need one each
@@ -646,7 +647,8 @@ qspec_status qspec_beam_select(const uint16_t* logits, const float* scores, cons
  *   (negative: from none, with keep[r] = 0);  keep, need [new_rows]: 0 <= keep[r] <= room[parent[r]], keep[r] <= need[r];
  *   new_pages [new_rows, new_max_pages] (not the old table: entries beyond need[r] are left as they are);  refs, new_refs
  *   [n_pages], which may be the same array;  copy_src, copy_dst, copy_len [new_rows];  left [1].  new_rows may be 0 (its arrays
- *   NULL then: all rows end).  All int32, DEVICE, 4-byte aligned (refs and new_refs 16).
+ *   NULL then: all rows end).  All int32, DEVICE, 4-byte aligned (refs and new_refs 16); but for refs in place no output
+ *   overlaps another array.
  *   page is 16, 32, 64 or 128; rows and new_rows at most QSPEC_KV_MAX_B; max_pages * page <= 2^30
  * A row whose numbers are out of range gets no pages (an old one: releases none), an id outside [0, n_pages) is passed on without
  * being counted, and either of them or a count below zero makes the next qspec_check_status return QSPEC_ERR_INVALID_ARG.

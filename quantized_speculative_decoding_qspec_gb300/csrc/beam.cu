@@ -609,7 +609,9 @@ extern "C" qspec_status qspec_beam_select(const uint16_t* logits, const float* s
       !aligned4(score) || !aligned16(ws))
     return QSPEC_ERR_MISALIGNED;
   if (!ws || ws_bytes < p.total) return QSPEC_ERR_WORKSPACE;
-  if (score < scores + static_cast<int64_t>(B) * beams && scores < score + static_cast<int64_t>(B) * n) return QSPEC_ERR_INVALID_ARG;
+  const int64_t rows = static_cast<int64_t>(B) * beams, best = static_cast<int64_t>(B) * n;
+  const Words in[] = {{scores, rows}, {done, rows}, {weights, rows}}, out[] = {{parent, best}, {tok, best}, {score, best}};
+  if (outputs_overlap(out, 3, in, 3)) return QSPEC_ERR_INVALID_ARG;  // (a sequence's last block writes while others' read)
   char* w = static_cast<char*>(ws);
   BeamArgs a{logits, scores, done, weights, parent, tok, score, linear_error_word(), reinterpret_cast<unsigned int*>(w),
              reinterpret_cast<float2*>(w + p.stats), reinterpret_cast<unsigned long long*>(w + p.offers),

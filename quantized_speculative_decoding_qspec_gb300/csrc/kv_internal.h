@@ -71,6 +71,26 @@ __device__ __forceinline__ uint32_t f32_to_e4m3x2(float lo, float hi) {
 // 2^e for |e| <= 126.
 __device__ __forceinline__ float exp2_int(int e) { return __int_as_float((127 + e) << 23); }
 
+// n 32-bit words of memory (p null: none).
+struct Words {
+  const void* p;
+  int64_t n;
+};
+// An output shares a word with an input or another output.
+inline bool outputs_overlap(const Words* out, int n_out, const Words* in, int n_in) {
+  auto meet = [](const Words& x, const Words& y) {
+    const char *a = static_cast<const char*>(x.p), *b = static_cast<const char*>(y.p);
+    return a && b && a < b + 4 * y.n && b < a + 4 * x.n;
+  };
+  for (int i = 0; i < n_out; ++i) {
+    for (int j = 0; j < i; ++j)
+      if (meet(out[i], out[j])) return true;
+    for (int j = 0; j < n_in; ++j)
+      if (meet(out[i], in[j])) return true;
+  }
+  return false;
+}
+
 inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 inline qspec_status check_rotary_plan(const qspec_rotary_plan* p, int32_t dim) {

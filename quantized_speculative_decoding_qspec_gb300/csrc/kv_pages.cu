@@ -554,6 +554,13 @@ extern "C" qspec_status qspec_kv_pages(const int32_t* pages, const int32_t* room
   if (!aligned16(refs) || !aligned16(new_refs) || !aligned4(pages) || !aligned4(room) || !aligned4(parent) || !aligned4(keep) ||
       !aligned4(need) || !aligned4(new_pages) || !aligned4(copy_src) || !aligned4(copy_dst) || !aligned4(copy_len) || !aligned4(left))
     return QSPEC_ERR_MISALIGNED;
+  // no other input is written either, as rows are read again behind the first writes; the counts alone may be in place
+  const Words in[] = {{rows > 0 ? pages : nullptr, static_cast<int64_t>(rows) * max_pages}, {rows > 0 ? room : nullptr, rows},
+                      {new_rows > 0 ? parent : nullptr, new_rows}, {new_rows > 0 ? keep : nullptr, new_rows},
+                      {new_rows > 0 ? need : nullptr, new_rows}, {refs != new_refs ? refs : nullptr, n_pages}};
+  const Words out[] = {{new_refs, n_pages}, {left, 1}, {new_pages, static_cast<int64_t>(new_rows) * new_max_pages}, {copy_src, new_rows},
+                       {copy_dst, new_rows}, {copy_len, new_rows}};
+  if (outputs_overlap(out, new_rows > 0 ? 6 : 2, in, 6)) return QSPEC_ERR_INVALID_ARG;
   PagesArgs a{pages, room, parent, keep, need, refs, new_pages, new_refs, copy_src, copy_dst, copy_len, left, linear_error_word(),
               n_pages, rows, new_rows, rows > 0 ? max_pages : 0, new_rows > 0 ? new_max_pages : 0};
   if (!a.err) return QSPEC_ERR_CUDA;
