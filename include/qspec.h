@@ -616,9 +616,13 @@ qspec_status qspec_kv_attention(const qspec_kv_cache* cache, const qspec_kv_batc
  *          Calls that can overlap need one each
  *   1 <= beams <= QSPEC_BEAM_MAX_BEAMS, 1 <= n <= min(QSPEC_BEAM_MAX_N, beams * V), 2 <= V <= 2^24, B <= 65535,
  *   B*beams*V < 2^40; the other arrays 4-byte aligned
- * Sums of exponentials are fp32, by trees within 8192 logits and one addition for each 8192 more (together within
- * (25 + V / 8192) * 2^-24), their logarithms are within 2^-24, log probabilities and comparisons are fp64 and score is rounded to fp32
- * once; so two candidates of different beams can change places only where S is as near as that.
+ * Sums of exponentials are fp32, of approximate powers: by trees within 8192 logits and one addition for each 8192 more.  In units of
+ * 2^-24 of a sum the additions are within 25 + V / 8192; the terms' exponents within 3 ln V (a term's is off by three of its own
+ * size, which under the weights of a softmax averages ln V at most); their powers, of a relative error below 2^-22, within 20 with
+ * the three joinings, and 5 more for each time that the largest logit that a thread has seen rises (V / 8192 times at most).
+ * Logarithms are within 2^-24, log probabilities and comparisons are fp64 and score is rounded to fp32 once.  Together S is within
+ * 2^-16 for V = 152064, whatever the logits; two candidates of different beams can change places only where their S differ by less
+ * than the two errors, those of one beam never.
  * A beam with a NaN or +inf among its logits, a score that is NaN or +inf, or a weight that is not positive and finite offers
  * nothing and makes the next qspec_check_status return QSPEC_ERR_INVALID_ARG.
  */
@@ -692,9 +696,13 @@ qspec_status qspec_kv_compact(const qspec_kv_cache* caches, int32_t n_caches, co
  * qspec_kv_attention_shared -- qspec_kv_attention for sequences that share a prefix, which is read and multiplied once for all of
  * them.  Group g is the sequences cu_seq[g] .. cu_seq[g+1] - 1; the first len[g] cache positions of all of them hold the same
  * tokens, and are read through the page table of the group's first sequence that has new tokens: entries of pages that lie wholly in the
- * prefix are not read in the others' tables.  (A group of one sequence, or
- * of any sequences with len = 0, is plain attention.)  len[g] may exceed what its sequences have in common with their new tokens
- * taken off: the prefix ends where the new tokens of one of them begin, at the latest.
+ * prefix are not read in the others' tables.  (A group of one sequence, or of any sequences with len = 0, is plain attention.)
+ * len[g] may exceed what its sequences have in common with their new tokens taken off: the prefix ends where the new tokens of one
+ * of them begin, at the latest.
+ * It pays for prefixes of some thousand positions that are longer than what the sequences have alone: its start takes longer than
+ * qspec_kv_attention's, and keys of one sequence take twice as long in groups of more than 32 rows.  With 32 query heads on 8 of 128
+ * it was the quicker one for 128 single tokens with 512 / 4000 positions of their own from 1500 / 4500 shared ones on, for 16 groups of
+ * four single tokens from 1000 and of 16 tokens from 6000, for one group of four from 4000.
  *   cu_seq [n_groups+1] int32, non-decreasing within [0, B];  len [n_groups] int32 (both DEVICE, 4-byte aligned)
  *   max_tok: at least the largest number of new tokens of one group, at most T.  1 <= n_groups <= QSPEC_KV_MAX_GROUPS
  * Arguments, masks, outputs and limits otherwise as for qspec_kv_attention, whose workspace serves both calls.  Sequences of

@@ -6,7 +6,8 @@
 // streams a part of a row through registers, a tile of 8192 at a time, two tiles under way.  A thread keeps its own maximum and sum of
 // exponentials; the maxima give a lower bound of the n-th largest logit, from the first tile on and better with every look, and the few
 // vectors that reach it are collected in shared memory.  The last CTA of a sequence (atomic ticket) merges the offers.
-// [64, 8, 152064]: 39 us, 4.0 TB/s; [16, 4, 128256] 14, [1, 4, 32000] 7.9.  512 blocks of 256 threads are resident at once, three or four
+// [64, 8, 152064]: 40 us for 156 MB, 3.9 TB/s (39 us with one beam in seven finished: 133 MB, 3.4 TB/s); [16, 4, 128256] 14,
+// [1, 4, 32000] 7.9.  512 blocks of 256 threads are resident at once, three or four
 // to an SM, and wait at their barriers in turn (two of 512 threads: 47 us; eight of 128: 57; a tile of 32768 to a CTA, selected and
 // handed over before the next CTA began: 102).  The smaller ones are a chain of latencies: the first tile 2 us, its bound 0.5, the list 1.5,
 // the ticket 1, the merge 4.
@@ -41,7 +42,6 @@ struct BeamArgs {
   unsigned int* tickets;        // [65536]
   float2* stats;                // [B, K, chunks]: maximum, sum of exponentials
   unsigned long long* offers;   // [B, K, chunks, n]: ordered logit << 32 | ~token; 0: none
-  long long total;              // logits in all
   int B, K, V, n, chunks, chunk_len, end_tok;
 };
 
@@ -394,7 +394,7 @@ struct Running {
 };
 
 // The n-th largest of 64 groups of threads' maxima: a bound of the n-th largest logit that they have seen.  A warp finds the places of
-// four, with eight lanes to each (all of them in every warp: 1.5 us, the warps' issue slots).  All threads; two barriers,
+// eight, with four lanes to each (all of them in every warp: 1.5 us, the warps' issue slots).  All threads; two barriers,
 // and the list of vectors, which all have read, is empty.
 __device__ __forceinline__ uint32_t bound_of(BeamShared& sh, uint32_t mine, int n) {
   const int tid = threadIdx.x;
@@ -564,7 +564,8 @@ struct BeamPlan {
 };
 
 // Chunks of a row: two to an SM, of 4096 logits at least; at most a list a thread in the merge.  (More of them cost the merge
-// and their own beginnings and ends: [16, 4, 128256] 14.0 us with four to a row, 15.2 with nine, 15.0 with two.)
+// and their own beginnings and ends: [16, 4, 128256] 14.0 us with four to a row, 15.2 with nine, 15.0 with two.  Four blocks fit an
+// SM, so rows that just miss a second chunk leave places empty: 152 rows of 128256 logits take 16.8 us, 160 take 21.9, 304 23.6.)
 bool beam_plan(int64_t B, int64_t K, int64_t V, int64_t n, BeamPlan& p) {
   if (B < 1 || K < 1 || K > kMaxBeams || V < 2 || V > QSPEC_MAX_V || n < 1 || n > kMaxN || n > K * V || B > 65535 ||
       B * K * V >= (int64_t(1) << 40))
@@ -615,7 +616,7 @@ extern "C" qspec_status qspec_beam_select(const uint16_t* logits, const float* s
   char* w = static_cast<char*>(ws);
   BeamArgs a{logits, scores, done, weights, parent, tok, score, linear_error_word(), reinterpret_cast<unsigned int*>(w),
              reinterpret_cast<float2*>(w + p.stats), reinterpret_cast<unsigned long long*>(w + p.offers),
-             static_cast<long long>(B) * beams * V, B, beams, V, n, p.chunks, p.chunk_len, end_tok};
+             B, beams, V, n, p.chunks, p.chunk_len, end_tok};
   if (!a.err) return QSPEC_ERR_CUDA;
   static_assert(sizeof(BeamShared) <= 48 * 1024, "no opt-in needed");
   return launch_pdl(beam_kernel, dim3(static_cast<unsigned int>(blocks)), dim3(kThreads), sizeof(BeamShared),

@@ -50,7 +50,7 @@ qspec_status launch(AttArgs& a, int64_t rows, cudaStream_t s) {
   // sequences of 4096, 64 rows: 71 against 77 us; one of 32768: 51 against 94); with 96 rows and more it reads them three
   // times and computes on the legacy tensor path (128 rows: 119 against 78 us).
   // With shared prefixes the prefill kernel takes key tiles in turn with its two query tiles, and wins from 33 rows on (16 groups
-  // over 6001 + 300 positions, 32 rows: 109 us here, 104 there; 64 rows: 182 against 140; one group over 32768, 32 rows: 46 against 49).
+  // over 6001 + 300 positions, 32 rows: 103 us in either; 64 rows: 182 here, 141 there; one group over 32768, 32 rows: 45 here, 49 there).
   if (rows > (kShared ? 32 : 64)) {
     if (a.c.page >= 64) return d128 ? launch_prefill<128, true, kShared>(a, rows, s) : launch_prefill<64, true, kShared>(a, rows, s);
     return d128 ? launch_prefill<128, false, kShared>(a, rows, s) : launch_prefill<64, false, kShared>(a, rows, s);

@@ -111,7 +111,6 @@ __device__ __forceinline__ SideAt side_at(int i, int T) {
   const bool last = i == 2 * T - 1, keys = i == 0 || ((i & 1) && !last);
   return SideAt{last ? T - 1 : keys ? (i + 1) / 2 : i / 2 - 1, keys ? 0 : 1};
 }
-__device__ __forceinline__ int side_of_keys(int tile) { return tile == 0 ? 0 : 2 * tile - 1; }
 __device__ __forceinline__ int side_of_values(int tile, int T) { return tile == T - 1 ? 2 * T - 1 : 2 * tile + 2; }
 
 // kBigPages: pages of 64 slots or more, so 64 keys lie in one page and share its scales.
@@ -121,8 +120,8 @@ __device__ __forceinline__ int side_of_values(int tile, int T) { return tile == 
 // softmax of one runs under the products of the other (the two sums meet in shared memory at the end).  The converted sides come in
 // the order K0 K1 V0 K2 V1 ...: with the values of a tile right behind its keys they held one of the three places for as long as its
 // softmax took, and the next keys' conversion stood open (16 groups of 32 single tokens over 6001 + 300 positions: 337 us).
-// 64 samples over 32768 + 512 positions, 64 heads on 8: 112 us; 128 sequences of four tokens under three prompts of 16384 with up to 2000
-// of their own, 32 heads on 8: 197 (as single sequences 575 and 397).  A prefix tile of 256 rows takes 4100 cycles, 64% of the
+// 64 samples over 32768 + 512 positions, 64 heads on 8: 113 us; 128 sequences of four tokens under three prompts of 16384 with up to 2000
+// of their own, 32 heads on 8: 198 (as single sequences 575 and 397).  A prefix tile of 256 rows takes 4100 cycles, 64% of the
 // measured bf16 rate (two softmax steps of 64 keys, 2000 cycles a query tile, with the waits around them); a tile of a
 // sequence's own keys, or of an item of up to 128 rows, takes as long as the converters need for its two sides, 2400.
 template <int D, bool kBigPages, bool kShared = false>
