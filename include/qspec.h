@@ -666,7 +666,8 @@ qspec_status qspec_kv_pages(const int32_t* pages, const int32_t* room, int32_t r
 /*
  * qspec_kv_copy_pages -- page src[i] -> page dst[i] in each of n_caches caches (the layers of a model, which share page tables):
  * the scales, and the codes of the first len[i] slots of every head (len NULL: of all).
- *   caches HOST array of n_caches descriptors of one shape, 1 <= n_caches <= QSPEC_KV_MAX_LAYERS (read during the call)
+ *   caches HOST array of n_caches descriptors of one shape, 1 <= n_caches <= QSPEC_KV_MAX_LAYERS (read during the call; deeper
+ *          models take a call for each 64 of their layers)
  *   src, dst, len [n] int32 DEVICE, 4-byte aligned (n may be 0, all three NULL then); pairs with src[i] < 0 are skipped.  No
  *   dst[i] may be any other pair's src or dst
  * A pair with an id outside [0, n_pages) or a len[i] outside [0, page] copies nothing and makes the next qspec_check_status return
